@@ -445,6 +445,142 @@ pmx_status pmx_sketch_gaussian(pmx_handle handle, uint64_t seed, int matrix, int
                                int n, int p, float* S, int lds, uint32_t* words, void* stream);
 
 /*
+ * Operators of the training step around the preconditioned update: products
+ * grouped by expert, the token embedding, the distillation loss, each with its
+ * gradient.  They take part in a step that the functions above finish: their
+ * gradients are the G of pmx_shampoo_stats_update, pmx_matfn_polar and the
+ * Shampoo plan.  All of them enqueue on `stream`, read no device data on the
+ * host and can be captured into a HIP graph; every result has a fixed order of
+ * summation (the same bits on every call).  Index arrays (offsets, ids,
+ * labels) are device arrays of int32 or int64 (pmx_itype).
+ */
+typedef int32_t pmx_itype;
+enum { PMX_I32 = 0, PMX_I64 = 1 };
+#define PMX_MAX_GROUPS 1000
+#define PMX_MAX_TOP 1024
+#define PMX_MAX_VOCAB 4194303       /* 2^22 - 1 */
+#define PMX_MAX_TOKENS 1073741824   /* 2^30, of an embedding gradient */
+
+/*
+ * Products grouped by expert.  The rows of A are sorted by group: group e has
+ * rows offsets[e] .. offsets[e + 1] - 1 (`groups` + 1 offsets).
+ *   trans_b = 1: C[t][j] = sum_k A[t][k] B_e[j][k]  (B_e n x k: weights stored
+ *                out x in; the forward pass)
+ *   trans_b = 0: C[t][j] = sum_k A[t][k] B_e[k][j]  (B_e k x n; the input
+ *                gradient of the same weights)
+ * A is rows x k, C rows x n, B_e = B + e stride_b (stride_b = 0: one matrix
+ * shared by all groups).  Rows in no group (before offsets[0], from
+ * offsets[groups] on) are set to zero.  Offsets are clamped to [0, rows] and
+ * made non-decreasing, so none leads outside the matrices.  A and B have
+ * `dtype`; C has out_dtype: PMX_F32, or PMX_BF16 for bf16 operands (fp32
+ * operands with a bf16 C: PMX_ERR_NOT_SUPPORTED).  Accumulation is fp32 with
+ * one rounding.  No alignment beyond the element's is asked for.  rows may be
+ * 0 (nothing is enqueued); 1 <= k, n <= 2^20, 1 <= groups <= PMX_MAX_GROUPS.
+ * The workspace may be NULL when the query says 0.
+ */
+pmx_status pmx_grouped_product_workspace_size(int64_t rows, int k, int n, int groups,
+                                              pmx_dtype dtype, size_t* bytes);
+pmx_status pmx_grouped_product(pmx_handle handle, const void* A, pmx_dtype dtype, int64_t rows,
+                               int k, int64_t lda, const void* B, int n, int64_t ldb,
+                               int64_t stride_b, int trans_b, const void* offsets,
+                               pmx_itype itype, int groups, void* C, pmx_dtype out_dtype,
+                               int64_t ldc, void* workspace, size_t workspace_bytes,
+                               void* stream);
+/*
+ * C_e = A_e^T B_e, or C_e += A_e^T B_e with accumulate = 1 (the weight
+ * gradient: A = dY, B = X gives out x in).  A is rows x m, B rows x n, C_e
+ * m x n at C + e stride_c.  A group without rows gives zeros (accumulate: C_e
+ * stays).  rows may be 0.  Types, offsets and errors as above.
+ */
+pmx_status pmx_grouped_outer_workspace_size(int64_t rows, int m, int n, int groups,
+                                            pmx_dtype dtype, size_t* bytes);
+pmx_status pmx_grouped_outer(pmx_handle handle, const void* A, pmx_dtype dtype, int64_t rows, int m,
+                             int64_t lda, const void* B, int n, int64_t ldb, const void* offsets,
+                             pmx_itype itype, int groups, void* C, pmx_dtype out_dtype,
+                             int64_t ldc, int64_t stride_c, int accumulate, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Token embedding: Y[t] = scale W[ids[t]] for the vocab x dim table W; an id
+ * outside [0, vocab) gives a row of zeros.  Y has the table's type.
+ */
+pmx_status pmx_embedding(pmx_handle handle, const void* table, pmx_dtype dtype, int vocab, int dim,
+                         int64_t ldt, const void* ids, pmx_itype itype, int64_t tokens,
+                         float scale, void* Y, int64_t ldy, void* stream);
+/*
+ * Its gradient: dW[v] = scale sum_{t: ids[t] = v} dY[t], every row of dW
+ * written (zeros where no token is); accumulate = 1 adds to dW instead and
+ * leaves the other rows alone.  Tokens whose id is padding_idx or outside
+ * [0, vocab) are left out (padding_idx = -1: none).  dY and dW may have
+ * different types; sums are fp32, in an order fixed by the tokens' order.
+ * tokens may be 0, at most PMX_MAX_TOKENS.
+ */
+pmx_status pmx_embedding_grad_workspace_size(int64_t tokens, int vocab, int dim, size_t* bytes);
+pmx_status pmx_embedding_grad(pmx_handle handle, const void* dY, pmx_dtype dtype, int64_t tokens,
+                              int dim, int64_t lddy, const void* ids, pmx_itype itype, int vocab,
+                              float scale, int64_t padding_idx, void* dW, pmx_dtype out_dtype,
+                              int64_t lddw, int accumulate, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top logits.  Row t of the student's logits Z
+ * (rows x vocab) has a list of `top` vocabulary ids and the teacher's logits
+ * there.  Over the listed entries with an id in [0, vocab):
+ *   p = softmax(teacher / tau), q = softmax(z / tau), s = softmax(z),
+ *   L_t = mix tau^2 sum_i p_i (log p_i - log q_{id_i}) - (1 - mix) log s_{label_t}
+ *   total = sum_t w_t L_t
+ *   dZ[t][j] = u w_t (mix tau (q_j - sum_{i: id_i = j} p_i)
+ *                     + (1 - mix) (s_j - [j = label_t]))
+ * with w = weights, or 1 / rows each when NULL, and u the upstream gradient.
+ * The teacher's log-probabilities do as well as its logits (p is the same).
+ *   - w_t = 0: the row is ignored, whatever it holds: L_t = 0, zero gradient.
+ *   - a label outside [0, vocab): the row has no label term.
+ *   - teacher ids outside [0, vocab), or logits of -inf: no weight; a row with
+ *     none left has no distillation term.  An id listed twice counts twice.
+ *   - logits z of -inf: masked, zero gradient (L_t = inf where the teacher
+ *     gives them weight); a row of nothing but -inf: L_t = 0, zero gradient.
+ *   - NaN, or +inf, in a row that counts: NaN.
+ * labels may be NULL when mix = 1; top may be 0 when mix = 0 (plain cross
+ * entropy).  tau > 0, 0 <= mix <= 1, top <= PMX_MAX_TOP, vocab <= PMX_MAX_VOCAB.
+ */
+typedef struct {
+  int32_t struct_version;  /* 1 */
+  pmx_dtype dtype;         /* of z and dZ */
+  int64_t rows;
+  int32_t vocab, top;
+  const void* z;
+  int64_t ldz;
+  const void* teacher_ids; /* rows x top */
+  int64_t ld_ids;
+  const void* teacher;     /* rows x top */
+  int64_t ld_teacher;
+  const void* labels;      /* rows */
+  const float* weights;    /* rows, fp32 */
+  pmx_itype ids_type, labels_type;
+  pmx_dtype teacher_dtype;
+  float tau, mix;
+  int32_t reserved;        /* 0 */
+} pmx_distill_problem;
+
+pmx_status pmx_distill_workspace_size(const pmx_distill_problem* problem, size_t* bytes);
+/*
+ * The loss: rows_loss[t] = L_t, *total, and in stats (rows x 3 floats, or NULL)
+ * what pmx_distill_grad needs.  With dZ the gradient for u = 1 is written in
+ * the same pass (the logits are read once); dZ may be z itself (same address
+ * and row distance).
+ */
+pmx_status pmx_distill_loss(pmx_handle handle, const pmx_distill_problem* problem,
+                            float* rows_loss, float* total, float* stats, void* dZ, int64_t lddz,
+                            void* workspace, size_t workspace_bytes, void* stream);
+/*
+ * The gradient later, from the stats of a loss of the same problem; upstream
+ * is a device float (NULL: 1).  dZ may be z itself.
+ */
+pmx_status pmx_distill_grad(pmx_handle handle, const pmx_distill_problem* problem,
+                            const float* stats, const float* upstream, void* dZ, int64_t lddz,
+                            void* stream);
+
+/*
  * Launch trace for benchmarking.  While enabled, every kernel that a call on
  * this handle enqueues is bracketed by a pair of HIP events recorded on the
  * call's stream (host-side event objects owned by the handle; no device

@@ -79,7 +79,7 @@ def build(verbose=True):
 # compiled as usual) and linked with the other objects into libpmx_san.so.
 # Load it with the clang ASan runtime preloaded (asan_runtime()).
 SAN_LIB = os.path.join(HERE, "libpmx_san.so")
-SAN_SOURCES = ("pmx_api.hip", "pmx_shampoo.hip")
+SAN_SOURCES = ("pmx_api.hip", "pmx_shampoo.hip", "pmx_train_api.hip")
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=all"]
 

@@ -1,0 +1,503 @@
+// Token embedding: Y[t] = scale W[id_t], and the gradient of the table,
+//   dW[v] (+)= scale sum_{t : id_t = v, v != padding_idx} dY[t].
+//
+// The gradient sorts the tokens by id (stable, least significant digit first,
+// one or two passes) and sums runs of equal ids over fixed chunks of the sorted
+// order, so every row of dW is written once and every sum has a fixed order:
+// no floating atomics, the same bits on every call.  Sums are fp32.
+//
+// Bound: HBM, tokens x dim read and vocab x dim written; the sort moves 8
+// bytes a token and pass and is all latency.
+#include "pmx_train.h"
+
+namespace pmx {
+namespace {
+
+constexpr int kSortThreads = 256, kSortItems = 8, kSortTile = kSortThreads * kSortItems;
+constexpr int kSortMaxBlocks = 256;  // a block sorts several tiles beyond 2^19 tokens
+constexpr int kMaxDigits = 2048;     // 11 bits a pass
+constexpr int kZeroRows = 16;        // rows of dW per clearing block
+
+struct SortPlan {
+  int bits;     // key bits: keys 0 .. vocab (vocab: tokens without a row)
+  int passes;   // 1 or 2
+  int dbits;    // bits a pass
+  int span;     // tokens a block
+  int blocks;
+  int chunk;    // sorted positions summed by one block
+  int chunks;
+};
+
+SortPlan sort_plan(int64_t tokens, int vocab) {
+  SortPlan s;
+  s.bits = 1;
+  while ((int64_t)vocab >> s.bits) ++s.bits;
+  s.passes = s.bits <= 11 ? 1 : 2;
+  s.dbits = (s.bits + s.passes - 1) / s.passes;
+  const int64_t tiles = (tokens + kSortTile - 1) / kSortTile;
+  const int64_t per = (tiles + kSortMaxBlocks - 1) / kSortMaxBlocks;
+  s.span = (int)(per * kSortTile);
+  s.blocks = s.span ? (int)((tokens + s.span - 1) / s.span) : 0;
+  // chunks of 32 tokens, longer ones once there are 4096
+  const int64_t c = (tokens + 4095) / 4096;
+  s.chunk = (int)(c < 32 ? 32 : (c + 7) / 8 * 8);
+  s.chunks = (int)((tokens + s.chunk - 1) / s.chunk);
+  return s;
+}
+
+struct EmbedWs {
+  int* cnt;       // [passes][blocks][digits]
+  uint2* a;       // key, position
+  uint2* b;
+  float* part;    // [chunks][2][dim]
+  size_t bytes;
+};
+
+EmbedWs embed_ws(void* base, const SortPlan& s, int64_t tokens, int dim) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  EmbedWs w;
+  char* p = reinterpret_cast<char*>(base);
+  size_t o = 0;
+  w.cnt = reinterpret_cast<int*>(p + o);
+  o += up((size_t)s.passes * s.blocks * ((size_t)1 << s.dbits) * sizeof(int));
+  w.a = reinterpret_cast<uint2*>(p + o);
+  o += up((size_t)tokens * sizeof(uint2));
+  w.b = reinterpret_cast<uint2*>(p + o);
+  o += up((size_t)tokens * sizeof(uint2));
+  w.part = reinterpret_cast<float*>(p + o);
+  o += up((size_t)s.chunks * 2 * (size_t)dim * sizeof(float));
+  w.bytes = o;
+  return w;
+}
+
+// ---------------------------------------------------------------- lookup
+// VB bytes a thread and step: the largest power of two up to 16 that divides
+// the row length, both row strides and both addresses.  threadIdx.x walks a
+// row, threadIdx.y the rows.
+template <int VB>
+struct Raw;
+template <> struct Raw<16> { typedef u32x4_t type; };
+template <> struct Raw<8> { typedef u32x2_t type; };
+template <> struct Raw<4> { typedef uint32_t type; };
+template <> struct Raw<2> { typedef uint16_t type; };
+
+template <typename T, int VB>
+__global__ __launch_bounds__(256) void embed_lookup_kernel(EmbedParams p) {
+  typedef typename Raw<VB>::type R;
+  constexpr int NE = VB / (int)sizeof(T);
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= p.tokens) return;
+  const int64_t id = load_index(p.ids, t, p.ids64);
+  const bool row = id >= 0 && id < p.vocab;  // an id outside the table reads nothing: zeros
+  const T* src = reinterpret_cast<const T*>(p.table) + (row ? id : 0) * p.ld_table;
+  T* dst = reinterpret_cast<T*>(p.out) + t * p.ld_out;
+  const int n = p.dim / NE;
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    R r = {};
+    if (row) {
+      r = reinterpret_cast<const R*>(src)[c];
+      if (p.scale != 1.f) {
+        T x[NE];
+        __builtin_memcpy(x, &r, VB);
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int j = 0; j < NE; ++j) x[j] *= p.scale;
+        } else {
+#pragma unroll
+          for (int j = 0; j < NE; ++j)
+            x[j] = (T)pack_bf16(__uint_as_float((uint32_t)x[j] << 16) * p.scale, 0.f);
+        }
+        __builtin_memcpy(&r, x, VB);
+      }
+    }
+    reinterpret_cast<R*>(dst)[c] = r;
+  }
+}
+
+// ---------------------------------------------------------------- sort
+__device__ __forceinline__ uint32_t key_of(const EmbedParams& p, int64_t t) {
+  const int64_t id = load_index(p.ids, t, p.ids64);
+  return id < 0 || id >= p.vocab || id == p.padding_idx ? (uint32_t)p.vocab : (uint32_t)id;
+}
+
+// Digit counts of pass 1 per block; the counts of pass 2 are cleared here and
+// filled while pass 1 scatters.
+__global__ __launch_bounds__(kSortThreads) void embed_hist_kernel(EmbedParams p, SortPlan s, int* cnt) {
+  __shared__ int h[kMaxDigits];
+  const int nd = 1 << s.dbits;
+  for (int d = threadIdx.x; d < nd; d += kSortThreads) h[d] = 0;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * s.span;
+  const int64_t t1 = t0 + s.span < p.tokens ? t0 + s.span : p.tokens;
+  for (int64_t t = t0 + threadIdx.x; t < t1; t += kSortThreads)
+    atomicAdd(&h[key_of(p, t) & (nd - 1)], 1);
+  __syncthreads();
+  int* c1 = cnt + (int64_t)blockIdx.x * nd;
+  int* c2 = cnt + ((int64_t)s.blocks + blockIdx.x) * nd;
+  for (int d = threadIdx.x; d < nd; d += kSortThreads) {
+    c1[d] = h[d];
+    if (s.passes > 1) c2[d] = 0;
+  }
+}
+
+// One stable scatter pass.  A wave ranks 64 consecutive tokens at a time by
+// matching digits with ballots; waves and tiles follow each other in order.
+template <bool FIRST>
+__global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(EmbedParams p, SortPlan s, int* cnt,
+                                                                     const uint2* in, uint2* out) {
+  constexpr int W = kSortThreads / 64;
+  __shared__ int wcnt[W][kMaxDigits];
+  __shared__ int base[kMaxDigits];
+  __shared__ int part[kSortThreads];
+  const int nd = 1 << s.dbits, shift = FIRST ? 0 : s.dbits;
+  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+  // where each digit's tokens of this block begin: the digit's place in the
+  // whole order plus what earlier blocks hold of it
+  const int* c = cnt + (FIRST ? 0 : (int64_t)s.blocks * nd);
+  const int each = nd > kSortThreads ? nd / kSortThreads : 1;  // digits a thread
+  int total = 0;
+  for (int i = 0; i < each; ++i) {
+    const int d = tid * each + i;
+    if (d < nd) {
+      int all = 0, before = 0;
+      for (int b = 0; b < s.blocks; ++b) {
+        const int x = c[(int64_t)b * nd + d];
+        if (b < (int)blockIdx.x) before += x;
+        all += x;
+      }
+      base[d] = total + before;
+      total += all;
+    }
+  }
+  part[tid] = total;
+  __syncthreads();
+  for (int o = 1; o < kSortThreads; o <<= 1) {
+    const int x = tid >= o ? part[tid - o] : 0;
+    __syncthreads();
+    part[tid] += x;
+    __syncthreads();
+  }
+  const int excl = part[tid] - total;
+  for (int i = 0; i < each; ++i) {
+    const int d = tid * each + i;
+    if (d < nd) base[d] += excl;
+  }
+  const int64_t t0 = (int64_t)blockIdx.x * s.span;
+  const int64_t t1 = t0 + s.span < p.tokens ? t0 + s.span : p.tokens;
+  for (int64_t tile = t0; tile < t1; tile += kSortTile) {
+    __syncthreads();
+    for (int d = tid; d < nd; d += kSortThreads)
+#pragma unroll
+      for (int w = 0; w < W; ++w) wcnt[w][d] = 0;
+    __syncthreads();
+    uint32_t key[kSortItems], pos[kSortItems];
+    int rank[kSortItems];
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      const int64_t t = tile + wid * (64 * kSortItems) + i * 64 + lane;
+      key[i] = 0;
+      pos[i] = 0;
+      if (t < t1) {
+        if (FIRST) {
+          key[i] = key_of(p, t);
+          pos[i] = (uint32_t)t;
+        } else {
+          const uint2 v = in[t];
+          key[i] = v.x;
+          pos[i] = v.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      const int64_t t = tile + wid * (64 * kSortItems) + i * 64 + lane;
+      const bool live = t < t1;
+      const int d = (key[i] >> shift) & (nd - 1);
+      uint64_t m = __ballot(live);
+      for (int bit = 0; bit < s.dbits; ++bit) {
+        const uint64_t v = __ballot((d >> bit) & 1);
+        m &= ((d >> bit) & 1) ? v : ~v;
+      }
+      // m: the live lanes with this lane's digit
+      const int first = m ? __builtin_ctzll(m) : 0;
+      int old = 0;
+      if (live && lane == first) old = atomicAdd(&wcnt[wid][d], __popcll(m));
+      old = __shfl(old, first);
+      rank[i] = old + __popcll(m & ((1ull << lane) - 1));
+    }
+    __syncthreads();
+    for (int d = tid; d < nd; d += kSortThreads) {
+      int o = base[d];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const int x = wcnt[w][d];
+        wcnt[w][d] = o;
+        o += x;
+      }
+      base[d] = o;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      const int64_t t = tile + wid * (64 * kSortItems) + i * 64 + lane;
+      if (t < t1) {
+        const int dst = wcnt[wid][(key[i] >> shift) & (nd - 1)] + rank[i];
+        out[dst] = make_uint2(key[i], pos[i]);
+        if (FIRST && s.passes > 1)
+          atomicAdd(&cnt[((int64_t)s.blocks + dst / s.span) * nd + ((key[i] >> s.dbits) & (nd - 1))], 1);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sums
+// Four columns of a row (fewer at its end), at any element alignment.
+struct __attribute__((packed, aligned(4))) F4 { float x[4]; };
+struct __attribute__((packed, aligned(2))) H4 { uint32_t x[2]; };
+
+template <typename T>
+__device__ __forceinline__ f32x4_t load4(const T* p, int left) {
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  if (left >= 4) {
+    if constexpr (sizeof(T) == 4) {
+      const F4 r = *reinterpret_cast<const F4*>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = r.x[j];
+    } else {
+      const H4 r = *reinterpret_cast<const H4*>(p);
+      v = {bf16_lo(r.x[0]), bf16_hi(r.x[0]), bf16_lo(r.x[1]), bf16_hi(r.x[1])};
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < left) {
+        if constexpr (sizeof(T) == 4) v[j] = p[j];
+        else v[j] = __uint_as_float((uint32_t)p[j] << 16);
+      }
+  }
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, int left, f32x4_t v) {
+  if (left >= 4) {
+    if constexpr (sizeof(T) == 4) {
+      F4 r;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.x[j] = v[j];
+      *reinterpret_cast<F4*>(p) = r;
+    } else {
+      H4 r;
+      r.x[0] = pack_bf16(v[0], v[1]);
+      r.x[1] = pack_bf16(v[2], v[3]);
+      *reinterpret_cast<H4*>(p) = r;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < left) {
+        if constexpr (sizeof(T) == 4) p[j] = v[j];
+        else p[j] = (T)pack_bf16(v[j], 0.f);
+      }
+  }
+}
+
+// A finished row: four of its columns.
+template <typename O>
+__device__ __forceinline__ void put_row(const EmbedParams& p, uint32_t key, int col, f32x4_t acc) {
+  O* d = reinterpret_cast<O*>(p.out) + (int64_t)key * p.ld_out + col;
+  const int left = p.dim - col;
+  f32x4_t v = acc * p.scale;
+  if (p.accumulate) v += load4<O>(d, left);
+  store4<O>(d, left, v);
+}
+
+// Sums of runs of equal keys.  Sub-block (blockIdx, threadIdx.y) has one chunk
+// of the sorted order and 4 blockDim.x columns; a run inside the chunk is
+// finished here, a run that reaches over its ends leaves a partial sum (slot 0:
+// the run that enters the chunk, slot 1: the run that leaves it), joined by
+// embed_join_kernel.  Blocks past the chunks clear the rows without tokens.
+template <typename T, typename O>
+__global__ __launch_bounds__(256) void embed_sum_kernel(EmbedParams p, SortPlan s, const uint2* sorted,
+                                                        float* part, int sum_blocks, int slabs) {
+  const int tokens = (int)p.tokens;
+  if ((int)blockIdx.x >= sum_blocks) {
+    __shared__ int present[kZeroRows];
+    __shared__ int lim[2];
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+    const int nt = blockDim.x * blockDim.y;
+    const int64_t v0 = (int64_t)(blockIdx.x - sum_blocks) * kZeroRows;
+    const int64_t v1 = v0 + kZeroRows < p.vocab ? v0 + kZeroRows : p.vocab;
+    if (tid < kZeroRows) present[tid] = 0;
+    if (tid < 2) {  // first sorted position with key >= v0, and >= v1
+      const uint32_t want = (uint32_t)(tid ? v1 : v0);
+      int lo = 0, hi = tokens;
+      while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        if (sorted[mid].x < want) lo = mid + 1;
+        else hi = mid;
+      }
+      lim[tid] = lo;
+    }
+    __syncthreads();
+    for (int i = lim[0] + tid; i < lim[1]; i += nt) present[sorted[i].x - (uint32_t)v0] = 1;
+    __syncthreads();
+    const int quads = (p.dim + 3) / 4;
+    for (int64_t v = v0; v < v1; ++v) {
+      if (present[v - v0]) continue;
+      O* d = reinterpret_cast<O*>(p.out) + v * p.ld_out;
+      for (int q = tid; q < quads; q += nt) store4<O>(d + 4 * q, p.dim - 4 * q, f32x4_t{0.f, 0.f, 0.f, 0.f});
+    }
+    return;
+  }
+  const int cg = (int)blockIdx.x / slabs, slab = (int)blockIdx.x % slabs;
+  const int64_t chunk = (int64_t)cg * blockDim.y + threadIdx.y;
+  const int col = (slab * (int)blockDim.x + (int)threadIdx.x) * 4;
+  if (chunk >= s.chunks || col >= p.dim) return;
+  const int c0 = (int)(chunk * s.chunk);
+  const int c1 = c0 + s.chunk < tokens ? c0 + s.chunk : tokens;
+  const int left = p.dim - col;
+  const T* dy = reinterpret_cast<const T*>(p.dy) + col;
+  const uint32_t none = (uint32_t)p.vocab;
+  const uint32_t before = c0 > 0 ? sorted[c0 - 1].x : none;
+  const uint32_t after = c1 < tokens ? sorted[c1].x : none;
+  uint32_t cur = sorted[c0].x;
+  bool entered = cur == before;  // the run began in an earlier chunk
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  auto slot = [&](int k) { return part + ((int64_t)chunk * 2 + k) * p.dim + col; };
+  constexpr int U = 8;
+  for (int i0 = c0; i0 < c1; i0 += U) {
+    uint2 kp[U];
+    f32x4_t v[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) kp[j] = i0 + j < c1 ? sorted[i0 + j] : make_uint2(none, 0);
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      v[j] = kp[j].x != none ? load4<T>(dy + (int64_t)kp[j].y * p.ld_dy, left) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (i0 + j < c1) {
+        if (kp[j].x != cur) {
+          if (cur != none) {
+            if (entered) store4<float>(slot(0), left, acc);
+            else put_row<O>(p, cur, col, acc);
+          }
+          cur = kp[j].x;
+          entered = false;
+          acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        acc += v[j];
+      }
+    }
+  }
+  if (cur == none) return;
+  if (entered) store4<float>(slot(0), left, acc);
+  else if (cur == after) store4<float>(slot(1), left, acc);
+  else put_row<O>(p, cur, col, acc);
+}
+
+// Runs over chunk ends: the chunk a run begins in adds the partial sums of
+// the chunks it goes through, in their order.
+template <typename O>
+__global__ __launch_bounds__(256) void embed_join_kernel(EmbedParams p, SortPlan s, const uint2* sorted,
+                                                         const float* part, int slabs) {
+  const int tokens = (int)p.tokens;
+  const int cg = (int)blockIdx.x / slabs, slab = (int)blockIdx.x % slabs;
+  const int64_t chunk = (int64_t)cg * blockDim.y + threadIdx.y;
+  const int col = (slab * (int)blockDim.x + (int)threadIdx.x) * 4;
+  if (chunk >= s.chunks || col >= p.dim) return;
+  const int64_t c0 = chunk * s.chunk, c1 = c0 + s.chunk;
+  if (c1 >= tokens) return;  // nothing follows
+  const uint32_t key = sorted[c1 - 1].x;
+  if (key == (uint32_t)p.vocab || sorted[c1].x != key) return;
+  if (c0 > 0 && sorted[c0].x == key && sorted[c0 - 1].x == key) return;  // began earlier
+  const int left = p.dim - col;
+  f32x4_t acc = load4<float>(part + ((int64_t)chunk * 2 + 1) * p.dim + col, left);
+  // the last chunk of the run: the one whose next position has another key
+  for (int64_t c = chunk + 1; c < s.chunks; ++c) {
+    acc += load4<float>(part + (c * 2) * p.dim + col, left);
+    const int64_t e = (c + 1) * s.chunk;
+    if (e >= tokens || sorted[e - 1].x != key || sorted[e].x != key) break;
+  }
+  put_row<O>(p, key, col, acc);
+}
+
+int pow2_up(int x) {
+  int p = 1;
+  while (p < x) p <<= 1;
+  return p;
+}
+
+template <typename T>
+hipError_t lookup_t(const EmbedParams& p, int vb, hipStream_t s) {
+  const int n = (int)(p.dim * sizeof(T) / vb);
+  int tx = pow2_up(n < 256 ? n : 256);
+  if (tx < 16) tx = 16;
+  const dim3 block(tx, 256 / tx);
+  const dim3 grid((unsigned)((p.tokens + block.y - 1) / block.y));
+  switch (vb) {
+    case 16: hipLaunchKernelGGL((embed_lookup_kernel<T, 16>), grid, block, 0, s, p); break;
+    case 8: hipLaunchKernelGGL((embed_lookup_kernel<T, 8>), grid, block, 0, s, p); break;
+    case 4: hipLaunchKernelGGL((embed_lookup_kernel<T, 4>), grid, block, 0, s, p); break;
+    default:
+      if constexpr (sizeof(T) == 2) hipLaunchKernelGGL((embed_lookup_kernel<T, 2>), grid, block, 0, s, p);
+      else return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t grad_t(const EmbedParams& p, hipStream_t st) {
+  const SortPlan s = sort_plan(p.tokens, p.vocab);
+  const EmbedWs w = embed_ws(p.ws, s, p.tokens, p.dim);
+  const uint2* sorted = w.a;
+  hipError_t e;
+  if (p.tokens > 0) {
+    const dim3 g(s.blocks), b(kSortThreads);
+    hipLaunchKernelGGL(embed_hist_kernel, g, b, 0, st, p, s, w.cnt);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((embed_scatter_kernel<true>), g, b, 0, st, p, s, w.cnt, (const uint2*)nullptr, w.a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (s.passes > 1) {
+      hipLaunchKernelGGL((embed_scatter_kernel<false>), g, b, 0, st, p, s, w.cnt, (const uint2*)w.a, w.b);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      sorted = w.b;
+    }
+  }
+  const int quads = (p.dim + 3) / 4;
+  int tx = pow2_up(quads < 256 ? quads : 256);
+  if (tx < 16) tx = 16;
+  const dim3 block(tx, 256 / tx);
+  const int slabs = (quads + tx - 1) / tx;
+  const int sum_blocks = (int)((s.chunks + block.y - 1) / block.y) * slabs;
+  const int zero_blocks = p.accumulate ? 0 : (p.vocab + kZeroRows - 1) / kZeroRows;
+  if (sum_blocks + zero_blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL((embed_sum_kernel<T, O>), dim3(sum_blocks + zero_blocks), block, 0, st, p, s, sorted,
+                     w.part, sum_blocks, slabs);
+  if ((e = hipGetLastError()) != hipSuccess || s.chunks < 2) return e;
+  hipLaunchKernelGGL((embed_join_kernel<O>), dim3(sum_blocks), block, 0, st, p, s, sorted,
+                     (const float*)w.part, slabs);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t embed_grad_workspace(int64_t tokens, int vocab, int dim) {
+  return embed_ws(nullptr, sort_plan(tokens, vocab), tokens, dim).bytes;
+}
+
+hipError_t launch_embed_lookup(const EmbedParams& p, hipStream_t s) {
+  if (p.tokens == 0) return hipSuccess;
+  const int es = p.dtype == PMX_F32 ? 4 : 2;
+  const uint64_t all = (uint64_t)(uintptr_t)p.table | (uint64_t)(uintptr_t)p.out | (uint64_t)p.dim * es |
+                       (uint64_t)p.ld_table * es | (uint64_t)p.ld_out * es;
+  const int vb = !(all & 15) ? 16 : !(all & 7) ? 8 : !(all & 3) ? 4 : 2;
+  return es == 4 ? lookup_t<float>(p, vb, s) : lookup_t<uint16_t>(p, vb, s);
+}
+
+hipError_t launch_embed_grad(const EmbedParams& p, hipStream_t s) {
+  if (p.dtype == PMX_F32)
+    return p.out_dtype == PMX_F32 ? grad_t<float, float>(p, s) : grad_t<float, uint16_t>(p, s);
+  return p.out_dtype == PMX_F32 ? grad_t<uint16_t, float>(p, s) : grad_t<uint16_t, uint16_t>(p, s);
+}
+
+}  // namespace pmx

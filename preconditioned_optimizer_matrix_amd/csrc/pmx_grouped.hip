@@ -1,0 +1,626 @@
+// Matrix products grouped by expert.  The rows of A (and of the outer form's
+// B) are sorted by group; offsets[e] .. offsets[e + 1] are group e's rows and
+// stay on the device.
+//   product, trans_b: C[t][j] = sum_k A[t][k] B_e[j][k]     (NT)
+//   product:          C[t][j] = sum_k A[t][k] B_e[k][j]     (NN)
+//   outer:            C_e[i][j] = sum_t A[t][i] B[t][j]     (TN)
+// NT is the forward pass of out x in weights, NN its input gradient, TN its
+// weight gradient.
+//
+// Design (CDNA4):
+//  * Every block builds the groups' row ranges and tile counts from the
+//    offsets (one wave, scans), so a launch needs neither the host's knowledge
+//    of the sizes nor a table kernel.  Offsets are clamped to [0, rows] and
+//    made monotone, so no offset leads outside the matrices.
+//  * bf16: v_mfma_f32_32x32x16_bf16, k tiles of 64, operands through LDS, double
+//    buffered; the registers hold the loads of the tile after the next.  An
+//    operand stored k-contiguous is staged as rows; one stored along its rows
+//    or columns (NN's B, TN's A and B) is staged as it lies and read with LDS
+//    transpose reads.  fp32: v_mfma_f32_32x32x2_f32, k tiles of 16 or
+//    32.
+//  * The MFMA operands are swapped (B first), so a lane ends with four
+//    consecutive columns of one row of C: 8- and 16-byte pieces.
+//  * Rows past a group's end are read from the group's last row (their results
+//    are not stored); places past the contraction's end are zeros in both
+//    operands, so whatever lies there (infinities, NaN) does not enter.
+//  * Loads are 16 bytes at any element alignment; a piece over a row's end is
+//    read as the row's last 16 bytes and shifted.
+//  * Accumulation in fp32, one rounding at the end.  With too few tiles to fill
+//    the card the contraction is cut into splits whose fp32 partial results are
+//    joined in order by a second launch.
+#include <algorithm>
+
+#include "pmx_train.h"
+
+namespace pmx {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+
+enum Form : int { NT = 0, NN = 1, TN = 2 };
+constexpr bool a_kc(int f) { return f != TN; }  // A stored with k contiguous
+constexpr bool b_kc(int f) { return f == NT; }
+
+constexpr int kCU = 256;
+
+// ------------------------------------------------------------ group table
+struct Table {
+  int begin[PMX_MAX_GROUPS + 1];  // clamped, monotone row offsets
+  int tile[PMX_MAX_GROUPS + 1];   // first tile of each group
+};
+
+// One wave fills the table: inclusive maximum scan of the clamped offsets, then
+// the exclusive sum of ceil(rows / bm) * tiles_n (product) or `fixed` tiles a
+// group (outer).
+__device__ __forceinline__ void build_table(Table& T, const GroupedParams& p, int bm, int tiles_n,
+                                            int fixed) {
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int carry = 0;
+    for (int b = 0; b <= p.groups; b += 64) {
+      const int i = b + lane;
+      int v = 0;
+      if (i <= p.groups) {
+        int64_t o = load_index(p.offsets, i, p.off64);
+        o = o < 0 ? 0 : o > p.rows ? p.rows : o;
+        v = (int)o;
+      }
+      for (int d = 1; d < 64; d <<= 1) {
+        const int x = __shfl_up(v, d);
+        if (lane >= d && x > v) v = x;
+      }
+      if (v < carry) v = carry;
+      if (i <= p.groups) T.begin[i] = v;
+      carry = __shfl(v, 63);
+    }
+    __builtin_amdgcn_wave_barrier();
+    carry = 0;
+    for (int b = 0; b <= p.groups; b += 64) {
+      const int i = b + lane;
+      int n = 0;
+      if (i < p.groups) {
+        const int rows = *(volatile int*)&T.begin[i + 1] - *(volatile int*)&T.begin[i];
+        n = fixed ? fixed : (rows + bm - 1) / bm * tiles_n;
+      }
+      int v = n;
+      for (int d = 1; d < 64; d <<= 1) {
+        const int x = __shfl_up(v, d);
+        if (lane >= d) v += x;
+      }
+      if (i <= p.groups) T.tile[i] = carry + v - n;
+      carry += __shfl(v, 63);
+    }
+  }
+  __syncthreads();
+}
+
+// the group of tile `t`: the last e with tile[e] <= t
+__device__ __forceinline__ int group_of(const Table& T, int groups, int t) {
+  int lo = 0, hi = groups;  // tile[lo] <= t < tile[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (T.tile[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Tiles of a matrix in groups of 8 tile rows per column sweep.
+__device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int GM = 8;
+  const int per = GM * tiles_n, g = t / per, first = g * GM;
+  const int size = tiles_m - first < GM ? tiles_m - first : GM;
+  const int in = t - g * per;
+  tm = first + in % size;
+  tn = in / size;
+}
+
+// ------------------------------------------------------------ loads
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
+
+template <typename E>
+__device__ __forceinline__ u32x4_t load16(const E* p) {
+  if constexpr (sizeof(E) == 2) return *reinterpret_cast<const u32x4_a2*>(p);
+  else return *reinterpret_cast<const u32x4_a4*>(p);
+}
+
+// Elements c .. c + 15 / sizeof(E) of a row of n elements, zeros past its end.
+template <typename E>
+__device__ __forceinline__ u32x4_t load_win(const E* row, int c, int n) {
+  constexpr int VEC = 16 / (int)sizeof(E);
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (c + VEC <= n) return load16(row + c);
+  if (c >= n) return v;
+  if (n >= VEC) {  // the row's last 16 bytes, moved down
+    v = load16(row + n - VEC);
+    const int sh = (c + VEC - n) * 8 * (int)sizeof(E);  // 16 .. 112 bits
+    uint64_t lo = v[0] | ((uint64_t)v[1] << 32), hi = v[2] | ((uint64_t)v[3] << 32);
+    if (sh >= 64) {
+      lo = hi >> (sh - 64);
+      hi = 0;
+    } else {
+      lo = (lo >> sh) | (hi << (64 - sh));
+      hi >>= sh;
+    }
+    return {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
+  if constexpr (sizeof(E) == 2) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (c + j < n) v[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (c + j < n) v[j] = __float_as_uint(row[c + j]);
+  }
+  return v;
+}
+
+// ------------------------------------------------------------ tiles
+// Block tile BM x BN x BK, wave tile WM x WN; LDS layout of an operand of
+// `R` rows: k-contiguous [R][BK + 16 bytes], or [BK][pitch] as it lies.  The
+// pitch of the transpose-read form is 16 or 48 dwords modulo 64, which puts the
+// four k rows of a read on distinct banks; fp32 reads rows of consecutive
+// words (any pitch).
+template <typename E_, int BM_, int BN_, int BK_, int WM_, int WN_, int MINB_>
+struct Cfg {
+  typedef E_ E;
+  static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, MINB = MINB_;
+  static constexpr int VEC = 16 / (int)sizeof(E);
+  static constexpr int WAVES = (BM / WM) * (BN / WN), THREADS = 64 * WAVES;
+  static constexpr int FM = WM / 32, FN = WN / 32;
+  static constexpr int LDK = BK + VEC;
+  static constexpr int pitch(int r) {
+    return sizeof(E) == 2 ? (r == 32 ? 32 : r + 32) : r + 4;
+  }
+  static constexpr int size(bool kc, int r) { return kc ? r * LDK : BK * pitch(r); }
+};
+
+template <class C, bool KC, int R>
+struct Operand {
+  typedef typename C::E E;
+  static constexpr int N = R * C::BK / C::VEC / C::THREADS;  // 16-byte pieces a thread
+  static_assert(N * C::THREADS * C::VEC == R * C::BK, "pieces a thread");
+  static constexpr int PER = KC ? C::BK / C::VEC : R / C::VEC;  // pieces a stored row
+  const E* ptr[N];   // the piece at k tile 0
+  const E* base;     // the operand's origin (element k = 0, row or column 0)
+  int64_t ld;
+  int r0, limit;     // first row (column) of the tile, rows (columns) there are
+
+  // KC: rows r0 .. r0 + R - 1 of `limit` rows, read past the end from the last
+  // one.  Otherwise columns r0 .. of `limit`.
+  __device__ __forceinline__ void init(const E* b, int64_t ld_, int r0_, int limit_) {
+    base = b;
+    ld = ld_;
+    r0 = r0_;
+    limit = limit_;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = threadIdx.x + C::THREADS * i, s = idx / PER, c = idx % PER * C::VEC;
+      if (KC) {
+        const int row = r0 + s < limit ? r0 + s : limit - 1;
+        ptr[i] = base + (int64_t)row * ld + c;
+      } else {
+        ptr[i] = base + (int64_t)s * ld + r0 + c;
+      }
+    }
+  }
+  // whole k tile starting at k0; columns (not KC) all inside
+  __device__ __forceinline__ void load(u32x4_t (&v)[N], int k0) const {
+    const int64_t o = KC ? k0 : (int64_t)k0 * ld;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = load16(ptr[i] + o);
+  }
+  // any k tile: zeros at k >= kend and past the last column
+  __device__ __forceinline__ void load_edge(u32x4_t (&v)[N], int k0, int kend) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = threadIdx.x + C::THREADS * i, s = idx / PER, c = idx % PER * C::VEC;
+      if (KC) {
+        v[i] = load_win(ptr[i] - c, k0 + c, kend);
+      } else {
+        v[i] = u32x4_t{0u, 0u, 0u, 0u};
+        if (k0 + s < kend) v[i] = load_win(base + (int64_t)(k0 + s) * ld, r0 + c, limit);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(E* lds, const u32x4_t (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = threadIdx.x + C::THREADS * i, s = idx / PER, c = idx % PER * C::VEC;
+      *reinterpret_cast<u32x4_t*>(lds + s * (KC ? C::LDK : C::pitch(R)) + c) = v[i];
+    }
+  }
+};
+
+// bf16 fragment of 32 rows, 16 k: lane l has row l % 32, k = 8 (l / 32) .. + 7.
+// Not KC: two transpose reads; in each group of 16 lanes, lane j receives
+// element j % 4 of the 8 bytes addressed by lanes 4 t + j / 4 (t = 0 .. 3), so
+// the lane addresses k row 8 (g / 2) + j / 4 (+ 4) and column 16 (g % 2) + 4 (j % 4).
+template <class C, bool KC, int R>
+__device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int row, int s) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (KC) {
+    return *reinterpret_cast<const bf16x8*>(lds + (row + (lane & 31)) * C::LDK + (lane >> 5) * 8 + 16 * s);
+  } else {
+    constexpr int P = C::pitch(R);
+    const int g = lane >> 4, j = lane & 15;
+    const uint16_t* q = lds + (16 * s + 8 * (g >> 1) + (j >> 2)) * P + row + 16 * (g & 1) + 4 * (j & 3);
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)q);
+    const i16x4 hi =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)(q + 4 * P));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+}
+
+// fp32: k = k0 + 8 (l / 32) + s for step s of 16 values of k.
+template <class C, bool KC, int R>
+__device__ __forceinline__ void frag(float (&f)[8], const float* lds, int row, int k0) {
+  const int lane = threadIdx.x & 63;
+  const int r = row + (lane & 31), k = k0 + (lane >> 5) * 8;
+  if constexpr (KC) {
+    const f32x4_t* q = reinterpret_cast<const f32x4_t*>(lds + r * C::LDK + k);
+    const f32x4_t x = q[0], y = q[1];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      f[s] = x[s];
+      f[4 + s] = y[s];
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) f[s] = lds[(k + s) * C::pitch(R) + r];
+  }
+}
+
+// acc += the staged k tile.
+template <class C, int FORM>
+__device__ __forceinline__ void multiply(f32x16 (&acc)[C::FM][C::FN], const typename C::E* sa,
+                                         const typename C::E* sb, int wm, int wn) {
+  if constexpr (sizeof(typename C::E) == 2) {
+    constexpr int STEPS = C::BK / 16;
+    bf16x8 fa[2][C::FM], fb[2][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) fa[0][i] = frag<C, a_kc(FORM), C::BM>(sa, wm + 32 * i, 0);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) fb[0][j] = frag<C, b_kc(FORM), C::BN>(sb, wn + 32 * j, 0);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int c = s & 1, n = c ^ 1;
+      if (s + 1 < STEPS) {
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) fa[n][i] = frag<C, a_kc(FORM), C::BM>(sa, wm + 32 * i, s + 1);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) fb[n][j] = frag<C, b_kc(FORM), C::BN>(sb, wn + 32 * j, s + 1);
+      }
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c][j], fa[c][i], acc[i][j], 0, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int k0 = 0; k0 < C::BK; k0 += 16) {
+      float fa[C::FM][8], fb[C::FN][8];
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) frag<C, a_kc(FORM), C::BM>(fa[i], sa, wm + 32 * i, k0);
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) frag<C, b_kc(FORM), C::BN>(fb[j], sb, wn + 32 * j, k0);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j][s], fa[i][s], acc[i][j], 0, 0, 0);
+    }
+  }
+}
+
+// Product of one tile over k tiles [kb, ke) of a contraction of `K`.
+template <class C, int FORM, bool EDGE>
+__device__ __forceinline__ void mainloop(f32x16 (&acc)[C::FM][C::FN], typename C::E* smem,
+                                         const Operand<C, a_kc(FORM), C::BM>& A,
+                                         const Operand<C, b_kc(FORM), C::BN>& B, int kb, int ke, int K,
+                                         int wm, int wn) {
+  constexpr int SA = C::size(a_kc(FORM), C::BM), SB = C::size(b_kc(FORM), C::BN);
+  constexpr int ST = SA + SB;
+  u32x4_t va[Operand<C, a_kc(FORM), C::BM>::N], vb[Operand<C, b_kc(FORM), C::BN>::N];
+  const int nfull = EDGE ? 0 : K / C::BK;
+  auto load = [&](int kt) {
+    if (kt < nfull) {
+      A.load(va, kt * C::BK);
+      B.load(vb, kt * C::BK);
+    } else {
+      A.load_edge(va, kt * C::BK, K);
+      B.load_edge(vb, kt * C::BK, K);
+    }
+  };
+  load(kb);
+  A.store(smem, va);
+  B.store(smem + SA, vb);
+  if (kb + 1 < ke) load(kb + 1);
+  __syncthreads();
+  for (int kt = kb; kt < ke; ++kt) {
+    const int cur = (kt - kb) & 1;
+    typename C::E* s = smem + cur * ST;
+    typename C::E* d = smem + (cur ^ 1) * ST;
+    multiply<C, FORM>(acc, s, s + SA, wm, wn);
+    if (kt + 1 < ke) {
+      A.store(d, va);
+      B.store(d + SA, vb);
+      if (kt + 2 < ke) load(kt + 2);
+    }
+    __syncthreads();
+  }
+}
+
+// Four columns of a row of C at c (row length n): plain, or added to.
+template <typename O>
+__device__ __forceinline__ void put4(O* row, int c, int n, f32x4_t v, bool add) {
+  if (c + 4 <= n) {
+    if constexpr (sizeof(O) == 4) {
+      typedef f32x4_t f32x4_a4 __attribute__((aligned(4)));
+      f32x4_a4* q = reinterpret_cast<f32x4_a4*>(row + c);
+      if (add) v += *q;
+      *q = v;
+    } else {
+      typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
+      u32x2_a2* q = reinterpret_cast<u32x2_a2*>(row + c);
+      if (add) {
+        const u32x2_t o = *q;
+        v += f32x4_t{bf16_lo(o[0]), bf16_hi(o[0]), bf16_lo(o[1]), bf16_hi(o[1])};
+      }
+      *q = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (c + j < n) {
+        if constexpr (sizeof(O) == 4) row[c + j] = add ? row[c + j] + v[j] : v[j];
+        else
+          row[c + j] = (O)pack_bf16(add ? v[j] + __uint_as_float((uint32_t)row[c + j] << 16) : v[j], 0.f);
+      }
+  }
+}
+
+// O: element of C (float or bf16 bits); SPLIT: fp32 partial results to p.part.
+template <class C, int FORM, typename O, bool SPLIT>
+__global__ __launch_bounds__(C::THREADS, C::MINB) void grouped_kernel(GroupedParams p) {
+  typedef typename C::E E;
+  constexpr int ST = C::size(a_kc(FORM), C::BM) + C::size(b_kc(FORM), C::BN);
+  __shared__ __attribute__((aligned(16))) E smem[2 * ST];
+  __shared__ Table T;
+  const int tiles_n = (p.n + C::BN - 1) / C::BN;
+  const int tiles_m = FORM == TN ? (p.m + C::BM - 1) / C::BM : 0;
+  build_table(T, p, C::BM, tiles_n, FORM == TN ? tiles_m * tiles_n : 0);
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  constexpr int WGN = C::BN / C::WN;
+  const int wm = wid / WGN * C::WM, wn = wid % WGN * C::WN;
+  const int splits = SPLIT ? p.splits : 1;
+  const int64_t part_ld = p.n;
+
+  if constexpr (FORM != TN) {
+    // rows of no group are zeros
+    const int b0 = T.begin[0], b1 = T.begin[p.groups], outside = b0 + (int)p.rows - b1;
+    for (int i = blockIdx.x; i < outside; i += gridDim.x) {
+      const int64_t row = i < b0 ? i : b1 + (i - b0);
+      for (int c = threadIdx.x * 4; c < p.n; c += C::THREADS * 4) {
+        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (SPLIT) {
+          for (int s = 0; s < splits; ++s)
+            put4<float>(p.part + ((int64_t)s * p.rows + row) * part_ld, c, p.n, zero, false);
+        } else {
+          put4<O>(reinterpret_cast<O*>(p.c) + row * p.ldc, c, p.n, zero, false);
+        }
+      }
+    }
+  }
+
+  // Blocks are dealt to the 8 XCDs round-robin: XCD x takes a contiguous range
+  // of the items, so neighbouring tiles share its L2.
+  const int items = T.tile[p.groups] * splits;
+  const int per = (items + 7) >> 3, x = blockIdx.x & 7, step = gridDim.x >> 3;
+  for (int jx = blockIdx.x >> 3; jx < per; jx += step) {
+    const int it = x * per + jx;
+    if (it >= items) break;
+    const int t = SPLIT ? it / splits : it, sp = SPLIT ? it - t * splits : 0;
+    const int e = group_of(T, p.groups, t);
+    const int r0 = T.begin[e], nr = T.begin[e + 1] - r0;
+    int tm, tn;
+    tile_of(t - T.tile[e], FORM == TN ? tiles_m : (nr + C::BM - 1) / C::BM, tiles_n, tm, tn);
+    const int m0 = tm * C::BM, n0 = tn * C::BN;
+    const int K = FORM == TN ? nr : p.k;
+    const int M = FORM == TN ? p.m : nr;
+    const int nk = (K + C::BK - 1) / C::BK;
+    const int kb = SPLIT ? (int)((int64_t)nk * sp / splits) : 0;
+    const int ke = SPLIT ? (int)((int64_t)nk * (sp + 1) / splits) : nk;
+    f32x16 acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    if (kb < ke) {
+      const E* a = reinterpret_cast<const E*>(p.a) + (int64_t)r0 * p.lda;
+      const E* b = reinterpret_cast<const E*>(p.b) +
+                   (FORM == TN ? (int64_t)r0 * p.ldb : (int64_t)e * p.stride_b);
+      Operand<C, a_kc(FORM), C::BM> A;
+      Operand<C, b_kc(FORM), C::BN> B;
+      A.init(a, p.lda, m0, M);
+      B.init(b, p.ldb, n0, p.n);
+      // columns of an operand that is not k-contiguous past its end
+      const bool edge = (!a_kc(FORM) && m0 + C::BM > M) || (!b_kc(FORM) && n0 + C::BN > p.n);
+      if (edge) mainloop<C, FORM, true>(acc, smem, A, B, kb, ke, K, wm, wn);
+      else mainloop<C, FORM, false>(acc, smem, A, B, kb, ke, K, wm, wn);
+    }
+    // lane l has row l % 32; register v column 8 (v / 4) + 4 (l / 32) + v % 4
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+      const int row = m0 + wm + 32 * i + (lane & 31);
+      if (row >= M) continue;
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int col = n0 + wn + 32 * j + 8 * g + 4 * (lane >> 5);
+          if (col >= p.n) continue;
+          const f32x4_t v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                             acc[i][j][4 * g + 3]};
+          if constexpr (SPLIT) {
+            float* q = FORM == TN ? p.part + (((int64_t)sp * p.groups + e) * M + row) * part_ld
+                                  : p.part + ((int64_t)sp * p.rows + r0 + row) * part_ld;
+            put4<float>(q, col, p.n, v, false);
+          } else {
+            O* q = reinterpret_cast<O*>(p.c) +
+                   (FORM == TN ? (int64_t)e * p.stride_c + (int64_t)row * p.ldc
+                               : (int64_t)(r0 + row) * p.ldc);
+            put4<O>(q, col, p.n, v, FORM == TN && p.accumulate);
+          }
+        }
+    }
+  }
+}
+
+// C = (C +) the sum of the splits' partial results, in their order.  `rows`
+// rows of n in all; row r of C is at (r / m) stride_c + (r % m) ldc.
+template <typename O>
+__global__ __launch_bounds__(256) void grouped_join_kernel(GroupedParams p, int64_t rows, int m) {
+  const int quads = (p.n + 3) / 4;
+  const int64_t total = rows * quads;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / quads;
+    const int c = (int)(i - r * quads) * 4;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.splits; ++s) {
+      const float* q = p.part + ((int64_t)s * rows + r) * p.n + c;
+      if (c + 4 <= p.n) {
+        typedef f32x4_t f32x4_a4 __attribute__((aligned(4)));
+        v += *reinterpret_cast<const f32x4_a4*>(q);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (c + j < p.n) v[j] += q[j];
+      }
+    }
+    const int64_t e = r / m;
+    put4<O>(reinterpret_cast<O*>(p.c) + e * p.stride_c + (r - e * m) * p.ldc, c, p.n, v, p.accumulate);
+  }
+}
+
+// ------------------------------------------------------------ launchers
+using BLarge = Cfg<uint16_t, 256, 256, 64, 128, 64, 1>;  // 8 waves
+using BMid = Cfg<uint16_t, 128, 128, 64, 64, 64, 2>;     // 4 waves
+using BSmall = Cfg<uint16_t, 32, 128, 64, 32, 32, 2>;    // 4 waves
+using FMid = Cfg<float, 128, 128, 16, 64, 64, 2>;
+using FSmall = Cfg<float, 32, 128, 32, 32, 32, 2>;
+
+// Tile sizes by the average group: 0 small (32 x 128), 1 middle (128 x 128),
+// 2 large (256 x 256, bf16).
+struct Choice {
+  int cfg, bm, bn, bk;
+};
+Choice choose_product(int64_t rows, int n, int groups, int dtype) {
+  const int64_t avg = rows / groups;
+  if (avg <= 48) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
+  if (dtype == PMX_BF16 && avg >= 256 && n >= 256 && (rows / 256) * ((n + 255) / 256) >= kCU)
+    return {2, 256, 256, 64};
+  return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
+}
+Choice choose_outer(int64_t rows, int m, int n, int groups, int dtype) {
+  const int64_t large = (int64_t)groups * ((m + 255) / 256) * ((n + 255) / 256);
+  if (dtype == PMX_BF16 && m >= 256 && n >= 256 && large >= kCU && rows / groups >= 64) return {2, 256, 256, 64};
+  return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
+}
+
+// Splits so that the items come to two a compute unit, a split keeping at
+// least 8 k tiles.
+int splits_for(int64_t tiles, int64_t nk) {
+  if (tiles * 2 > kCU || tiles == 0) return 1;
+  const int64_t want = (2 * kCU) / tiles, most = nk / 8;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 64));
+}
+
+int64_t max_tiles_product(const Choice& c, int64_t rows, int n, int groups) {
+  return (rows / c.bm + std::min<int64_t>(groups, rows)) * ((n + c.bn - 1) / c.bn);
+}
+
+template <class C, int FORM>
+hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s) {
+  int64_t g = items < (int64_t)p.num_cu * C::MINB ? items : (int64_t)p.num_cu * C::MINB;
+  g = (g + 7) / 8 * 8;
+  if (g < 8) g = 8;
+  const dim3 grid((unsigned)g), block(C::THREADS);
+  if (p.splits > 1) {
+    hipLaunchKernelGGL((grouped_kernel<C, FORM, float, true>), grid, block, 0, s, p);
+  } else if (p.out_dtype == PMX_F32) {
+    hipLaunchKernelGGL((grouped_kernel<C, FORM, float, false>), grid, block, 0, s, p);
+  } else {
+    if constexpr (sizeof(typename C::E) == 2)
+      hipLaunchKernelGGL((grouped_kernel<C, FORM, uint16_t, false>), grid, block, 0, s, p);
+    else return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+template <class C>
+hipError_t launch_product_cfg(const GroupedParams& p, int64_t items, hipStream_t s) {
+  return p.trans_b ? launch_form<C, NT>(p, items, s) : launch_form<C, NN>(p, items, s);
+}
+
+hipError_t launch_join(const GroupedParams& p, int64_t rows, int m, hipStream_t s) {
+  const int64_t total = rows * ((p.n + 3) / 4);
+  const dim3 grid((unsigned)std::min<int64_t>((total + 255) / 256, 2048));
+  if (p.out_dtype == PMX_F32) hipLaunchKernelGGL(grouped_join_kernel<float>, grid, dim3(256), 0, s, p, rows, m);
+  else hipLaunchKernelGGL(grouped_join_kernel<uint16_t>, grid, dim3(256), 0, s, p, rows, m);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int grouped_product_splits(int64_t rows, int k, int n, int groups, int dtype) {
+  const Choice c = choose_product(rows, n, groups, dtype);
+  return splits_for(max_tiles_product(c, rows, n, groups), (k + c.bk - 1) / c.bk);
+}
+
+int grouped_outer_splits(int64_t rows, int m, int n, int groups, int dtype) {
+  const Choice c = choose_outer(rows, m, n, groups, dtype);
+  const int64_t tiles = (int64_t)groups * ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
+  return splits_for(tiles, rows / groups / c.bk);
+}
+
+hipError_t launch_grouped_product(const GroupedParams& p, hipStream_t s) {
+  if (p.rows == 0) return hipSuccess;
+  const Choice c = choose_product(p.rows, p.n, p.groups, p.dtype);
+  const int64_t items = max_tiles_product(c, p.rows, p.n, p.groups) * p.splits;
+  hipError_t e;
+  if (p.dtype == PMX_BF16) {
+    e = c.cfg == 0   ? launch_product_cfg<BSmall>(p, items, s)
+        : c.cfg == 1 ? launch_product_cfg<BMid>(p, items, s)
+                     : launch_product_cfg<BLarge>(p, items, s);
+  } else {
+    e = c.cfg == 0 ? launch_product_cfg<FSmall>(p, items, s) : launch_product_cfg<FMid>(p, items, s);
+  }
+  if (e != hipSuccess || p.splits == 1) return e;
+  return launch_join(p, p.rows, (int)p.rows, s);
+}
+
+hipError_t launch_grouped_outer(const GroupedParams& p, hipStream_t s) {
+  const Choice c = choose_outer(p.rows, p.m, p.n, p.groups, p.dtype);
+  const int64_t items =
+      (int64_t)p.groups * ((p.m + c.bm - 1) / c.bm) * ((p.n + c.bn - 1) / c.bn) * p.splits;
+  hipError_t e;
+  if (p.dtype == PMX_BF16)
+    e = c.cfg == 1 ? launch_form<BMid, TN>(p, items, s) : launch_form<BLarge, TN>(p, items, s);
+  else
+    e = launch_form<FMid, TN>(p, items, s);
+  if (e != hipSuccess || p.splits == 1) return e;
+  return launch_join(p, (int64_t)p.groups * p.m, p.m, s);
+}
+
+}  // namespace pmx

@@ -19,6 +19,8 @@ LIB_PATH = os.environ.get("PMX_LIBRARY") or os.path.join(_HERE, "libpmx.so")
 OK, ERR_INVALID_VALUE, ERR_NOT_SUPPORTED, ERR_WORKSPACE, ERR_ALIAS, ERR_HIP = range(6)
 RUNNING, CONVERGED, MAXITER, STAGNATED, NONFINITE, DIVERGED = -1, 0, 1, 2, 3, 4
 F32, BF16 = 0, 1
+I32, I64 = 0, 1
+MAX_GROUPS, MAX_TOP, MAX_VOCAB, MAX_TOKENS = 1000, 1024, (1 << 22) - 1, 1 << 30
 OP_STATS, OP_INV_ROOT, OP_POLAR, OP_APPLY, OP_POLAR_VARBATCH = range(5)
 VARBATCH_MAX_DIM = 64
 VARBATCH_MAX_SIDE = 8192
@@ -41,6 +43,10 @@ EXPORTS = [
     "pmx_shampoo_config_default", "pmx_shampoo_plan_create", "pmx_shampoo_plan_destroy",
     "pmx_shampoo_plan_sizes", "pmx_shampoo_plan_init", "pmx_shampoo_plan_step",
     "pmx_sketch_gaussian", "pmx_precond_apply_noalloc", "pmx_polar_varbatch_workspace_size",
+    "pmx_grouped_product", "pmx_grouped_product_workspace_size",
+    "pmx_grouped_outer", "pmx_grouped_outer_workspace_size",
+    "pmx_embedding", "pmx_embedding_grad", "pmx_embedding_grad_workspace_size",
+    "pmx_distill_loss", "pmx_distill_grad", "pmx_distill_workspace_size",
 ]
 
 # kernel classes of the launch trace (pmx_kernel_class)
@@ -73,6 +79,18 @@ class Layer(ctypes.Structure):
 class PolarBlock(ctypes.Structure):
     _fields_ = [("g", ctypes.c_void_p), ("u", ctypes.c_void_p), ("m", ctypes.c_int32),
                 ("n", ctypes.c_int32), ("ldg", ctypes.c_int32), ("ldu", ctypes.c_int32)]
+
+
+class DistillProblem(ctypes.Structure):
+    _fields_ = [("struct_version", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+                ("teacher_ids", ctypes.c_void_p), ("ld_ids", ctypes.c_int64),
+                ("teacher", ctypes.c_void_p), ("ld_teacher", ctypes.c_int64),
+                ("labels", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("ids_type", ctypes.c_int32), ("labels_type", ctypes.c_int32),
+                ("teacher_dtype", ctypes.c_int32), ("tau", ctypes.c_float),
+                ("mix", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 class Info(ctypes.Structure):
@@ -150,6 +168,25 @@ def _load():
                                        _i32, _vp, _vp]),
         "pmx_trace_collect": (_i32, [_vp, ctypes.POINTER(ctypes.c_double),
                                      ctypes.POINTER(ctypes.c_int64)]),
+        "pmx_grouped_product_workspace_size": (_i32, [_i64, _i32, _i32, _i32, _i32,
+                                                      ctypes.POINTER(_sz)]),
+        "pmx_grouped_product": (_i32, [_vp, _vp, _i32, _i64, _i32, _i64, _vp, _i32, _i64, _i64,
+                                       _i32, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _sz, _vp]),
+        "pmx_grouped_outer_workspace_size": (_i32, [_i64, _i32, _i32, _i32, _i32,
+                                                    ctypes.POINTER(_sz)]),
+        "pmx_grouped_outer": (_i32, [_vp, _vp, _i32, _i64, _i32, _i64, _vp, _i32, _i64, _vp, _i32,
+                                     _i32, _vp, _i32, _i64, _i64, _i32, _vp, _sz, _vp]),
+        "pmx_embedding": (_i32, [_vp, _vp, _i32, _i32, _i32, _i64, _vp, _i32, _i64, _f32, _vp,
+                                 _i64, _vp]),
+        "pmx_embedding_grad_workspace_size": (_i32, [_i64, _i32, _i32, ctypes.POINTER(_sz)]),
+        "pmx_embedding_grad": (_i32, [_vp, _vp, _i32, _i64, _i32, _i64, _vp, _i32, _i32, _f32,
+                                      _i64, _vp, _i32, _i64, _i32, _vp, _sz, _vp]),
+        "pmx_distill_workspace_size": (_i32, [ctypes.POINTER(DistillProblem),
+                                              ctypes.POINTER(_sz)]),
+        "pmx_distill_loss": (_i32, [_vp, ctypes.POINTER(DistillProblem), _vp, _vp, _vp, _vp, _i64,
+                                    _vp, _sz, _vp]),
+        "pmx_distill_grad": (_i32, [_vp, ctypes.POINTER(DistillProblem), _vp, _vp, _vp, _i64,
+                                    _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -212,6 +249,10 @@ def _stream(t):
 def _stream_of(device):
     torch = _torch()
     return _vp(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _raw_stream(device):
+    return _torch().cuda.current_stream(device).cuda_stream
 
 
 def _dtype_code(t):
@@ -536,3 +577,286 @@ def trace_collect(device=None):
     cnt = (ctypes.c_int64 * n)()
     check(lib.pmx_trace_collect(handle(device), ms, cnt), "trace_collect")
     return {KERNEL_CLASSES[i]: (ms[i], cnt[i]) for i in range(n)}
+
+
+# ---------------------------------------------------------------- training step
+# Products grouped by expert, the token embedding, the distillation loss.
+# Arguments that describe one call are checked here only as far as the tensors
+# themselves go (device, type, shape agreement, unit column stride); sizes,
+# strides, alignment and overlap are checked by the library.
+
+def _index_code(t):
+    torch = _torch()
+    if t.dtype == torch.int32:
+        return I32
+    if t.dtype == torch.int64:
+        return I64
+    raise TypeError("index tensors are int32 or int64, not %s" % t.dtype)
+
+
+def _same_device(first, *rest):
+    if not first.is_cuda:
+        raise ValueError("tensors live on the GPU")
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors on different devices")
+
+
+def _rows_of(t, what):
+    """(rows, columns, row distance) of a 2-D tensor with unit column stride."""
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D" % what)
+    r, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit column stride" % what)
+    return r, c, (t.stride(0) if r > 1 else max(c, 1))
+
+
+def _vector(t, what):
+    if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be a contiguous vector" % what)
+    return t.numel()
+
+
+def _matrices_of(t, what):
+    """(batch, rows, columns, row distance, matrix distance) of a 3-D tensor."""
+    if t.dim() != 3:
+        raise ValueError("%s must be 3-D" % what)
+    b, r, c = t.shape
+    if c > 1 and t.stride(2) != 1:
+        raise ValueError("%s must have unit column stride" % what)
+    ld = t.stride(1) if r > 1 else max(c, 1)
+    return b, r, c, ld, (t.stride(0) if b > 1 else r * ld)
+
+
+_sizes = {}
+
+
+def _need(query, *args):
+    """Workspace bytes of a call's sizes (host arithmetic only, remembered)."""
+    key = (query,) + args
+    n = _sizes.get(key)
+    if n is None:
+        sz = _sz()
+        check(getattr(lib, query)(*args, ctypes.byref(sz)), query)
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        n = _sizes[key] = sz.value
+    return n
+
+
+def _ws_for(need, ws, device):
+    if not need:
+        return None, 0
+    if ws is None or ws.numel() < need:
+        ws = workspace(need, device)
+    return ws.data_ptr(), ws.numel()
+
+
+def grouped_product(A, B, offsets, trans_b=False, out=None, out_dtype=None, ws=None):
+    """C[t] = A[t] B[e] (trans_b: A[t] B[e]^T) for the rows offsets[e] <= t <
+    offsets[e + 1] of group e; rows in no group are zeros.  A (rows x k), B
+    (groups x k x n, or groups x n x k with trans_b) bf16 or fp32, offsets
+    (groups + 1) int32 or int64 on the device; C in A's type or fp32."""
+    torch = _torch()
+    _same_device(A, B, offsets, out)
+    rows, k, lda = _rows_of(A, "A")
+    groups, br, bc, ldb, sb = _matrices_of(B, "B")
+    n = br if trans_b else bc
+    if (bc if trans_b else br) != k:
+        raise ValueError("A and B disagree about k")
+    if B.dtype != A.dtype:
+        raise TypeError("A and B have different types")
+    if _vector(offsets, "offsets") != groups + 1:
+        raise ValueError("one offset per group and one more")
+    if out is None:
+        out = torch.empty((rows, n), dtype=out_dtype or A.dtype, device=A.device)
+    elif tuple(out.shape) != (rows, n) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out has another shape or type")
+    _, _, ldc = _rows_of(out, "out")
+    dt = _dtype_code(A)
+    need = _need("pmx_grouped_product_workspace_size", rows, k, n, groups, dt)
+    wp, wn = _ws_for(need, ws, A.device)
+    check(lib.pmx_grouped_product(
+        handle(A.device.index), A.data_ptr(), dt, rows, k, lda, B.data_ptr(), n, ldb, sb,
+        1 if trans_b else 0, offsets.data_ptr(), _index_code(offsets), groups, out.data_ptr(),
+        _dtype_code(out), ldc, wp, wn, _raw_stream(A.device)), "grouped_product")
+    return out
+
+
+def grouped_outer(A, B, offsets, out=None, out_dtype=None, accumulate=False, ws=None):
+    """C[e] = A_e^T B_e over the rows of group e (accumulate: C[e] += ...):
+    with A = dY and B = X the gradient of out x in weights.  A (rows x m), B
+    (rows x n); C (groups x m x n) in A's type or fp32."""
+    torch = _torch()
+    _same_device(A, B, offsets, out)
+    rows, m, lda = _rows_of(A, "A")
+    rb, n, ldb = _rows_of(B, "B")
+    if rb != rows:
+        raise ValueError("A and B have different numbers of rows")
+    if B.dtype != A.dtype:
+        raise TypeError("A and B have different types")
+    groups = _vector(offsets, "offsets") - 1
+    if groups < 1:
+        raise ValueError("one offset per group and one more")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((groups, m, n), dtype=out_dtype or A.dtype, device=A.device)
+    elif tuple(out.shape) != (groups, m, n) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out has another shape or type")
+    _, _, _, ldc, sc = _matrices_of(out, "out")
+    dt = _dtype_code(A)
+    need = _need("pmx_grouped_outer_workspace_size", rows, m, n, groups, dt)
+    wp, wn = _ws_for(need, ws, A.device)
+    check(lib.pmx_grouped_outer(
+        handle(A.device.index), A.data_ptr(), dt, rows, m, lda, B.data_ptr(), n, ldb,
+        offsets.data_ptr(), _index_code(offsets), groups, out.data_ptr(), _dtype_code(out), ldc, sc,
+        1 if accumulate else 0, wp, wn, _raw_stream(A.device)), "grouped_outer")
+    return out
+
+
+def embedding(W, ids, scale=1.0, out=None):
+    """scale W[ids] for a table W (vocab x dim) and ids of any shape; an id
+    outside the table gives zeros."""
+    torch = _torch()
+    _same_device(W, ids, out)
+    vocab, dim, ldt = _rows_of(W, "W")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    shape = tuple(ids.shape) + (dim,)
+    if out is None:
+        out = torch.empty(shape, dtype=W.dtype, device=W.device)
+        ldy = dim
+    else:
+        if tuple(out.shape) != shape or out.dtype != W.dtype:
+            raise ValueError("out has another shape or type")
+        if out.dim() == 2:
+            ldy = _rows_of(out, "out")[2]
+        elif out.is_contiguous():
+            ldy = dim
+        else:
+            raise ValueError("out must be contiguous")
+    check(lib.pmx_embedding(handle(W.device.index), W.data_ptr(), _dtype_code(W), vocab, dim, ldt,
+                            ids.data_ptr(), _index_code(ids), ids.numel(), scale, out.data_ptr(),
+                            ldy, _raw_stream(W.device)), "embedding")
+    return out
+
+
+def embedding_grad(dY, ids, vocab, scale=1.0, padding_idx=-1, out=None, out_dtype=None,
+                   accumulate=False, ws=None):
+    """Gradient of embedding's table: dW[v] = scale sum of dY over the tokens
+    of id v, zeros elsewhere (accumulate: added to out instead).  Tokens of
+    padding_idx, or of ids outside the table, are left out.  dY is tokens x dim
+    (or ids' shape x dim, contiguous); dW in dY's type or out_dtype."""
+    torch = _torch()
+    _same_device(dY, ids, out)
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    if tuple(dY.shape[:-1]) != tuple(ids.shape):
+        raise ValueError("one row of dY per id")
+    if dY.dim() != 2:
+        if not dY.is_contiguous():
+            raise ValueError("dY must be contiguous")
+        dY = dY.view(-1, dY.shape[-1])
+    tokens, dim, lddy = _rows_of(dY, "dY")
+    vocab = int(vocab)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((vocab, dim), dtype=out_dtype or dY.dtype, device=dY.device)
+    elif tuple(out.shape) != (vocab, dim) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out has another shape or type")
+    _, _, lddw = _rows_of(out, "out")
+    need = _need("pmx_embedding_grad_workspace_size", tokens, vocab, dim)
+    wp, wn = _ws_for(need, ws, dY.device)
+    check(lib.pmx_embedding_grad(
+        handle(dY.device.index), dY.data_ptr(), _dtype_code(dY), tokens, dim, lddy, ids.data_ptr(),
+        _index_code(ids), vocab, scale, padding_idx, out.data_ptr(), _dtype_code(out), lddw,
+        1 if accumulate else 0, wp, wn, _raw_stream(dY.device)), "embedding_grad")
+    return out
+
+
+def _distill_problem(Z, teacher_ids, teacher, tau, mix, labels, weights):
+    torch = _torch()
+    _same_device(Z, teacher_ids, teacher, labels, weights)
+    rows, vocab, ldz = _rows_of(Z, "Z")
+    q = DistillProblem()
+    q.struct_version = 1
+    q.dtype = _dtype_code(Z)
+    q.rows, q.vocab, q.z, q.ldz = rows, vocab, Z.data_ptr(), ldz
+    if teacher_ids is not None:
+        ri, top, q.ld_ids = _rows_of(teacher_ids, "teacher_ids")
+        rt, tt, q.ld_teacher = _rows_of(teacher, "teacher")
+        if (ri, rt) != (rows, rows) or tt != top:
+            raise ValueError("teacher_ids and teacher are rows x top")
+        q.top, q.teacher_ids, q.teacher = top, teacher_ids.data_ptr(), teacher.data_ptr()
+        q.ids_type, q.teacher_dtype = _index_code(teacher_ids), _dtype_code(teacher)
+    if labels is not None:
+        if _vector(labels, "labels") != rows:
+            raise ValueError("one label per row")
+        q.labels, q.labels_type = labels.data_ptr(), _index_code(labels)
+    if weights is not None:
+        if _vector(weights, "weights") != rows:
+            raise ValueError("one weight per row")
+        if weights.dtype != torch.float32:
+            raise TypeError("weights are fp32")
+        q.weights = weights.data_ptr()
+    q.tau, q.mix = tau, mix
+    return q
+
+
+def _dz_of(Z, out):
+    if out is None:
+        torch = _torch()
+        out = torch.empty(Z.shape, dtype=Z.dtype, device=Z.device)
+    elif out.shape != Z.shape or out.dtype != Z.dtype or out.device != Z.device:
+        raise ValueError("out has another shape, type or device")
+    return out, _rows_of(out, "out")[2]
+
+
+def distill_loss(Z, teacher_ids, teacher, tau=1.0, mix=1.0, labels=None, weights=None, grad=False,
+                 out=None, ws=None):
+    """Distillation of the student's logits Z (rows x vocab) from a teacher's
+    top logits: teacher_ids and teacher (rows x top), mixed with the cross
+    entropy of the labels; weights (rows, fp32; zero: the row is ignored)
+    default to 1 / rows.  Returns (total, rows, stats, dZ): the weighted sum,
+    every row's loss, what distill_grad needs, and with grad (or out, which
+    may be Z itself) the gradient of total."""
+    torch = _torch()
+    q = _distill_problem(Z, teacher_ids, teacher, tau, mix, labels, weights)
+    res = torch.empty(q.rows + 1, dtype=torch.float32, device=Z.device)
+    dz, lddz, stats = None, max(q.vocab, 1), None
+    if grad or out is not None:
+        dz, lddz = _dz_of(Z, out)
+    else:
+        stats = torch.empty((q.rows, 3), dtype=torch.float32, device=Z.device)
+    sz = _sz()
+    check(lib.pmx_distill_workspace_size(ctypes.byref(q), ctypes.byref(sz)), "distill_workspace_size")
+    wp, wn = _ws_for(sz.value, ws, Z.device)
+    base = res.data_ptr()
+    check(lib.pmx_distill_loss(
+        handle(Z.device.index), ctypes.byref(q), base + 4, base,
+        stats.data_ptr() if stats is not None else None, dz.data_ptr() if dz is not None else None,
+        lddz, wp, wn, _raw_stream(Z.device)), "distill_loss")
+    return res[0], res[1:], stats, dz
+
+
+def distill_grad(Z, teacher_ids, teacher, stats, upstream=None, tau=1.0, mix=1.0, labels=None,
+                 weights=None, out=None):
+    """Gradient of distill_loss's total times `upstream` (a device fp32 scalar,
+    default 1), from the stats of a distill_loss call of the same problem.  out
+    may be Z itself."""
+    torch = _torch()
+    q = _distill_problem(Z, teacher_ids, teacher, tau, mix, labels, weights)
+    _same_device(Z, stats, upstream)
+    if tuple(stats.shape) != (q.rows, 3) or stats.dtype != torch.float32 or not stats.is_contiguous():
+        raise ValueError("stats are those distill_loss returned")
+    if upstream is not None and (upstream.numel() != 1 or upstream.dtype != torch.float32):
+        raise ValueError("upstream is one fp32 value")
+    dz, lddz = _dz_of(Z, out)
+    check(lib.pmx_distill_grad(
+        handle(Z.device.index), ctypes.byref(q), stats.data_ptr(),
+        upstream.data_ptr() if upstream is not None else None, dz.data_ptr(), lddz,
+        _raw_stream(Z.device)), "distill_grad")
+    return dz

@@ -1,0 +1,219 @@
+"""Token embedding and its gradient against a plain fp64 implementation.
+
+Tolerances: the lookup is one fp32 product and one rounding, so it is compared
+bit for bit with that.  The gradient's row sums c terms in fp32, off by at most
+(c + 3) 2^-24 sum |dY| scale; a bf16 result adds its rounding (2^-8)."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    from preconditioned_optimizer_matrix_amd import pmx
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    return torch, pmx, dev
+
+
+def _dt(torch, name):
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, 1, 1), (5, 7, 3), (33, 100, 64), (300, 1000, 130), (64, 50, 515), (1000, 33, 1024)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_lookup(env, tokens, vocab, dim, dtype):
+    torch, pmx, dev = env
+    dt = _dt(torch, dtype)
+    print("lookup", tokens, vocab, dim, dtype, flush=True)
+    for pad, off, it in ((0, 0, torch.int64), (3, 1, torch.int32)):
+        W = torch.randn(vocab, dim + pad + off, device=dev).to(dt)[:, off:off + dim]
+        ids = torch.randint(0, vocab, (tokens,), device=dev, dtype=it)
+        for scale in (1.0, 11.3):
+            ref = (W[ids.long()].float() * torch.tensor(scale, device=dev, dtype=torch.float32)).to(dt)
+            assert torch.equal(pmx.embedding(W, ids, scale=scale), ref)
+            buf = torch.full((tokens, dim + 5), 3.0, dtype=dt, device=dev)
+            pmx.embedding(W, ids, scale=scale, out=buf[:, 1:1 + dim])
+            assert torch.equal(buf[:, 1:1 + dim], ref) and (buf[:, :1] == 3).all() and (buf[:, 1 + dim:] == 3).all()
+
+
+def test_lookup_of_ids_outside(env):
+    torch, pmx, dev = env
+    W = torch.full((6, 40), float("nan"), device=dev)
+    W[:5] = torch.randn(5, 40, device=dev)
+    ids = torch.tensor([[0, -1, 4], [6, 2 ** 40, -2 ** 40]], device=dev)
+    Y = pmx.embedding(W, ids, scale=2.0)
+    assert Y.shape == (2, 3, 40)
+    assert torch.equal(Y[0, 0], 2 * W[0]) and torch.equal(Y[0, 2], 2 * W[4])
+    assert (Y[0, 1] == 0).all() and (Y[1] == 0).all()
+    assert pmx.embedding(W, torch.empty(0, dtype=torch.int64, device=dev)).shape == (0, 40)
+
+
+def _ids(kind, tokens, vocab, seed):
+    rng = np.random.default_rng(seed)
+    if kind == "even":
+        return rng.integers(0, vocab, tokens)
+    if kind == "one":  # every token the same
+        return np.full(tokens, vocab - 1)
+    if kind == "zipf":
+        return np.minimum(np.exp(rng.random(tokens) * np.log(vocab + 1)).astype(np.int64) - 1, vocab - 1)
+    out = rng.integers(-3, vocab + 3, tokens)  # "outside": some ids outside the table
+    out[:2] = (-(2 ** 40), 2 ** 40)
+    return out
+
+
+def _check_grad(torch, pmx, dev, kind, tokens, vocab, dim, dtype, out, accumulate, pad=-1, it=None, ldp=0):
+    ids = _ids(kind, tokens, vocab, tokens + dim)
+    scale = 1.7
+    g = torch.Generator().manual_seed(tokens)
+    dY = torch.randn(tokens, dim + ldp, generator=g).to(_dt(torch, dtype)).to(dev)[:, :dim]
+    W0 = torch.randn(vocab, dim + ldp, generator=g).to(_dt(torch, out)).to(dev)
+    W = W0.clone()
+    t = torch.from_numpy(ids).to(dev)
+    pmx.embedding_grad(dY, t if it is None else t.to(it), vocab, scale=scale, padding_idx=pad, out=W[:, :dim], accumulate=accumulate)
+    d = dY.double().cpu().numpy()
+    ref = W0[:, :dim].double().cpu().numpy() if accumulate else np.zeros((vocab, dim))
+    mag = np.abs(ref)
+    keep = (ids >= 0) & (ids < vocab) & (ids != pad)
+    scale = float(np.float32(scale))
+    np.add.at(ref, ids[keep], d[keep] * scale)
+    np.add.at(mag, ids[keep], np.abs(d[keep]) * scale)
+    count = np.bincount(ids[keep], minlength=vocab)[:, None]
+    bound = (count + 3) * 2.0 ** -24 * mag + (2.0 ** -8 * (1 + 1e-6) * np.abs(ref) if out == "bf16" else 2.0 ** -24 * np.abs(ref))
+    got = W[:, :dim].double().cpu().numpy()
+    assert (np.abs(got - ref) <= bound).all()
+    assert (got[count[:, 0] == 0] == (W0[:, :dim].double().cpu().numpy()[count[:, 0] == 0] if accumulate else 0)).all()
+    assert torch.equal(W[:, dim:], W0[:, dim:])
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, 1, 1), (7, 5, 3), (32, 40, 64), (33, 3, 130), (500, 2047, 20), (2049, 2048, 36),
+                                              (3000, 70000, 5), (5000, 300, 515)])
+@pytest.mark.parametrize("kind", ["even", "one", "zipf", "outside"])
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
+def test_grad(env, tokens, vocab, dim, kind, dtype, out):
+    torch, pmx, dev = env
+    if tokens < 2 and kind == "outside":
+        kind = "even"
+    print("grad", tokens, vocab, dim, kind, dtype, out, flush=True)
+    _check_grad(torch, pmx, dev, kind, tokens, vocab, dim, dtype, out, False)
+
+
+@pytest.mark.parametrize("kind", ["one", "zipf", "outside"])
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
+def test_grad_accumulated_padded_strided(env, kind, dtype, out):
+    torch, pmx, dev = env
+    for tokens, vocab, dim in ((700, 90, 33), (4100, 5000, 260)):
+        print("accumulated", kind, dtype, out, tokens, flush=True)
+        _check_grad(torch, pmx, dev, kind, tokens, vocab, dim, dtype, out, True, pad=1, it=torch.int64, ldp=3)
+        _check_grad(torch, pmx, dev, kind, tokens, vocab, dim, dtype, out, False, pad=vocab - 1, ldp=1)
+
+
+def test_grad_long(env):
+    """Several sort tiles a block and chunks of more than 32 tokens."""
+    torch, pmx, dev = env
+    _check_grad(torch, pmx, dev, "zipf", 600000, 3000, 6, "f32", "f32", False, it=torch.int32)
+    _check_grad(torch, pmx, dev, "one", 140000, 70000, 4, "bf16", "f32", False)
+
+
+def test_grad_without_tokens(env):
+    torch, pmx, dev = env
+    dY, ids = torch.empty(0, 12, device=dev), torch.empty(0, dtype=torch.int32, device=dev)
+    assert (pmx.embedding_grad(dY, ids, 50) == 0).all()
+    keep = torch.ones(50, 12, device=dev)
+    pmx.embedding_grad(dY, ids, 50, out=keep, accumulate=True)
+    assert (keep == 1).all()
+    # nothing but padding
+    dY, ids = torch.full((100, 12), float("nan"), device=dev), torch.full((100,), 4, device=dev)
+    assert (pmx.embedding_grad(dY, ids, 50, padding_idx=4) == 0).all()
+
+
+def test_grad_against_differences(env):
+    """f(W) = sum R * embedding(W) is linear: a difference quotient over a unit
+    step is exact but for fp32 rounding of Y (2 roundings a term)."""
+    torch, pmx, dev = env
+    W, V = torch.randn(60, 34, device=dev), torch.randn(60, 34, device=dev)
+    ids = torch.randint(0, 60, (200,), device=dev)
+    R = torch.randn(200, 34, device=dev)
+    f = lambda w: float((pmx.embedding(w, ids, scale=3.0).double() * R.double()).sum())
+    g = pmx.embedding_grad(R, ids, 60, scale=3.0)
+    size = float((R.abs().double() * 3.0 * (W.abs() + V.abs())[ids].double()).sum())
+    assert abs((f(W + V) - f(W - V)) / 2 - float((g.double() * V.double()).sum())) <= 220 * 2.0 ** -24 * size
+
+
+def test_same_bits_and_graph(env):
+    torch, pmx, dev = env
+    ids = torch.from_numpy(_ids("zipf", 5000, 800, 1)).to(dev)
+    dY, W = torch.randn(5000, 72, device=dev).bfloat16(), torch.randn(800, 72, device=dev)
+    out, Y = torch.empty(800, 72, device=dev), torch.empty(5000, 72, device=dev)
+    ws = pmx.workspace(pmx._need("pmx_embedding_grad_workspace_size", 5000, 800, 72), dev)
+
+    def call():
+        pmx.embedding(W, ids, scale=0.5, out=Y)
+        pmx.embedding_grad(dY, ids, 800, out=out, ws=ws)
+
+    call()
+    torch.cuda.synchronize()
+    ref = out.clone(), Y.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, ref[0]) and torch.equal(Y, ref[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        out.zero_()
+        Y.zero_()
+        ws.random_(0, 255)  # nothing in the workspace is taken over from an earlier call
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref[0]) and torch.equal(Y, ref[1])
+        x = torch.randn(300, 300, device=dev)
+        float((x @ x).sum())
+
+
+def test_refusals(env):
+    torch, pmx, dev = env
+    W = torch.randn(10, 8, device=dev)
+    ids = torch.zeros(6, dtype=torch.int64, device=dev)
+    dY = torch.randn(6, 8, device=dev)
+    for bad in (lambda: pmx.embedding(W.half(), ids), lambda: pmx.embedding(W, ids.float()),
+                lambda: pmx.embedding_grad(dY, ids.short(), 10)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: pmx.embedding(W.t(), ids), lambda: pmx.embedding(W, ids[::2]), lambda: pmx.embedding(W[0], ids),
+                lambda: pmx.embedding(W, ids, out=torch.empty(6, 9, device=dev)), lambda: pmx.embedding(W.cpu(), ids),
+                lambda: pmx.embedding_grad(dY[:5], ids, 10), lambda: pmx.embedding_grad(dY, ids, 10, accumulate=True),
+                lambda: pmx.embedding_grad(dY, ids, 10, out=torch.empty(9, 8, device=dev))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad, code in ((lambda: pmx.embedding_grad(dY, ids, 0), pmx.ERR_INVALID_VALUE),
+                      (lambda: pmx.embedding_grad(dY, ids, pmx.MAX_VOCAB + 1, out=torch.empty(pmx.MAX_VOCAB + 1, 8, device=dev)),
+                       pmx.ERR_INVALID_VALUE),
+                      (lambda: pmx.embedding(W, ids, out=W[:6]), pmx.ERR_ALIAS),
+                      (lambda: pmx.embedding_grad(dY, ids, 6, out=dY), pmx.ERR_ALIAS)):
+        with pytest.raises(pmx.PmxError) as e:
+            bad()
+        assert e.value.code == code
+    L, h, p = pmx.lib, pmx.handle(0), lambda t: t.data_ptr()
+    G = torch.full((10, 8), 5.0, device=dev)
+    need = pmx._need("pmx_embedding_grad_workspace_size", 6, 10, 8)
+    ws = pmx.workspace(need, dev)
+
+    def grad(dy=p(dY), dt=pmx.F32, tokens=6, dim=8, lddy=8, i=p(ids), it=pmx.I64, vocab=10, w=p(G), odt=pmx.F32, lddw=8, acc=0,
+             wsp=p(ws), wsn=need):
+        return L.pmx_embedding_grad(h, dy, dt, tokens, dim, lddy, i, it, vocab, 1.0, -1, w, odt, lddw, acc, wsp, wsn, None)
+
+    inv = pmx.ERR_INVALID_VALUE
+    assert grad(dy=None) == inv and grad(i=None) == inv and grad(w=None) == inv and grad(tokens=-1) == inv
+    assert grad(tokens=pmx.MAX_TOKENS + 1) == inv and grad(dim=0) == inv and grad(lddy=7) == inv and grad(lddw=7) == inv
+    assert grad(dt=3) == inv and grad(it=2) == inv and grad(odt=-1) == inv and grad(acc=2) == inv and grad(i=p(ids) + 4) == inv
+    assert grad(wsp=None) == pmx.ERR_WORKSPACE and grad(wsn=need - 1) == pmx.ERR_WORKSPACE
+    assert grad(wsp=p(ws) + 8) == pmx.ERR_WORKSPACE
+    torch.cuda.synchronize()
+    assert (G == 5).all()
