@@ -457,7 +457,7 @@ pmx_status pmx_sketch_gaussian(pmx_handle handle, uint64_t seed, int matrix, int
 typedef int32_t pmx_itype;
 enum { PMX_I32 = 0, PMX_I64 = 1 };
 #define PMX_MAX_GROUPS 1000
-#define PMX_MAX_TOP 1024
+#define PMX_MAX_TOP 1023
 #define PMX_MAX_VOCAB 4194303       /* 2^22 - 1 */
 #define PMX_MAX_TOKENS 1073741824   /* 2^30, of an embedding gradient */
 

@@ -12,12 +12,16 @@
 //
 // Bound: HBM.  The logits are read once and the gradient written once: the
 // row stays in registers between the two (up to 16 16-byte chunks a thread,
-// up to 1024 threads: 128 Ki bf16 or 64 Ki fp32 logits).  Longer rows are read
-// twice (the second time mostly from the last-level cache).  When there are
-// few rows, the row is cut over several blocks: one launch for the partial
-// sums, one for the gradient.
+// up to 1024 threads: 128 Ki bf16 or 64 Ki fp32 logits), packed as it was
+// loaded.  Blocks are persistent: as soon as a chunk's gradient is computed,
+// its registers take the load of the block's next row, so the loads run under
+// the exponentials and the stores.  Longer rows are read twice (the second time
+// mostly from the last-level cache).  When there are few rows, a row is cut
+// over several blocks: one launch for partial sums, one for the rest.
 // exp(z - m) is the tau-th power of exp((z - m) / tau): for tau = 2, 4 or 8 it
 // is squared up instead of a second exponential (a quarter-rate instruction).
+#include <algorithm>
+
 #include "pmx_train.h"
 
 namespace pmx {
@@ -30,11 +34,14 @@ constexpr float kNegInf = -INFINITY;
 // one and squarings
 enum Exps : int { EXP_ONE = 0, EXP_TWO = 1, EXP_SQ = 2 };
 
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
   static constexpr int VEC = 4;
+  static constexpr uint32_t NEG = 0xFF800000u;  // -inf
   static __device__ __forceinline__ float load(const float* p) { return *p; }
   static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
   static __device__ __forceinline__ float get(const u32x4_t& v, int j) {
@@ -48,6 +55,7 @@ struct Elem<float> {
 template <>
 struct Elem<uint16_t> {
   static constexpr int VEC = 8;
+  static constexpr uint32_t NEG = 0xFF80FF80u;
   static __device__ __forceinline__ float load(const uint16_t* p) {
     return __uint_as_float((uint32_t)*p << 16);
   }
@@ -63,47 +71,52 @@ struct Elem<uint16_t> {
   }
 };
 
-// Elements from the row's start down to the 16-byte boundary below it: chunk
-// c of a row holds elements [c VEC - head, (c + 1) VEC - head).
+// A row as whole 16-byte aligned chunks and the few elements before and after
+// them (fewer than VEC each): element i of those is i < head from the row's
+// start, else from the chunks' end.
 template <typename T>
-__device__ __forceinline__ int head_of(const T* row) {
-  return (int)(((uintptr_t)row & 15) / sizeof(T));
-}
-
-// Chunk with first element e0 of a row of n elements; places outside the row
-// hold -inf (no weight in a maximum or a sum).  Whole chunks are one aligned
-// 16-byte load; the row's first and last chunk are read by element.
-template <typename T>
-__device__ __forceinline__ u32x4_t load_chunk(const T* row, int e0, int n) {
-  constexpr int VEC = Elem<T>::VEC;
-  if (e0 >= 0 && e0 + VEC <= n) return *reinterpret_cast<const u32x4_t*>(row + e0);
-  float x[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j)
-    x[j] = (e0 + j >= 0 && e0 + j < n) ? Elem<T>::load(row + e0 + j) : kNegInf;
-  return Elem<T>::pack(x);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* row, int e0, int n, bool vec, const float (&x)[Elem<T>::VEC]) {
-  constexpr int VEC = Elem<T>::VEC;
-  if (vec && e0 >= 0 && e0 + VEC <= n) {
-    *reinterpret_cast<u32x4_t*>(row + e0) = Elem<T>::pack(x);
-    return;
+struct Row {
+  static constexpr int VEC = Elem<T>::VEC;
+  int head, chunks, edges;
+  __device__ __forceinline__ Row(const T* row, int n) {
+    head = (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T);
+    if (head > n) head = n;
+    chunks = (n - head) / VEC;
+    edges = n - chunks * VEC;
   }
-#pragma unroll
-  for (int j = 0; j < VEC; ++j)
-    if (e0 + j >= 0 && e0 + j < n) Elem<T>::store(row + e0 + j, x[j]);
+  __device__ __forceinline__ int edge(int i) const { return i < head ? i : chunks * VEC + i; }
+};
+
+// Chunk `i` from a base that is the same for the whole block: a scalar address
+// and a 32-bit offset.
+template <typename T>
+__device__ __forceinline__ u32x4_t load_chunk(const T* base, uint32_t i) {
+  return *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(base) + 16u * i);
+}
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* base, uint32_t i, const float (&x)[Elem<T>::VEC]) {
+  // the gradient's rows may be aligned otherwise
+  *reinterpret_cast<u32x4_a2*>(reinterpret_cast<char*>(base) + 16u * i) = Elem<T>::pack(x);
 }
 
-// Exponentials of one logit: et = exp((z - m) / tau), e1 = exp(z - m).
+// Exponentials of one logit: et = exp((z - m) / tau), e1 = exp(z - m).  The
+// difference comes first: one fused multiply-add with a rounded -m / tau would
+// be off by 2^-24 |m / tau| in the exponent, and overflow for rows masked with
+// the type's lowest value.
 template <int EX>
 struct Expo {
-  float m, ct;  // ct = log2(e) / tau (EXP_ONE: of the only temperature)
-  int sq;       // EXP_SQ: tau = 2^sq
+  float m, a, rt;
+  int sq;  // EXP_SQ: tau = 2^sq
+  __device__ __forceinline__ Expo(const DistillParams& p, float m_) {
+    m = m_;
+    // the only temperature of EXP_ONE: tau, or 1 where only the label counts
+    rt = 1.f / (EX == EXP_ONE && p.mix == 0.f ? 1.f : p.tau);
+    a = kLog2e * rt;
+    sq = p.tau == 2.f ? 1 : p.tau == 4.f ? 2 : 3;
+  }
   __device__ __forceinline__ void operator()(float z, float& et, float& e1) const {
     const float d = z - m;
-    et = __builtin_amdgcn_exp2f(d * ct);
+    et = __builtin_amdgcn_exp2f(d * a);
     if (EX == EXP_ONE) e1 = et;
     if (EX == EXP_TWO) e1 = __builtin_amdgcn_exp2f(d * kLog2e);
     if (EX == EXP_SQ) {
@@ -137,9 +150,9 @@ __device__ __forceinline__ void block_max(float (&v)[N], float (*red)[16]) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float m = red[i][0];
+    float m = red[i][lane & (W - 1)];
 #pragma unroll
-    for (int w = 1; w < W; ++w) m = fmaxf(m, red[i][w]);
+    for (int o = W / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
     v[i] = m;
   }
   __syncthreads();
@@ -157,9 +170,9 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[16]) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float m = 0.f;
+    float m = red[i][lane & (W - 1)];
 #pragma unroll
-    for (int w = 0; w < W; ++w) m += red[i][w];
+    for (int o = W / 2; o; o >>= 1) m += __shfl_xor(m, o);
     v[i] = m;
   }
   __syncthreads();
@@ -167,84 +180,90 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[16]) {
 
 // The listed columns of a row: the teacher's entries and, last, the label.
 // Entries outside the vocabulary have id -1.
+constexpr int kListed = PMX_MAX_TOP + 1;
 struct Listed {
-  int id[PMX_MAX_TOP + 1];
-  float e[PMX_MAX_TOP + 1];  // teacher logit / tau, then exp(... - max)
-  float z[PMX_MAX_TOP + 1];  // the student's logit there
+  int id[kListed];
+  float e[kListed];  // teacher logit / tau, then exp(... - max)
+  float z[kListed];  // the student's logit there
 };
 
+// A thread's listed entries, on the way from memory (fetch, issued under the
+// previous row's work) to LDS (put).
 template <typename T, int NT>
-__device__ __forceinline__ void load_listed(Listed& L, const DistillParams& p, int64_t t,
-                                            const T* z, float& amax) {
-  const float rt = 1.f / p.tau;
-  amax = kNegInf;
-  const int n = p.top + 1;
-  for (int i = threadIdx.x; i < n; i += NT) {
-    int64_t id = -1;
-    float a = kNegInf;
-    if (i < p.top) {
-      id = load_index(p.ids, t * p.ld_ids + i, p.ids64);
-      if (id < 0 || id >= p.vocab) id = -1;
-      if (id >= 0) {
-        const int64_t o = t * p.ld_teacher + i;
-        a = rt * (p.teacher_dtype == PMX_F32
-                      ? reinterpret_cast<const float*>(p.teacher)[o]
-                      : Elem<uint16_t>::load(reinterpret_cast<const uint16_t*>(p.teacher) + o));
+struct Fetched {
+  static constexpr int N = (kListed + NT - 1) / NT;
+  int id[N];
+  float a[N], z[N];
+  // saved: the listed logits as distill_part_kernel kept them, not the row's
+  // (which other blocks may be overwriting with the gradient)
+  __device__ __forceinline__ void fetch(const DistillParams& p, int64_t t, const float* saved = nullptr) {
+    const T* row = reinterpret_cast<const T*>(p.z) + t * p.ldz;
+    const float rt = 1.f / p.tau;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + NT * k;
+      int64_t d = -1;
+      a[k] = kNegInf;
+      z[k] = 0.f;
+      if (i < p.top) {
+        d = load_index(p.ids, t * p.ld_ids + i, p.ids64);
+        if (d >= 0 && d < p.vocab) {
+          const int64_t o = t * p.ld_teacher + i;
+          a[k] = rt * (p.teacher_dtype == PMX_F32
+                           ? reinterpret_cast<const float*>(p.teacher)[o]
+                           : Elem<uint16_t>::load(reinterpret_cast<const uint16_t*>(p.teacher) + o));
+        }
+      } else if (i == p.top && p.labels) {
+        d = load_index(p.labels, t, p.labels64);
       }
-    } else if (p.labels) {
-      id = load_index(p.labels, t, p.labels64);
-      if (id < 0 || id >= p.vocab) id = -1;
+      if (d < 0 || d >= p.vocab) d = -1;
+      id[k] = (int)d;
+      if (d >= 0) z[k] = saved ? saved[i] : Elem<T>::load(row + d);
     }
-    L.id[i] = (int)id;
-    L.e[i] = a;
-    L.z[i] = id >= 0 ? Elem<T>::load(z + id) : 0.f;
-    amax = fmaxf(amax, a);
   }
-}
-
-// Row results: the scale of each exponential in the gradient and the loss.
-struct RowOut {
-  float m, inv_t, inv_1;  // maximum, 1 / S_tau, 1 / S_1 (0: no logit above -inf)
-  float a_inv;            // 1 / A (0: no teacher entry)
-  float loss;
+  __device__ __forceinline__ float put(Listed& L, const DistillParams& p) const {
+    float amax = kNegInf;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + NT * k;
+      if (i <= p.top) {
+        L.id[i] = id[k];
+        L.e[i] = a[k];
+        L.z[i] = z[k];
+        amax = fmaxf(amax, a[k]);
+      }
+    }
+    return amax;
+  }
 };
 
-// sums: A, sum e (a - amax), sum e (z - m) / tau, S_tau, S_1
-__device__ __forceinline__ RowOut finish_row(const DistillParams& p, const Listed& L, float m,
-                                             const float (&v)[5]) {
-  RowOut r;
-  r.m = m;
-  r.inv_t = v[3] != 0.f ? 1.f / v[3] : 0.f;
-  r.inv_1 = v[4] != 0.f ? 1.f / v[4] : 0.f;
-  r.a_inv = v[0] != 0.f ? 1.f / v[0] : 0.f;
-  r.loss = 0.f;
-  if (v[3] != 0.f) {
-    if (p.mix != 0.f && v[0] != 0.f)
-      r.loss += p.mix * p.tau * p.tau * ((v[1] - v[2]) * r.a_inv - logf(v[0]) + logf(v[3]));
-    if (p.mix != 1.f && L.id[p.top] >= 0)
-      r.loss += (1.f - p.mix) * (logf(v[4]) - (L.z[p.top] - m));
+// L.e becomes exp(a - am); sum[0] += e, sum[1] += e (a - am), sum[2] += e (z - m) / tau.
+template <int NT, int EX>
+__device__ __forceinline__ void teacher_sums(Listed& L, const DistillParams& p, const Expo<EX>& ex,
+                                             float am, float (&sum)[5]) {
+  for (int i = threadIdx.x; i < p.top; i += NT) {
+    const float a = L.e[i] - am;
+    const float e = __builtin_amdgcn_exp2f(a * kLog2e);
+    L.e[i] = e;
+    sum[0] += e;
+    if (e != 0.f) {  // nothing (not NaN) where the teacher gives no weight
+      sum[1] += e * a;
+      sum[2] += e * (L.z[i] - ex.m) * ex.rt;
+    }
   }
-  return r;
 }
 
-// Corrections of the gradient at the listed columns, over dense values already
-// written by this block.  Every entry naming the same column writes the same
-// value.
-template <typename T, int NT, int EX>
-__device__ __forceinline__ void fix_listed(const Listed& L, const DistillParams& p, T* dz,
-                                           const Expo<EX>& ex, float gt, float g1, float gp,
-                                           float gc, int lo, int hi) {
-  for (int i = threadIdx.x; i <= p.top; i += NT) {
-    const int id = L.id[i];
-    if (id < 0 || id < lo || id >= hi) continue;  // lo may lie before the row's start
-    float ps = 0.f;
-    for (int j = 0; j < p.top; ++j) ps += L.id[j] == id ? L.e[j] : 0.f;
-    float et, e1;
-    ex(L.z[i], et, e1);
-    float v = gt * et + (EX == EXP_ONE ? 0.f : g1 * e1) - gp * ps;
-    if (L.id[p.top] == id) v -= gc;
-    Elem<T>::store(dz + id, v);
+// The row's loss from its sums.
+template <int EX>
+__device__ __forceinline__ float row_loss(const DistillParams& p, const Listed& L, const Expo<EX>& ex,
+                                          const float (&v)[5]) {
+  float loss = 0.f;
+  if (v[3] != 0.f) {  // a row of nothing but -inf has none
+    if (p.mix != 0.f && v[0] != 0.f)
+      loss += p.mix * p.tau * p.tau * ((v[1] - v[2]) / v[0] - logf(v[0]) + logf(v[3]));
+    if (p.mix != 1.f && L.id[p.top] >= 0) loss += (1.f - p.mix) * (logf(v[4]) - (L.z[p.top] - ex.m));
   }
+  return loss;
 }
 
 // Gradient scales: gt and g1 multiply the exponentials (one temperature: gt
@@ -254,93 +273,148 @@ struct Scales {
 };
 template <int EX>
 __device__ __forceinline__ Scales grad_scales(const DistillParams& p, float w, float inv_t,
-                                              float inv_1, float a_inv, bool label) {
+                                              float inv_1, float sum_e, bool label) {
   const bool row = inv_t != 0.f;  // a row of nothing but -inf has no gradient
-  const float kd = row && a_inv != 0.f && p.mix != 0.f ? w * p.mix * p.tau : 0.f;
+  const float kd = row && sum_e != 0.f && p.mix != 0.f ? w * p.mix * p.tau : 0.f;
   const float ce = row && label && p.mix != 1.f ? w * (1.f - p.mix) : 0.f;
   Scales s;
   s.gt = kd * inv_t;
   s.g1 = ce * inv_1;
   if (EX == EXP_ONE) s.gt += s.g1;
-  s.gp = kd * a_inv;
+  s.gp = kd != 0.f ? kd / sum_e : 0.f;
   s.gc = ce;
   return s;
 }
+__device__ __forceinline__ float inverse(float s) { return s != 0.f ? 1.f / s : 0.f; }
 
 template <int EX>
-__device__ __forceinline__ Expo<EX> make_expo(const DistillParams& p, float m) {
-  Expo<EX> ex;
-  ex.m = m;
-  // the only temperature of EXP_ONE: tau, or 1 where only the label counts
-  ex.ct = kLog2e / (EX == EXP_ONE && p.mix == 0.f ? 1.f : p.tau);
-  ex.sq = p.tau == 2.f ? 1 : p.tau == 4.f ? 2 : 3;
-  return ex;
+__device__ __forceinline__ float grad_of(float z, const Expo<EX>& ex, const Scales& s) {
+  float et, e1;
+  ex(z, et, e1);
+  return EX == EXP_ONE ? s.gt * et : s.gt * et + s.g1 * e1;
 }
 
-// One block a row; NC > 0: the row in registers, NC chunks a thread; NC = 0:
-// the row is read twice.  GRAD: dz is written.
-template <typename T, int NT, int NC, int EX, bool GRAD>
-__global__ __launch_bounds__(NT) void distill_row_kernel(DistillParams p) {
-  constexpr int VEC = Elem<T>::VEC;
-  __shared__ Listed L;
-  __shared__ float red[5][16];
-  const int64_t t = blockIdx.x;
-  const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
-  T* dz = GRAD ? reinterpret_cast<T*>(p.dz) + t * p.lddz : nullptr;
-  const int n = p.vocab, head = head_of(z);
-  const bool vec = GRAD && head_of(dz) == head;
-  const float wt = p.weights ? p.weights[t] : 1.f / (float)p.rows;
-  if (wt == 0.f) {  // an ignored row: its logits are not read
+// Corrections of the gradient at the listed columns [lo, hi), over dense
+// values already written by this block.  Every entry naming the same column
+// writes the same value.
+template <typename T, int NT, int EX>
+__device__ __forceinline__ void fix_listed(const Listed& L, const DistillParams& p, T* dz,
+                                           const Expo<EX>& ex, const Scales& s, int lo, int hi) {
+  for (int i = threadIdx.x; i <= p.top; i += NT) {
+    const int id = L.id[i];
+    if (id < 0 || id < lo || id >= hi) continue;
+    float ps = 0.f;
+    for (int j = 0; j < p.top; ++j) ps += L.id[j] == id ? L.e[j] : 0.f;
+    float v = grad_of(L.z[i], ex, s) - s.gp * ps;
+    if (L.id[p.top] == id) v -= s.gc;
+    Elem<T>::store(dz + id, v);
+  }
+}
+
+__device__ __forceinline__ float weight_of(const DistillParams& p, int64_t t) {
+  return p.weights ? p.weights[t] : 1.f / (float)p.rows;
+}
+
+template <typename T, int NT>
+__device__ __forceinline__ void clear_row(T* row, int n) {
+  const Row<T> r(row, n);
+  const float zero[Elem<T>::VEC] = {};
+  for (int c = threadIdx.x; c < r.chunks; c += NT) store_chunk<T>(row + r.head, c, zero);
+  for (int i = threadIdx.x; i < r.edges; i += NT) Elem<T>::store(row + r.edge(i), 0.f);
+}
+
+// The next row from t on (stride `step`) that counts; ignored rows on the way
+// get their zeros.  p.rows: none.
+template <typename T, int NT, bool GRAD>
+__device__ __forceinline__ int64_t next_live(const DistillParams& p, int64_t t, int64_t step) {
+  for (; t < p.rows; t += step) {
+    if (weight_of(p, t) != 0.f) return t;
     if (threadIdx.x == 0) {
       p.rows_loss[t] = 0.f;
       if (p.stats) p.stats[3 * t] = p.stats[3 * t + 1] = p.stats[3 * t + 2] = 0.f;
     }
-    if (GRAD) {
-      const float zero[VEC] = {};
-      const int hd = head_of(dz);
-      for (int c = threadIdx.x; c * VEC - hd < n; c += NT) store_chunk<T>(dz, c * VEC - hd, n, true, zero);
+    if (GRAD) clear_row<T, NT>(reinterpret_cast<T*>(p.dz) + t * p.lddz, p.vocab);
+  }
+  return p.rows;
+}
+
+// Waves a SIMD for NC chunks a thread: registers for the row (4 NC) and 50
+// to 60 more.
+constexpr int waves_for(int nc) { return nc <= 4 ? 6 : nc <= 8 ? 5 : 4; }
+
+// Keeps a chunk packed: without it the compiler holds on to the unpacked
+// values from one phase to the next, twice the registers for bf16.
+__device__ __forceinline__ void stay_packed(u32x4_t& v) { asm volatile("" : "+v"(v)); }
+
+// Rows in registers: NC chunks a thread and one edge element.
+template <typename T, int NT, int NC, int EX, bool GRAD>
+__global__ __launch_bounds__(NT, waves_for(NC)) void distill_row_kernel(DistillParams p) {
+  constexpr int VEC = Elem<T>::VEC;
+  __shared__ Listed L;
+  __shared__ float red[5][16];
+  const int n = p.vocab, tid = threadIdx.x;
+  u32x4_t v[NC];
+  float edge;
+  Fetched<T, NT> f;
+  // every lane loads, from the row's last chunk where it has none (no branch:
+  // a value joined from two paths costs the row's registers twice); `mask`
+  // makes such chunks -inf before their first use
+  auto load_one = [&](const T* body, int last, int c) {
+    int i = tid;
+    asm volatile("" : "+v"(i));  // the offset is computed here, not kept from row to row
+    v[c] = load_chunk<T>(body, (uint32_t)min(i + c * NT, last));
+  };
+  auto mask = [&](int last, int c) {
+    const bool out = tid > last - c * NT;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[c][k] = out ? Elem<T>::NEG : v[c][k];
+  };
+  auto load_edge = [&](const T* z, const Row<T>& r) {
+    edge = tid < r.edges ? Elem<T>::load(z + r.edge(tid)) : kNegInf;
+  };
+  int64_t t = next_live<T, NT, GRAD>(p, blockIdx.x, gridDim.x);
+  if (t >= p.rows) return;
+  {
+    const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
+    const Row<T> r(z, n);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) load_one(z + r.head, r.chunks - 1, c);
+    load_edge(z, r);
+    f.fetch(p, t);
+  }
+  for (;;) {
+    const Row<T> r(reinterpret_cast<const T*>(p.z) + t * p.ldz, n);
+    float mx[2];
+    mx[0] = edge;
+    mx[1] = f.put(L, p);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      mask(r.chunks - 1, c);
+#pragma unroll
+      for (int j = 0; j < VEC; j += 2)
+        mx[0] = fmaxf(fmaxf(mx[0], Elem<T>::get(v[c], j)), Elem<T>::get(v[c], j + 1));
+      stay_packed(v[c]);
     }
-    return;
-  }
-  u32x4_t v[NC > 0 ? NC : 1];
-  float mx[2];
-  mx[0] = kNegInf;
-  if constexpr (NC > 0) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) v[c] = load_chunk<T>(z, (c * NT + (int)threadIdx.x) * VEC - head, n);
-  }
-  load_listed<T, NT>(L, p, t, z, mx[1]);
-  if constexpr (NC > 0) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) mx[0] = fmaxf(mx[0], Elem<T>::get(v[c], j));
-  } else {
-    for (int c = threadIdx.x; c * VEC - head < n; c += NT) {
-      const u32x4_t u = load_chunk<T>(z, c * VEC - head, n);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) mx[0] = fmaxf(mx[0], Elem<T>::get(u, j));
+    block_max<NT>(mx, red);
+    const float am = mx[1] == kNegInf ? 0.f : mx[1];
+    const Expo<EX> ex(p, mx[0] == kNegInf ? 0.f : mx[0]);  // -inf - 0 stays -inf
+    const int64_t tn = next_live<T, NT, GRAD>(p, t + gridDim.x, gridDim.x);
+    // without a next row every lane loads this row's first chunk again
+    const bool more = tn < p.rows;
+    const T* zn = reinterpret_cast<const T*>(p.z) + (more ? tn : t) * p.ldz;
+    const Row<T> rn(zn, n);
+    const T* body = zn + rn.head;
+    const int last = more ? rn.chunks - 1 : 0;
+    float sum[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+    teacher_sums<NT>(L, p, ex, am, sum);
+    {
+      float et, e1;
+      ex(edge, et, e1);
+      sum[3] += et;
+      if (EX != EXP_ONE) sum[4] += e1;
     }
-  }
-  block_max<NT>(mx, red);
-  const float m = mx[0] == kNegInf ? 0.f : mx[0];  // -inf - m stays -inf
-  const float am = mx[1] == kNegInf ? 0.f : mx[1];
-  const Expo<EX> ex = make_expo<EX>(p, m);
-  float sum[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
-  const float rt = 1.f / p.tau;
-  for (int i = threadIdx.x; i < p.top; i += NT) {
-    const float a = L.e[i] - am;
-    const float e = __builtin_amdgcn_exp2f(a * kLog2e);
-    L.e[i] = e;
-    sum[0] += e;
-    if (e != 0.f) {  // nothing (not NaN) where the teacher gives no weight
-      sum[1] += e * a;
-      sum[2] += e * (L.z[i] - m) * rt;
-    }
-  }
-  if constexpr (NC > 0) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < NC; ++c) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         float et, e1;
@@ -348,9 +422,83 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(DistillParams p) {
         sum[3] += et;
         if (EX != EXP_ONE) sum[4] += e1;
       }
-  } else {
-    for (int c = threadIdx.x; c * VEC - head < n; c += NT) {
-      const u32x4_t u = load_chunk<T>(z, c * VEC - head, n);
+      if (GRAD) {
+        stay_packed(v[c]);
+      } else {
+        // the sums are taken here, before the registers are loaded again
+        asm volatile("" : "+v"(sum[3]), "+v"(sum[4]) : : "memory");
+        load_one(body, last, c);
+      }
+    }
+    if (EX == EXP_ONE) sum[4] = sum[3];
+    asm volatile("" : "+v"(sum[3]), "+v"(sum[4]) : : "memory");
+    const float own_edge = edge;
+    if (!GRAD) load_edge(zn, rn);
+    if (more) f.fetch(p, tn);
+    block_sum<NT>(sum, red);
+    if (tid == 0) {
+      p.rows_loss[t] = row_loss(p, L, ex, sum);
+      if (p.stats) {
+        p.stats[3 * t] = ex.m;
+        p.stats[3 * t + 1] = inverse(sum[3]);
+        p.stats[3 * t + 2] = inverse(sum[4]);
+      }
+    }
+    if constexpr (GRAD) {
+      T* dz = reinterpret_cast<T*>(p.dz) + t * p.lddz;
+      const Scales s = grad_scales<EX>(p, weight_of(p, t), inverse(sum[3]), inverse(sum[4]), sum[0],
+                                       L.id[p.top] >= 0);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float x[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x[j] = grad_of(Elem<T>::get(v[c], j), ex, s);
+        if (tid < r.chunks - c * NT) store_chunk<T>(dz + r.head + c * NT * VEC, tid, x);
+        load_one(body, last, c);
+      }
+      if (tid < r.edges) Elem<T>::store(dz + r.edge(tid), grad_of(own_edge, ex, s));
+      load_edge(zn, rn);
+      __syncthreads();
+      fix_listed<T, NT>(L, p, dz, ex, s, 0, n);
+    }
+    if (!more) return;
+    __syncthreads();  // L is free
+    t = tn;
+  }
+}
+
+// Rows too long for the registers: read twice.
+template <typename T, int EX, bool GRAD>
+__global__ __launch_bounds__(1024) void distill_long_kernel(DistillParams p) {
+  constexpr int VEC = Elem<T>::VEC, NT = 1024;
+  __shared__ Listed L;
+  __shared__ float red[5][16];
+  const int n = p.vocab, tid = threadIdx.x;
+  for (int64_t t = blockIdx.x; (t = next_live<T, NT, GRAD>(p, t, gridDim.x)) < p.rows; t += gridDim.x) {
+    const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
+    const Row<T> r(z, n);
+    const T* body = z + r.head;
+    Fetched<T, NT> f;
+    f.fetch(p, t);
+    float mx[2];
+    mx[0] = tid < r.edges ? Elem<T>::load(z + r.edge(tid)) : kNegInf;
+    const float edge = mx[0];
+    mx[1] = f.put(L, p);
+#pragma unroll 4
+    for (int c = tid; c < r.chunks; c += NT) {
+      const u32x4_t u = load_chunk<T>(body, c);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) mx[0] = fmaxf(mx[0], Elem<T>::get(u, j));
+    }
+    block_max<NT>(mx, red);
+    const float am = mx[1] == kNegInf ? 0.f : mx[1];
+    const Expo<EX> ex(p, mx[0] == kNegInf ? 0.f : mx[0]);
+    float sum[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+    teacher_sums<NT>(L, p, ex, am, sum);
+    ex(edge, sum[3], sum[4]);
+#pragma unroll 4
+    for (int c = tid; c < r.chunks; c += NT) {
+      const u32x4_t u = load_chunk<T>(body, c);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         float et, e1;
@@ -359,43 +507,207 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(DistillParams p) {
         if (EX != EXP_ONE) sum[4] += e1;
       }
     }
-  }
-  if (EX == EXP_ONE) sum[4] = sum[3];
-  block_sum<NT>(sum, red);
-  const RowOut r = finish_row(p, L, m, sum);
-  if (threadIdx.x == 0) {
-    p.rows_loss[t] = r.loss;
-    if (p.stats) {
-      p.stats[3 * t] = r.m;
-      p.stats[3 * t + 1] = r.inv_t;
-      p.stats[3 * t + 2] = r.inv_1;
+    if (EX == EXP_ONE) sum[4] = sum[3];
+    block_sum<NT>(sum, red);
+    if (tid == 0) {
+      p.rows_loss[t] = row_loss(p, L, ex, sum);
+      if (p.stats) {
+        p.stats[3 * t] = ex.m;
+        p.stats[3 * t + 1] = inverse(sum[3]);
+        p.stats[3 * t + 2] = inverse(sum[4]);
+      }
     }
-  }
-  if constexpr (GRAD) {
-    const float w = wt * (p.upstream ? *p.upstream : 1.f);
-    const Scales s = grad_scales<EX>(p, w, r.inv_t, r.inv_1, r.a_inv, L.id[p.top] >= 0);
-    auto emit = [&](const u32x4_t& u, int e0) {
-      float x[VEC];
+    if constexpr (GRAD) {
+      T* dz = reinterpret_cast<T*>(p.dz) + t * p.lddz;
+      const Scales s = grad_scales<EX>(p, weight_of(p, t), inverse(sum[3]), inverse(sum[4]), sum[0],
+                                       L.id[p.top] >= 0);
+#pragma unroll 4
+      for (int c = tid; c < r.chunks; c += NT) {
+        const u32x4_t u = load_chunk<T>(body, c);
+        float x[VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float et, e1;
-        ex(Elem<T>::get(u, j), et, e1);
-        x[j] = s.gt * et + (EX == EXP_ONE ? 0.f : s.g1 * e1);
+        for (int j = 0; j < VEC; ++j) x[j] = grad_of(Elem<T>::get(u, j), ex, s);
+        store_chunk<T>(dz + r.head, c, x);
       }
-      store_chunk<T>(dz, e0, n, vec, x);
-    };
-    if constexpr (NC > 0) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int e0 = (c * NT + (int)threadIdx.x) * VEC - head;
-        if (e0 < n) emit(v[c], e0);
-      }
-    } else {
-      for (int c = threadIdx.x; c * VEC - head < n; c += NT)
-        emit(load_chunk<T>(z, c * VEC - head, n), c * VEC - head);
+      if (tid < r.edges) Elem<T>::store(dz + r.edge(tid), grad_of(edge, ex, s));
+      __syncthreads();
+      fix_listed<T, NT>(L, p, dz, ex, s, 0, n);
     }
     __syncthreads();
-    fix_listed<T, NT, EX>(L, p, dz, ex, s.gt, s.g1, s.gp, s.gc, 0, n);
+  }
+}
+
+// Few rows: block (x, y) has slab x of gridDim.x of row y.  A slab is a range
+// of whole chunks; the row's edges belong to slab 0.
+template <typename T>
+struct Slab {
+  int c0, c1, edges;
+  __device__ __forceinline__ Slab(const Row<T>& r) {
+    const int per = (r.chunks + (int)gridDim.x - 1) / (int)gridDim.x;
+    c0 = min((int)blockIdx.x * per, r.chunks);
+    c1 = min(c0 + per, r.chunks);
+    edges = blockIdx.x == 0 ? r.edges : 0;
+  }
+};
+
+// The listed logits kept for the second launch, behind the partial sums.
+__device__ __forceinline__ float* saved_of(const DistillParams& p, int64_t t) {
+  return p.part + p.rows * p.splits * 3 + t * (p.top + 1);
+}
+
+// Partial sums of a slab, relative to the slab's own maximum:
+// part[row][slab] = {max, S_tau, S_1}.  Slab 0 also keeps the listed logits.
+template <typename T, int EX>
+__global__ __launch_bounds__(256) void distill_part_kernel(DistillParams p) {
+  constexpr int VEC = Elem<T>::VEC, NT = 256;
+  __shared__ float red[2][16];
+  const int64_t t = blockIdx.y;
+  const int tid = threadIdx.x;
+  if (weight_of(p, t) == 0.f) return;
+  const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
+  const Row<T> r(z, p.vocab);
+  const Slab<T> b(r);
+  if (blockIdx.x == 0) {
+    Fetched<T, NT> f;
+    f.fetch(p, t);
+#pragma unroll
+    for (int k = 0; k < f.N; ++k)
+      if (tid + NT * k <= p.top) saved_of(p, t)[tid + NT * k] = f.z[k];
+  }
+  const float edge = tid < b.edges ? Elem<T>::load(z + r.edge(tid)) : kNegInf;
+  float mx[1];
+  mx[0] = edge;
+#pragma unroll 4
+  for (int c = b.c0 + tid; c < b.c1; c += NT) {
+    const u32x4_t u = load_chunk<T>(z + r.head, c);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) mx[0] = fmaxf(mx[0], Elem<T>::get(u, j));
+  }
+  block_max<NT>(mx, red);
+  const Expo<EX> ex(p, mx[0] == kNegInf ? 0.f : mx[0]);
+  float sum[2];
+  ex(edge, sum[0], sum[1]);
+#pragma unroll 4
+  for (int c = b.c0 + tid; c < b.c1; c += NT) {
+    const u32x4_t u = load_chunk<T>(z + r.head, c);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      float et, e1;
+      ex(Elem<T>::get(u, j), et, e1);
+      sum[0] += et;
+      sum[1] += e1;
+    }
+  }
+  block_sum<NT>(sum, red);
+  if (tid == 0) {
+    float* q = p.part + (t * gridDim.x + blockIdx.x) * 3;
+    q[0] = mx[0];
+    q[1] = sum[0];
+    q[2] = sum[1];
+  }
+}
+
+// The row's maximum and sums from its slabs' (in their order), or from the
+// saved statistics.
+template <int EX>
+__device__ __forceinline__ float join_parts(const DistillParams& p, int64_t t, float& st, float& s1) {
+  const float* q = p.part + t * p.splits * 3;
+  float m = kNegInf;
+  for (int i = 0; i < p.splits; ++i) m = fmaxf(m, q[3 * i]);
+  if (m == kNegInf) m = 0.f;
+  const Expo<EX> ex(p, m);
+  st = s1 = 0.f;
+  for (int i = 0; i < p.splits; ++i) {
+    // a slab of nothing but -inf has zero sums (NaN ones stay NaN)
+    const float d = (q[3 * i] == kNegInf ? 0.f : q[3 * i]) - m;
+    const float ft = __builtin_amdgcn_exp2f(d * ex.a);
+    const float f1 = EX == EXP_ONE ? ft : __builtin_amdgcn_exp2f(d * kLog2e);
+    if (q[3 * i + 1] != 0.f) st += q[3 * i + 1] * ft;
+    if (q[3 * i + 2] != 0.f) s1 += q[3 * i + 2] * f1;
+  }
+  return m;
+}
+
+// One slab of one row at a time: the gradient from the saved statistics
+// (JOIN false), or the whole rest of a row cut over blocks (JOIN; slab 0 also
+// writes the loss; without dz there is only slab 0).
+template <typename T, int EX, bool JOIN>
+__global__ __launch_bounds__(256) void distill_grad_kernel(DistillParams p) {
+  constexpr int VEC = Elem<T>::VEC, NT = 256;
+  __shared__ Listed L;
+  __shared__ float red[5][16];
+  const int n = p.vocab, tid = threadIdx.x;
+  for (int64_t t = blockIdx.y; t < p.rows; t += gridDim.y) {
+    const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
+    T* dz = reinterpret_cast<T*>(p.dz) + t * p.lddz;
+    const Row<T> r(z, n);
+    const Slab<T> b(r);
+    const float wt = weight_of(p, t);
+    const bool first = JOIN && blockIdx.x == 0 && tid == 0;
+    if (wt == 0.f) {
+      if (first) {
+        p.rows_loss[t] = 0.f;
+        if (p.stats) p.stats[3 * t] = p.stats[3 * t + 1] = p.stats[3 * t + 2] = 0.f;
+      }
+      if (p.dz) {
+        const float zero[VEC] = {};
+        for (int c = b.c0 + tid; c < b.c1; c += NT) store_chunk<T>(dz + r.head, c, zero);
+        if (tid < b.edges) Elem<T>::store(dz + r.edge(tid), 0.f);
+      }
+      continue;
+    }
+    Fetched<T, NT> f;
+    f.fetch(p, t, JOIN ? saved_of(p, t) : nullptr);
+    float m, inv_t, inv_1, sum[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+    float st = 0.f, s1 = 0.f;
+    if (JOIN) {
+      m = join_parts<EX>(p, t, st, s1);
+      inv_t = inverse(st);
+      inv_1 = inverse(s1);
+    } else {
+      m = p.stats[3 * t];
+      inv_t = p.stats[3 * t + 1];
+      inv_1 = p.stats[3 * t + 2];
+    }
+    const Expo<EX> ex(p, m);
+    float am[1];
+    am[0] = f.put(L, p);
+    block_max<NT>(am, red);
+    teacher_sums<NT>(L, p, ex, am[0] == kNegInf ? 0.f : am[0], sum);
+    block_sum<NT>(sum, red);
+    if (first) {
+      sum[3] = st;
+      sum[4] = s1;
+      p.rows_loss[t] = row_loss(p, L, ex, sum);
+      if (p.stats) {
+        p.stats[3 * t] = m;
+        p.stats[3 * t + 1] = inv_t;
+        p.stats[3 * t + 2] = inv_1;
+      }
+    }
+    if (p.dz) {
+      const float w = wt * (p.upstream ? *p.upstream : 1.f);
+      const Scales s = grad_scales<EX>(p, w, inv_t, inv_1, sum[0], L.id[p.top] >= 0);
+#pragma unroll 4
+      for (int c = b.c0 + tid; c < b.c1; c += NT) {
+        const u32x4_t u = load_chunk<T>(z + r.head, c);
+        float x[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x[j] = grad_of(Elem<T>::get(u, j), ex, s);
+        store_chunk<T>(dz + r.head, c, x);
+      }
+      if (tid < b.edges) {
+        const int i = r.edge(tid);
+        Elem<T>::store(dz + i, grad_of(Elem<T>::load(z + i), ex, s));
+      }
+      __syncthreads();
+      if (b.c1 > b.c0) fix_listed<T, NT>(L, p, dz, ex, s, r.head + b.c0 * VEC, r.head + b.c1 * VEC);
+      if (b.edges) {
+        fix_listed<T, NT>(L, p, dz, ex, s, 0, r.head);
+        fix_listed<T, NT>(L, p, dz, ex, s, r.head + r.chunks * VEC, n);
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -417,74 +729,33 @@ __global__ __launch_bounds__(1024) void distill_total_kernel(DistillParams p) {
   }
 }
 
-// Gradient from the saved statistics: blockIdx.x cuts the row into gridDim.x
-// slabs of whole chunks, blockIdx.y (and a stride) walks the rows.
-template <typename T, int EX>
-__global__ __launch_bounds__(256) void distill_grad_kernel(DistillParams p) {
-  constexpr int VEC = Elem<T>::VEC, NT = 256;
-  __shared__ Listed L;
-  __shared__ float red[1][16];
-  const int n = p.vocab;
-  for (int64_t t = blockIdx.y; t < p.rows; t += gridDim.y) {
-    const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
-    T* dz = reinterpret_cast<T*>(p.dz) + t * p.lddz;
-    const int head = head_of(z);
-    const bool vec = head_of(dz) == head;
-    const int chunks = (n + head + VEC - 1) / VEC;
-    const int per = (chunks + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int c0 = (int)blockIdx.x * per, c1 = c0 + per < chunks ? c0 + per : chunks;
-    const float wt = p.weights ? p.weights[t] : 1.f / (float)p.rows;
-    const float m = p.stats[3 * t], inv_t = p.stats[3 * t + 1], inv_1 = p.stats[3 * t + 2];
-    if (wt == 0.f) {
-      const float zero[VEC] = {};
-      for (int c = c0 + threadIdx.x; c < c1; c += NT) store_chunk<T>(dz, c * VEC - head, n, vec, zero);
-      continue;
-    }
-    // in place (dz = z) a later block may have overwritten a listed logit, so
-    // the corrected columns are handled where their own slab is written: the
-    // value at hand is the slab's own
-    float am[1];
-    load_listed<T, NT>(L, p, t, z, am[0]);
-    block_max<NT>(am, red);
-    const float amx = am[0] == kNegInf ? 0.f : am[0];
-    float sum[1] = {0.f};
-    for (int i = threadIdx.x; i < p.top; i += NT) {
-      const float e = __builtin_amdgcn_exp2f((L.e[i] - amx) * kLog2e);
-      L.e[i] = e;
-      sum[0] += e;
-    }
-    block_sum<NT>(sum, red);
-    const float a_inv = sum[0] != 0.f ? 1.f / sum[0] : 0.f;
-    const float w = wt * (p.upstream ? *p.upstream : 1.f);
-    const Expo<EX> ex = make_expo<EX>(p, m);
-    const Scales s = grad_scales<EX>(p, w, inv_t, inv_1, a_inv, L.id[p.top] >= 0);
-    for (int c = c0 + threadIdx.x; c < c1; c += NT) {
-      const u32x4_t u = load_chunk<T>(z, c * VEC - head, n);
-      float x[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float et, e1;
-        ex(Elem<T>::get(u, j), et, e1);
-        x[j] = s.gt * et + (EX == EXP_ONE ? 0.f : s.g1 * e1);
-      }
-      store_chunk<T>(dz, c * VEC - head, n, vec, x);
-    }
-    __syncthreads();
-    fix_listed<T, NT, EX>(L, p, dz, ex, s.gt, s.g1, s.gp, s.gc, c0 * VEC - head, c1 * VEC - head);
-    __syncthreads();
-  }
+// Slabs of a row when there are few rows (1: one block a row): about two
+// blocks a compute unit, slabs of at least 1024 chunks.
+int splits_of(int64_t rows, int vocab, int dtype) {
+  const int chunks = vocab / (dtype == PMX_F32 ? 4 : 8);
+  if (rows > 128 || rows == 0 || chunks < 2048) return 1;
+  return (int)std::min<int64_t>(std::min<int64_t>(512 / rows, chunks / 1024), 64);
 }
 
 template <typename T, int EX, bool GRAD>
 hipError_t launch_rows(const DistillParams& p, hipStream_t s) {
   constexpr int VEC = Elem<T>::VEC;
-  const dim3 grid((unsigned)p.rows);
-  // the smallest block whose registers hold the row (VEC more for its head)
-  const int64_t need = (int64_t)p.vocab + VEC;
-#define PMX_ROWS(NT, NC)                                                                        \
-  if (need <= (int64_t)NT * NC * VEC) {                                                         \
-    hipLaunchKernelGGL((distill_row_kernel<T, NT, NC, EX, GRAD>), grid, dim3(NT), 0, s, p);     \
-    return hipGetLastError();                                                                   \
+  if (p.splits > 1) {
+    hipLaunchKernelGGL((distill_part_kernel<T, EX>), dim3(p.splits, (unsigned)p.rows), dim3(256), 0, s, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((distill_grad_kernel<T, EX, true>), dim3(GRAD ? p.splits : 1, (unsigned)p.rows),
+                       dim3(256), 0, s, p);
+    return hipGetLastError();
+  }
+  // the smallest block whose registers hold the row's chunks; a row shorter
+  // than two chunks may have no whole one and takes the other kernel
+  const int64_t chunks = p.vocab / VEC;
+#define PMX_ROWS(NT, NC)                                                                          \
+  if (chunks >= 2 && chunks <= (int64_t)NT * NC) {                                                               \
+    const int64_t g = std::min<int64_t>(p.rows, (int64_t)p.num_cu * waves_for(NC) * 256 / NT);    \
+    hipLaunchKernelGGL((distill_row_kernel<T, NT, NC, EX, GRAD>), dim3((unsigned)g), dim3(NT), 0, s, p); \
+    return hipGetLastError();                                                                     \
   }
   PMX_ROWS(256, 2)
   PMX_ROWS(256, 4)
@@ -493,7 +764,8 @@ hipError_t launch_rows(const DistillParams& p, hipStream_t s) {
   PMX_ROWS(512, 16)
   PMX_ROWS(1024, 16)
 #undef PMX_ROWS
-  hipLaunchKernelGGL((distill_row_kernel<T, 1024, 0, EX, GRAD>), grid, dim3(1024), 0, s, p);
+  const int64_t g = std::min<int64_t>(p.rows, (int64_t)p.num_cu * 2);
+  hipLaunchKernelGGL((distill_long_kernel<T, EX, GRAD>), dim3((unsigned)g), dim3(1024), 0, s, p);
   return hipGetLastError();
 }
 
@@ -514,30 +786,34 @@ hipError_t launch_loss_t(const DistillParams& p, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_grad_t(const DistillParams& p, hipStream_t s) {
-  // four chunks a thread and more, and blocks enough to fill the card
-  const int chunks = (p.vocab + Elem<T>::VEC - 1) / Elem<T>::VEC + 1;
-  int slabs = chunks / 1024;
-  if (slabs < 1) slabs = 1;
-  if (p.z == p.dz) slabs = 1;  // in place: one block owns the row
+  // slabs of at least 1024 chunks (four a thread); in place one block owns the
+  // row: it reads the listed logits before it overwrites them
+  int slabs = p.vocab / Elem<T>::VEC / 1024;
+  if (slabs < 1 || p.z == p.dz) slabs = 1;
   const dim3 grid((unsigned)slabs, (unsigned)(p.rows < 65535 ? p.rows : 65535));
   switch (exps_of(p)) {
-    case EXP_ONE: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_ONE>), grid, dim3(256), 0, s, p); break;
-    case EXP_TWO: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_TWO>), grid, dim3(256), 0, s, p); break;
-    default: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_SQ>), grid, dim3(256), 0, s, p); break;
+    case EXP_ONE: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_ONE, false>), grid, dim3(256), 0, s, p); break;
+    case EXP_TWO: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_TWO, false>), grid, dim3(256), 0, s, p); break;
+    default: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_SQ, false>), grid, dim3(256), 0, s, p); break;
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t distill_part_floats(int64_t, int, int) { return 0; }
+int64_t distill_part_floats(int64_t rows, int vocab, int top, int dtype) {
+  const int k = splits_of(rows, vocab, dtype);
+  return k > 1 ? rows * (k * 3 + top + 1) : 0;
+}
 
-hipError_t launch_distill_loss(const DistillParams& p, hipStream_t s) {
+hipError_t launch_distill_loss(DistillParams p, hipStream_t s) {
+  p.splits = splits_of(p.rows, p.vocab, p.dtype);
   hipError_t e = hipSuccess;
-  if (p.rows == 0) ;  // total = 0
-  else if (p.dtype == PMX_F32) e = p.dz ? launch_loss_t<float, true>(p, s) : launch_loss_t<float, false>(p, s);
-  else e = p.dz ? launch_loss_t<uint16_t, true>(p, s) : launch_loss_t<uint16_t, false>(p, s);
-  if (e != hipSuccess || !p.total) return e;
+  if (p.rows > 0) {  // (no rows: total = 0)
+    if (p.dtype == PMX_F32) e = p.dz ? launch_loss_t<float, true>(p, s) : launch_loss_t<float, false>(p, s);
+    else e = p.dz ? launch_loss_t<uint16_t, true>(p, s) : launch_loss_t<uint16_t, false>(p, s);
+  }
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(distill_total_kernel, dim3(1), dim3(1024), 0, s, p);
   return hipGetLastError();
 }

@@ -48,7 +48,8 @@ struct DistillParams {
   float* rows_loss;
   float* total;
   float* stats;          // [rows][3]: max, 1 / sum exp((z - max) / tau), 1 / sum exp(z - max)
-  float* part;           // split rows: [rows][splits][4]
+  float* part;           // rows cut over blocks: [rows][splits][3], then [rows][top + 1]
+  int splits;
   int64_t rows;
   int vocab, top;
   int dtype, teacher_dtype;
@@ -57,9 +58,9 @@ struct DistillParams {
   int num_cu;
 };
 
-// Floats of workspace (split rows only).
-int64_t distill_part_floats(int64_t rows, int vocab, int dtype);
-hipError_t launch_distill_loss(const DistillParams& p, hipStream_t s);
+// Floats of workspace (rows cut over blocks only).
+int64_t distill_part_floats(int64_t rows, int vocab, int top, int dtype);
+hipError_t launch_distill_loss(DistillParams p, hipStream_t s);
 hipError_t launch_distill_grad(const DistillParams& p, hipStream_t s);
 
 // ---------------------------------------------------------------------------

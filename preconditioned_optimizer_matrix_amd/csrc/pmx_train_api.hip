@@ -331,7 +331,7 @@ pmx_status pmx_embedding_grad(pmx_handle h, const void* dY, pmx_dtype dtype, int
 // ------------------------------------------------------------ distillation
 pmx_status pmx_distill_workspace_size(const pmx_distill_problem* q, size_t* bytes) {
   if (!bytes || !distill_shape_ok(q)) return PMX_ERR_INVALID_VALUE;
-  *bytes = (size_t)distill_part_floats(q->rows, q->vocab, q->dtype) * sizeof(float);
+  *bytes = (size_t)distill_part_floats(q->rows, q->vocab, q->top, q->dtype) * sizeof(float);
   return PMX_OK;
 }
 
@@ -343,7 +343,7 @@ pmx_status pmx_distill_loss(pmx_handle h, const pmx_distill_problem* q, float* r
   const size_t es = elem_size(q->dtype);
   if (dZ && !layout_ok(dZ, q->rows, q->vocab, lddz, es)) return PMX_ERR_INVALID_VALUE;
   if (dZ && dz_aliases(q, dZ, lddz)) return PMX_ERR_ALIAS;
-  const size_t need = (size_t)distill_part_floats(q->rows, q->vocab, q->dtype) * sizeof(float);
+  const size_t need = (size_t)distill_part_floats(q->rows, q->vocab, q->top, q->dtype) * sizeof(float);
   const Extent outs[] = {extent(rows_loss, 1, q->rows, q->rows, 4), extent(total, 1, 1, 1, 4),
                          extent(stats, q->rows, 3, 3, 4), extent(ws, 1, (int64_t)need, (int64_t)need, 1)};
   const Extent in[] = {extent(q->z, q->rows, q->vocab, q->ldz, es),

@@ -20,7 +20,7 @@ OK, ERR_INVALID_VALUE, ERR_NOT_SUPPORTED, ERR_WORKSPACE, ERR_ALIAS, ERR_HIP = ra
 RUNNING, CONVERGED, MAXITER, STAGNATED, NONFINITE, DIVERGED = -1, 0, 1, 2, 3, 4
 F32, BF16 = 0, 1
 I32, I64 = 0, 1
-MAX_GROUPS, MAX_TOP, MAX_VOCAB, MAX_TOKENS = 1000, 1024, (1 << 22) - 1, 1 << 30
+MAX_GROUPS, MAX_TOP, MAX_VOCAB, MAX_TOKENS = 1000, 1023, (1 << 22) - 1, 1 << 30
 OP_STATS, OP_INV_ROOT, OP_POLAR, OP_APPLY, OP_POLAR_VARBATCH = range(5)
 VARBATCH_MAX_DIM = 64
 VARBATCH_MAX_SIDE = 8192
