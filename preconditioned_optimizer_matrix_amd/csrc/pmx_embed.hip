@@ -7,7 +7,12 @@
 // no floating atomics, the same bits on every call.  Sums are fp32.
 //
 // Bound: HBM, tokens x dim read and vocab x dim written; the sort moves 8
-// bytes a token and pass and is all latency.
+// bytes a token and pass and is all latency.  So the sort's launches also clear
+// dW: their other blocks write zeros to every row, the rows that have tokens
+// are written again afterwards.  Up to kSmallSort tokens one block sorts them
+// in LDS in one launch.
+#include <algorithm>
+
 #include "pmx_train.h"
 
 namespace pmx {
@@ -16,7 +21,7 @@ namespace {
 constexpr int kSortThreads = 256, kSortItems = 8, kSortTile = kSortThreads * kSortItems;
 constexpr int kSortMaxBlocks = 256;  // a block sorts several tiles beyond 2^19 tokens
 constexpr int kMaxDigits = 2048;     // 11 bits a pass
-constexpr int kZeroRows = 16;        // rows of dW per clearing block
+constexpr int kSmallSort = 8192;     // tokens one block sorts in LDS
 
 struct SortPlan {
   int bits;     // key bits: keys 0 .. vocab (vocab: tokens without a row)
@@ -38,15 +43,15 @@ SortPlan sort_plan(int64_t tokens, int vocab) {
   const int64_t per = (tiles + kSortMaxBlocks - 1) / kSortMaxBlocks;
   s.span = (int)(per * kSortTile);
   s.blocks = s.span ? (int)((tokens + s.span - 1) / s.span) : 0;
-  // chunks of 32 tokens, longer ones once there are 4096
-  const int64_t c = (tokens + 4095) / 4096;
-  s.chunk = (int)(c < 32 ? 32 : (c + 7) / 8 * 8);
+  // chunks of 8 to 32 tokens, about 1024 of them; longer ones once there are 4096
+  const int64_t c = tokens <= 32768 ? (tokens + 1023) / 1024 : std::max<int64_t>(32, (tokens + 4095) / 4096);
+  s.chunk = (int)std::max<int64_t>(8, (c + 7) / 8 * 8);
   s.chunks = (int)((tokens + s.chunk - 1) / s.chunk);
   return s;
 }
 
 struct EmbedWs {
-  int* cnt;       // [passes][blocks][digits]
+  int* cnt;       // [blocks][digits]
   uint2* a;       // key, position
   uint2* b;
   float* part;    // [chunks][2][dim]
@@ -59,7 +64,7 @@ EmbedWs embed_ws(void* base, const SortPlan& s, int64_t tokens, int dim) {
   char* p = reinterpret_cast<char*>(base);
   size_t o = 0;
   w.cnt = reinterpret_cast<int*>(p + o);
-  o += up((size_t)s.passes * s.blocks * ((size_t)1 << s.dbits) * sizeof(int));
+  o += up((size_t)s.blocks * ((size_t)1 << s.dbits) * sizeof(int));
   w.a = reinterpret_cast<uint2*>(p + o);
   o += up((size_t)tokens * sizeof(uint2));
   w.b = reinterpret_cast<uint2*>(p + o);
@@ -120,46 +125,173 @@ __device__ __forceinline__ uint32_t key_of(const EmbedParams& p, int64_t t) {
   return id < 0 || id >= p.vocab || id == p.padding_idx ? (uint32_t)p.vocab : (uint32_t)id;
 }
 
-// Digit counts of pass 1 per block; the counts of pass 2 are cleared here and
-// filled while pass 1 scatters.
-__global__ __launch_bounds__(kSortThreads) void embed_hist_kernel(EmbedParams p, SortPlan s, int* cnt) {
+// Rows [r0, r1) of dW to be cleared by the blocks of a launch from
+// `first_block` on.
+struct Clear {
+  int r0, r1, first_block;
+};
+
+template <typename O>
+__device__ __forceinline__ void store_zero4(O* d, int left);
+
+template <typename O>
+__device__ __forceinline__ void clear_rows(const EmbedParams& p, const Clear& z) {
+  const int quads = (p.dim + 3) / 4;
+  const int blocks = (int)gridDim.x - z.first_block;
+  for (int v = z.r0 + ((int)blockIdx.x - z.first_block); v < z.r1; v += blocks) {
+    O* d = reinterpret_cast<O*>(p.out) + (int64_t)v * p.ld_out;
+    for (int q = threadIdx.x; q < quads; q += blockDim.x) store_zero4<O>(d + 4 * q, p.dim - 4 * q);
+  }
+}
+__device__ __forceinline__ void clear_any(const EmbedParams& p, const Clear& z) {
+  if (p.out_dtype == PMX_F32) clear_rows<float>(p, z);
+  else clear_rows<uint16_t>(p, z);
+}
+
+// All of the sort in one block, for up to kSmallSort tokens: LDS holds the
+// (key, position) pairs, a pass ranks them (in registers) and puts them back
+// in the new order.
+__global__ __launch_bounds__(1024) void embed_sort_small_kernel(EmbedParams p, SortPlan s, uint2* out, Clear z) {
+  constexpr int W = 16, N = kSmallSort / 1024;
+  __shared__ uint2 pair[kSmallSort];
+  __shared__ uint16_t wcnt[W][kMaxDigits];
+  __shared__ int wsum[W];
+  if ((int)blockIdx.x >= z.first_block) {
+    clear_any(p, z);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, tokens = (int)p.tokens;
+  const int nd = 1 << s.dbits;
+  // wave w has tokens w per .. of `per`, a multiple of 64
+  const int steps = (tokens + 1023) / 1024, base = wid * steps * 64;
+  uint2 kp[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int t = base + i * 64 + lane;
+    kp[i] = i < steps && t < tokens ? make_uint2(key_of(p, t), (uint32_t)t) : make_uint2(0, 0);
+  }
+  for (int pass = 0; pass < s.passes; ++pass) {
+    const int shift = pass * s.dbits;
+    if (pass) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int t = base + i * 64 + lane;
+        if (i < steps && t < tokens) kp[i] = pair[t];
+      }
+    }
+    for (int d = tid; d < nd; d += 1024)
+#pragma unroll
+      for (int w = 0; w < W; ++w) wcnt[w][d] = 0;
+    __syncthreads();
+    int rank[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      rank[i] = 0;
+      if (i < steps) {
+        const bool live = base + i * 64 + lane < tokens;
+        const int d = (kp[i].x >> shift) & (nd - 1);
+        uint64_t m = __ballot(live);
+        for (int bit = 0; bit < s.dbits; ++bit) {
+          const uint64_t v = __ballot((d >> bit) & 1);
+          m &= ((d >> bit) & 1) ? v : ~v;
+        }
+        const int first = m ? __builtin_ctzll(m) : 0;
+        // one wave's counters: the first lane of each digit reads and adds
+        int old = 0;
+        if (live && lane == first) {
+          volatile uint16_t* c = &wcnt[wid][d];
+          old = *c;
+          *c = (uint16_t)(old + __popcll(m));
+        }
+        old = __shfl(old, first);
+        rank[i] = old + __popcll(m & ((1ull << lane) - 1));
+      }
+    }
+    __syncthreads();
+    // digits' totals, their exclusive sum, then every wave's start
+    const int each = (nd + 1023) / 1024;  // 1 or 2 digits a thread
+    int total = 0;
+    for (int e = 0; e < each; ++e) {
+      const int d = tid * each + e;
+      if (d < nd)
+#pragma unroll
+        for (int w = 0; w < W; ++w) total += wcnt[w][d];
+    }
+    int incl = total;
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 63) wsum[wid] = incl;
+    __syncthreads();
+    int o = incl - total;
+    for (int w = 0; w < wid; ++w) o += wsum[w];
+    for (int e = 0; e < each; ++e) {
+      const int d = tid * each + e;
+      if (d < nd)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int x = wcnt[w][d];
+          wcnt[w][d] = (uint16_t)o;
+          o += x;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < steps && base + i * 64 + lane < tokens)
+        pair[wcnt[wid][(kp[i].x >> shift) & (nd - 1)] + rank[i]] = kp[i];
+    __syncthreads();
+  }
+  for (int t = tid; t < tokens; t += 1024) out[t] = pair[t];
+}
+
+// Digit counts of a pass per block, [blocks][digits].  (Counting pass 2 with
+// global atomics while pass 1 scatters took 24 us for 32768 tokens, of which a
+// frequent id's atomics on one counter were half.)
+template <bool FIRST>
+__global__ __launch_bounds__(kSortThreads) void embed_hist_kernel(EmbedParams p, SortPlan s, int* cnt,
+                                                                  const uint2* in, Clear z) {
   __shared__ int h[kMaxDigits];
+  if ((int)blockIdx.x >= z.first_block) {
+    clear_any(p, z);
+    return;
+  }
   const int nd = 1 << s.dbits;
   for (int d = threadIdx.x; d < nd; d += kSortThreads) h[d] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * s.span;
   const int64_t t1 = t0 + s.span < p.tokens ? t0 + s.span : p.tokens;
   for (int64_t t = t0 + threadIdx.x; t < t1; t += kSortThreads)
-    atomicAdd(&h[key_of(p, t) & (nd - 1)], 1);
+    atomicAdd(&h[((FIRST ? key_of(p, t) : in[t].x) >> (FIRST ? 0 : s.dbits)) & (nd - 1)], 1);
   __syncthreads();
-  int* c1 = cnt + (int64_t)blockIdx.x * nd;
-  int* c2 = cnt + ((int64_t)s.blocks + blockIdx.x) * nd;
-  for (int d = threadIdx.x; d < nd; d += kSortThreads) {
-    c1[d] = h[d];
-    if (s.passes > 1) c2[d] = 0;
-  }
+  for (int d = threadIdx.x; d < nd; d += kSortThreads) cnt[(int64_t)blockIdx.x * nd + d] = h[d];
 }
 
 // One stable scatter pass.  A wave ranks 64 consecutive tokens at a time by
 // matching digits with ballots; waves and tiles follow each other in order.
 template <bool FIRST>
-__global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(EmbedParams p, SortPlan s, int* cnt,
-                                                                     const uint2* in, uint2* out) {
+__global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(EmbedParams p, SortPlan s, const int* c,
+                                                                     const uint2* in, uint2* out, Clear z) {
   constexpr int W = kSortThreads / 64;
   __shared__ int wcnt[W][kMaxDigits];
   __shared__ int base[kMaxDigits];
   __shared__ int part[kSortThreads];
+  if ((int)blockIdx.x >= z.first_block) {
+    clear_any(p, z);
+    return;
+  }
   const int nd = 1 << s.dbits, shift = FIRST ? 0 : s.dbits;
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
   // where each digit's tokens of this block begin: the digit's place in the
   // whole order plus what earlier blocks hold of it
-  const int* c = cnt + (FIRST ? 0 : (int64_t)s.blocks * nd);
   const int each = nd > kSortThreads ? nd / kSortThreads : 1;  // digits a thread
   int total = 0;
   for (int i = 0; i < each; ++i) {
     const int d = tid * each + i;
     if (d < nd) {
       int all = 0, before = 0;
+#pragma unroll 8
       for (int b = 0; b < s.blocks; ++b) {
         const int x = c[(int64_t)b * nd + d];
         if (b < (int)blockIdx.x) before += x;
@@ -243,8 +375,6 @@ __global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(EmbedParams
       if (t < t1) {
         const int dst = wcnt[wid][(key[i] >> shift) & (nd - 1)] + rank[i];
         out[dst] = make_uint2(key[i], pos[i]);
-        if (FIRST && s.passes > 1)
-          atomicAdd(&cnt[((int64_t)s.blocks + dst / s.span) * nd + ((key[i] >> s.dbits) & (nd - 1))], 1);
       }
     }
   }
@@ -301,6 +431,11 @@ __device__ __forceinline__ void store4(T* p, int left, f32x4_t v) {
   }
 }
 
+template <typename O>
+__device__ __forceinline__ void store_zero4(O* d, int left) {
+  store4<O>(d, left, f32x4_t{0.f, 0.f, 0.f, 0.f});
+}
+
 // A finished row: four of its columns.
 template <typename O>
 __device__ __forceinline__ void put_row(const EmbedParams& p, uint32_t key, int col, f32x4_t acc) {
@@ -315,42 +450,16 @@ __device__ __forceinline__ void put_row(const EmbedParams& p, uint32_t key, int 
 // of the sorted order and 4 blockDim.x columns; a run inside the chunk is
 // finished here, a run that reaches over its ends leaves a partial sum (slot 0:
 // the run that enters the chunk, slot 1: the run that leaves it), joined by
-// embed_join_kernel.  Blocks past the chunks clear the rows without tokens.
-template <typename T, typename O>
-__global__ __launch_bounds__(256) void embed_sum_kernel(EmbedParams p, SortPlan s, const uint2* sorted,
-                                                        float* part, int sum_blocks, int slabs) {
+// embed_join_kernel.  WAVE: blockDim.x is a multiple of 64, so a wave has one
+// chunk and reads its keys through the scalar cache.
+template <typename T, typename O, bool WAVE>
+__global__ __launch_bounds__(256) void embed_sum_kernel(EmbedParams p, SortPlan s,
+                                                        const uint2* __restrict__ sorted,
+                                                        float* __restrict__ part, int slabs) {
   const int tokens = (int)p.tokens;
-  if ((int)blockIdx.x >= sum_blocks) {
-    __shared__ int present[kZeroRows];
-    __shared__ int lim[2];
-    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-    const int nt = blockDim.x * blockDim.y;
-    const int64_t v0 = (int64_t)(blockIdx.x - sum_blocks) * kZeroRows;
-    const int64_t v1 = v0 + kZeroRows < p.vocab ? v0 + kZeroRows : p.vocab;
-    if (tid < kZeroRows) present[tid] = 0;
-    if (tid < 2) {  // first sorted position with key >= v0, and >= v1
-      const uint32_t want = (uint32_t)(tid ? v1 : v0);
-      int lo = 0, hi = tokens;
-      while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (sorted[mid].x < want) lo = mid + 1;
-        else hi = mid;
-      }
-      lim[tid] = lo;
-    }
-    __syncthreads();
-    for (int i = lim[0] + tid; i < lim[1]; i += nt) present[sorted[i].x - (uint32_t)v0] = 1;
-    __syncthreads();
-    const int quads = (p.dim + 3) / 4;
-    for (int64_t v = v0; v < v1; ++v) {
-      if (present[v - v0]) continue;
-      O* d = reinterpret_cast<O*>(p.out) + v * p.ld_out;
-      for (int q = tid; q < quads; q += nt) store4<O>(d + 4 * q, p.dim - 4 * q, f32x4_t{0.f, 0.f, 0.f, 0.f});
-    }
-    return;
-  }
+  const int ty = WAVE ? __builtin_amdgcn_readfirstlane(threadIdx.y) : threadIdx.y;
   const int cg = (int)blockIdx.x / slabs, slab = (int)blockIdx.x % slabs;
-  const int64_t chunk = (int64_t)cg * blockDim.y + threadIdx.y;
+  const int64_t chunk = (int64_t)cg * blockDim.y + ty;
   const int col = (slab * (int)blockDim.x + (int)threadIdx.x) * 4;
   if (chunk >= s.chunks || col >= p.dim) return;
   const int c0 = (int)(chunk * s.chunk);
@@ -395,30 +504,58 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedParams p, SortPlan 
   else put_row<O>(p, cur, col, acc);
 }
 
-// Runs over chunk ends: the chunk a run begins in adds the partial sums of
-// the chunks it goes through, in their order.
+// Runs over chunk ends: one block a chunk (and slab of columns); the chunk a
+// run begins in adds the partial sums of the chunks it goes through.  Their
+// number comes from one look at the chunks' first keys by all threads; then
+// threadIdx.y deals them out in contiguous shares, joined in order.  (Partial
+// sums come from other XCDs' caches, about 2 us a dependent load: one thread
+// walking a frequent id's 65 chunks took 50 us.)
 template <typename O>
-__global__ __launch_bounds__(256) void embed_join_kernel(EmbedParams p, SortPlan s, const uint2* sorted,
-                                                         const float* part, int slabs) {
+__global__ __launch_bounds__(1024) void embed_join_kernel(EmbedParams p, SortPlan s, const uint2* __restrict__ sorted,
+                                                          const float* __restrict__ part, int slabs) {
+  __shared__ f32x4_t sums[1024];
   const int tokens = (int)p.tokens;
-  const int cg = (int)blockIdx.x / slabs, slab = (int)blockIdx.x % slabs;
-  const int64_t chunk = (int64_t)cg * blockDim.y + threadIdx.y;
+  const int slab = (int)blockIdx.x % slabs;
+  const int64_t chunk = (int)blockIdx.x / slabs;
   const int col = (slab * (int)blockDim.x + (int)threadIdx.x) * 4;
-  if (chunk >= s.chunks || col >= p.dim) return;
   const int64_t c0 = chunk * s.chunk, c1 = c0 + s.chunk;
   if (c1 >= tokens) return;  // nothing follows
   const uint32_t key = sorted[c1 - 1].x;
   if (key == (uint32_t)p.vocab || sorted[c1].x != key) return;
   if (c0 > 0 && sorted[c0].x == key && sorted[c0 - 1].x == key) return;  // began earlier
-  const int left = p.dim - col;
-  f32x4_t acc = load4<float>(part + ((int64_t)chunk * 2 + 1) * p.dim + col, left);
-  // the last chunk of the run: the one whose next position has another key
-  for (int64_t c = chunk + 1; c < s.chunks; ++c) {
-    acc += load4<float>(part + (c * 2) * p.dim + col, left);
-    const int64_t e = (c + 1) * s.chunk;
-    if (e >= tokens || sorted[e - 1].x != key || sorted[e].x != key) break;
+  const int nt = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
+  int n = 0;  // chunks after this one that the run enters
+  for (;;) {
+    const int64_t c = chunk + 1 + n + tid;
+    const int k = __syncthreads_count(c < s.chunks && sorted[c * s.chunk].x == key);
+    n += k;
+    if (k < nt) break;
   }
-  put_row<O>(p, key, col, acc);
+  const int left = p.dim - col;
+  // this thread's share of the slots 1 of `chunk`, then 0 of chunk + 1 .. + n
+  const int ny = blockDim.y, i0 = (int)((int64_t)(n + 1) * threadIdx.y / ny),
+            i1 = (int)((int64_t)(n + 1) * (threadIdx.y + 1) / ny);
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  if (left > 0) {
+    constexpr int U = 8;
+    for (int i = i0; i < i1; i += U) {
+      f32x4_t v[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int64_t at = i + j < i1 ? i + j : i;  // past the share: read, not added
+        v[j] = load4<float>(part + ((chunk + at) * 2 + (at == 0)) * p.dim + col, left);
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (i + j < i1) acc += v[j];
+    }
+  }
+  sums[tid] = acc;
+  __syncthreads();
+  if (threadIdx.y == 0 && left > 0) {
+    for (int y = 1; y < ny; ++y) acc += sums[y * blockDim.x + tid];
+    put_row<O>(p, key, col, acc);
+  }
 }
 
 int pow2_up(int x) {
@@ -445,20 +582,46 @@ hipError_t lookup_t(const EmbedParams& p, int vb, hipStream_t s) {
   return hipGetLastError();
 }
 
+// `blocks` sorting blocks and, unless dW is added to, blocks that clear its
+// rows [from, to) of `tenths` tenths.
+dim3 with_clear(const EmbedParams& p, int blocks, int from, int to, int tenths, Clear* z) {
+  z->r0 = (int)((int64_t)p.vocab * from / tenths);
+  z->r1 = (int)((int64_t)p.vocab * to / tenths);
+  z->first_block = blocks;
+  const int rows = p.accumulate ? 0 : z->r1 - z->r0;
+  return dim3((unsigned)(blocks + std::min(rows, 2048)));
+}
+
 template <typename T, typename O>
 hipError_t grad_t(const EmbedParams& p, hipStream_t st) {
   const SortPlan s = sort_plan(p.tokens, p.vocab);
   const EmbedWs w = embed_ws(p.ws, s, p.tokens, p.dim);
   const uint2* sorted = w.a;
   hipError_t e;
-  if (p.tokens > 0) {
-    const dim3 g(s.blocks), b(kSortThreads);
-    hipLaunchKernelGGL(embed_hist_kernel, g, b, 0, st, p, s, w.cnt);
+  Clear z;
+  const dim3 b(kSortThreads);
+  if (p.tokens <= kSmallSort) {
+    const dim3 g = with_clear(p, p.tokens > 0, 0, 1, 1, &z);
+    if (g.x == 0) return hipSuccess;
+    hipLaunchKernelGGL(embed_sort_small_kernel, g, dim3(1024), 0, st, p, s, w.a, z);
+    if ((e = hipGetLastError()) != hipSuccess || p.tokens == 0) return e;
+  } else {
+    // the clearing is dealt out over the launches by the sort's share of them
+    const bool two = s.passes > 1;
+    dim3 g = with_clear(p, s.blocks, 0, two ? 2 : 4, 10, &z);
+    hipLaunchKernelGGL((embed_hist_kernel<true>), g, b, 0, st, p, s, w.cnt, (const uint2*)nullptr, z);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((embed_scatter_kernel<true>), g, b, 0, st, p, s, w.cnt, (const uint2*)nullptr, w.a);
+    g = with_clear(p, s.blocks, two ? 2 : 4, two ? 5 : 10, 10, &z);
+    hipLaunchKernelGGL((embed_scatter_kernel<true>), g, b, 0, st, p, s, (const int*)w.cnt, (const uint2*)nullptr,
+                       w.a, z);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (s.passes > 1) {
-      hipLaunchKernelGGL((embed_scatter_kernel<false>), g, b, 0, st, p, s, w.cnt, (const uint2*)w.a, w.b);
+    if (two) {
+      g = with_clear(p, s.blocks, 5, 7, 10, &z);
+      hipLaunchKernelGGL((embed_hist_kernel<false>), g, b, 0, st, p, s, w.cnt, (const uint2*)w.a, z);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      g = with_clear(p, s.blocks, 7, 10, 10, &z);
+      hipLaunchKernelGGL((embed_scatter_kernel<false>), g, b, 0, st, p, s, (const int*)w.cnt, (const uint2*)w.a,
+                         w.b, z);
       if ((e = hipGetLastError()) != hipSuccess) return e;
       sorted = w.b;
     }
@@ -468,14 +631,14 @@ hipError_t grad_t(const EmbedParams& p, hipStream_t st) {
   if (tx < 16) tx = 16;
   const dim3 block(tx, 256 / tx);
   const int slabs = (quads + tx - 1) / tx;
-  const int sum_blocks = (int)((s.chunks + block.y - 1) / block.y) * slabs;
-  const int zero_blocks = p.accumulate ? 0 : (p.vocab + kZeroRows - 1) / kZeroRows;
-  if (sum_blocks + zero_blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL((embed_sum_kernel<T, O>), dim3(sum_blocks + zero_blocks), block, 0, st, p, s, sorted,
-                     w.part, sum_blocks, slabs);
+  const dim3 grid((unsigned)((s.chunks + block.y - 1) / block.y * slabs));
+  if (tx >= 64)
+    hipLaunchKernelGGL((embed_sum_kernel<T, O, true>), grid, block, 0, st, p, s, sorted, w.part, slabs);
+  else
+    hipLaunchKernelGGL((embed_sum_kernel<T, O, false>), grid, block, 0, st, p, s, sorted, w.part, slabs);
   if ((e = hipGetLastError()) != hipSuccess || s.chunks < 2) return e;
-  hipLaunchKernelGGL((embed_join_kernel<O>), dim3(sum_blocks), block, 0, st, p, s, sorted,
-                     (const float*)w.part, slabs);
+  hipLaunchKernelGGL((embed_join_kernel<O>), dim3((unsigned)(s.chunks * slabs)), dim3(tx, 1024 / tx), 0, st, p, s,
+                     sorted, (const float*)w.part, slabs);
   return hipGetLastError();
 }
 
