@@ -163,8 +163,8 @@ __device__ __forceinline__ u32x4_t load_win(const E* row, int c, int n) {
 // ------------------------------------------------------------ tiles
 // Block tile BM x BN x BK, wave tile WM x WN; LDS layout of an operand of
 // `R` rows: k-contiguous [R][BK + 16 bytes], or [BK][pitch] as it lies.  The
-// pitch of the transpose-read form is 16 or 48 dwords modulo 64, which puts the
-// four k rows of a read on distinct banks; fp32 reads rows of consecutive
+// pitch of the transpose-read form is 8, 16 or 48 dwords modulo 64, which puts
+// the four k rows of a read on distinct banks; fp32 reads rows of consecutive
 // words (any pitch).
 template <typename E_, int BM_, int BN_, int BK_, int WM_, int WN_, int MINB_>
 struct Cfg {
@@ -175,7 +175,7 @@ struct Cfg {
   static constexpr int FM = WM / 32, FN = WN / 32;
   static constexpr int LDK = BK + VEC;
   static constexpr int pitch(int r) {
-    return sizeof(E) == 2 ? (r == 32 ? 32 : r + 32) : r + 4;
+    return sizeof(E) == 2 ? (r == 32 ? 32 : r == 128 ? 144 : r + 32) : r + 4;
   }
   static constexpr int size(bool kc, int r) { return kc ? r * LDK : BK * pitch(r); }
 };
@@ -359,6 +359,134 @@ __device__ __forceinline__ void mainloop(f32x16 (&acc)[C::FM][C::FN], typename C
   }
 }
 
+// ------------------------------------------------------------ pipelined tiles
+// The middle and large tiles.  Operand pieces are a base that is the same for
+// the block and a 32-bit offset a piece; a k tile's whole pieces only (the rest
+// of the contraction follows by itself), k rows and tile rows in range.
+template <class C, bool KC, int R>
+struct Stream {
+  typedef typename C::E E;
+  typedef Operand<C, KC, R> O;
+  static constexpr int N = O::N, PER = O::PER, VEC = C::VEC;
+  const E* base;
+  int64_t step;      // elements a k tile
+  uint32_t off[N];
+  int r0, limit;     // as Operand
+  int64_t ld;
+
+  // limit >= VEC when not KC: the piece over the last column is read as the
+  // last VEC columns
+  __device__ __forceinline__ void init(const E* b, int64_t ld_, int r0_, int limit_) {
+    r0 = r0_;
+    limit = limit_;
+    ld = ld_;
+    base = KC ? b + (int64_t)r0 * ld : b;
+    step = KC ? C::BK : (int64_t)C::BK * ld;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = threadIdx.x + C::THREADS * i, s = idx / PER, c = idx % PER * VEC;
+      off[i] = KC ? (uint32_t)(min(s, limit - 1 - r0) * (int)ld + c)
+                  : (uint32_t)(s * (int)ld + min(r0 + c, limit - VEC));
+    }
+  }
+  __device__ __forceinline__ void load(u32x4_t (&v)[N], int kt) const {
+    const E* p = base + kt * step;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = load16(p + off[i]);
+  }
+  // EDGE: a piece that was moved down to the last VEC columns goes to their
+  // places by element (columns past the last hold anything)
+  template <bool EDGE>
+  __device__ __forceinline__ void store(E* lds, const u32x4_t (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = threadIdx.x + C::THREADS * i, s = idx / PER, c = idx % PER * VEC;
+      E* d = lds + s * (KC ? C::LDK : C::pitch(R)) + c;
+      if (!EDGE || KC || r0 + c + VEC <= limit) {
+        *reinterpret_cast<u32x4_t*>(d) = v[i];
+      } else if (r0 + c < limit) {
+        const int sh = r0 + c + VEC - limit;  // 1 .. VEC - 1
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (c - sh + j >= 0) {
+            if constexpr (sizeof(E) == 2) d[j - sh] = (E)(v[i][j >> 1] >> (16 * (j & 1)));
+            else d[j - sh] = __uint_as_float(v[i][j]);
+          }
+      }
+    }
+  }
+  // the last k tile: zeros at k >= kend, piece by piece
+  __device__ __forceinline__ void tail(E* lds, int k0, int kend) const {
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+      const int idx = threadIdx.x + C::THREADS * i, s = idx / PER, c = idx % PER * VEC;
+      u32x4_t v = {0u, 0u, 0u, 0u};
+      if (KC) v = load_win(base + (int64_t)min(s, limit - 1 - r0) * ld, k0 + c, kend);
+      else if (k0 + s < kend) v = load_win(base + (int64_t)(k0 + s) * ld, r0 + c, limit);
+      *reinterpret_cast<u32x4_t*>(lds + s * (KC ? C::LDK : C::pitch(R)) + c) = v;
+    }
+  }
+};
+
+// Scheduling groups: MF MFMAs, each followed by up to PER instructions of class
+// MASK (0x100 LDS read, 0x200 LDS write) until OPS are placed.
+template <int MF, int OPS, int MASK, int PER>
+__device__ __forceinline__ void interleave() {
+  if constexpr (MF > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    constexpr int k = OPS < PER ? OPS : PER;
+    if constexpr (k > 0) __builtin_amdgcn_sched_group_barrier(MASK, k, 0);
+    interleave<MF - 1, OPS - k, MASK, PER>();
+  } else if constexpr (OPS > 0) {
+    __builtin_amdgcn_sched_group_barrier(MASK, OPS, 0);
+  }
+}
+
+// k tiles [kb, ke) of whole pieces; `va`, `vb` hold k tile kb on entry.  A k
+// tile is one block of instructions: its fragments are read a 16-wide step
+// ahead of the MFMAs, the next tile goes from the registers to the other LDS
+// buffer under the last step's, and the loads of the tile after that are issued
+// before the barrier.
+template <class C, int FORM, bool EDGE>
+__device__ __forceinline__ void stream_loop(f32x16 (&acc)[C::FM][C::FN], typename C::E* smem,
+                                            const Stream<C, a_kc(FORM), C::BM>& A,
+                                            const Stream<C, b_kc(FORM), C::BN>& B,
+                                            u32x4_t (&va)[Stream<C, a_kc(FORM), C::BM>::N],
+                                            u32x4_t (&vb)[Stream<C, b_kc(FORM), C::BN>::N], int kb, int ke,
+                                            int wm, int wn) {
+  constexpr int SA = C::size(a_kc(FORM), C::BM), ST = SA + C::size(b_kc(FORM), C::BN);
+  constexpr int NA = Stream<C, a_kc(FORM), C::BM>::N, NB = Stream<C, b_kc(FORM), C::BN>::N;
+  A.template store<EDGE>(smem, va);
+  B.template store<EDGE>(smem + SA, vb);
+  {
+    const int k1 = min(kb + 1, ke - 1);  // past the last tile: the last one again
+    A.load(va, k1);
+    B.load(vb, k1);
+  }
+  __syncthreads();
+  for (int kt = kb; kt < ke; ++kt) {
+    const int cur = (kt - kb) & 1;
+    typename C::E* s = smem + cur * ST;
+    typename C::E* d = smem + (cur ^ 1) * ST;
+    multiply<C, FORM>(acc, s, s + SA, wm, wn);
+    A.template store<EDGE>(d, va);
+    B.template store<EDGE>(d + SA, vb);
+    const int k2 = min(kt + 2, ke - 1);
+    A.load(va, k2);
+    B.load(vb, k2);
+    if constexpr (!EDGE && sizeof(typename C::E) == 2) {
+      constexpr int MF = C::FM * C::FN, STEPS = C::BK / 16;
+      constexpr int NF = C::FM * (a_kc(FORM) ? 1 : 2) + C::FN * (b_kc(FORM) ? 1 : 2);
+      __builtin_amdgcn_sched_group_barrier(0x100, NF, 0);
+#pragma unroll
+      for (int st = 0; st + 1 < STEPS; ++st) interleave<MF, NF, 0x100, (NF + MF - 1) / MF>();
+      interleave<MF, NA + NB, 0x200, (NA + NB + MF - 1) / MF>();
+      __builtin_amdgcn_sched_group_barrier(0x020, NA + NB, 0);
+    }
+    __syncthreads();
+  }
+}
+
 // Four columns of a row of C at c (row length n): plain, or added to.
 template <typename O>
 __device__ __forceinline__ void put4(O* row, int c, int n, f32x4_t v, bool add) {
@@ -388,6 +516,24 @@ __device__ __forceinline__ void put4(O* row, int c, int n, f32x4_t v, bool add) 
   }
 }
 
+// Rows of no group are zeros.
+template <class C, typename O, bool SPLIT>
+__device__ __forceinline__ void zero_outside(const Table& T, const GroupedParams& p, int splits) {
+  const int b0 = T.begin[0], b1 = T.begin[p.groups], outside = b0 + (int)p.rows - b1;
+  for (int i = blockIdx.x; i < outside; i += gridDim.x) {
+    const int64_t row = i < b0 ? i : b1 + (i - b0);
+    for (int c = threadIdx.x * 4; c < p.n; c += C::THREADS * 4) {
+      const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (SPLIT) {
+        for (int s = 0; s < splits; ++s)
+          put4<float>(p.part + ((int64_t)s * p.rows + row) * p.n, c, p.n, zero, false);
+      } else {
+        put4<O>(reinterpret_cast<O*>(p.c) + row * p.ldc, c, p.n, zero, false);
+      }
+    }
+  }
+}
+
 // O: element of C (float or bf16 bits); SPLIT: fp32 partial results to p.part.
 template <class C, int FORM, typename O, bool SPLIT>
 __global__ __launch_bounds__(C::THREADS, C::MINB) void grouped_kernel(GroupedParams p) {
@@ -404,22 +550,7 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void grouped_kernel(GroupedPar
   const int splits = SPLIT ? p.splits : 1;
   const int64_t part_ld = p.n;
 
-  if constexpr (FORM != TN) {
-    // rows of no group are zeros
-    const int b0 = T.begin[0], b1 = T.begin[p.groups], outside = b0 + (int)p.rows - b1;
-    for (int i = blockIdx.x; i < outside; i += gridDim.x) {
-      const int64_t row = i < b0 ? i : b1 + (i - b0);
-      for (int c = threadIdx.x * 4; c < p.n; c += C::THREADS * 4) {
-        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (SPLIT) {
-          for (int s = 0; s < splits; ++s)
-            put4<float>(p.part + ((int64_t)s * p.rows + row) * part_ld, c, p.n, zero, false);
-        } else {
-          put4<O>(reinterpret_cast<O*>(p.c) + row * p.ldc, c, p.n, zero, false);
-        }
-      }
-    }
-  }
+  if constexpr (FORM != TN) zero_outside<C, O, SPLIT>(T, p, splits);
 
   // Blocks are dealt to the 8 XCDs round-robin: XCD x takes a contiguous range
   // of the items, so neighbouring tiles share its L2.
@@ -487,6 +618,178 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void grouped_kernel(GroupedPar
   }
 }
 
+// Rows of C leave through LDS: a wave writes 32 rows of its tile, then stores
+// them as 16-byte pieces, whole 128-byte lines, instead of 8- and 16-byte ones
+// of 32 rows at a time.  `stage`: the wave's own 32 x (WN + 8 or 4) elements.
+template <class C, typename O>
+__device__ __forceinline__ void store_rows(const f32x16 (&acc)[C::FN], O* stage, O* c, int64_t ldc, int row0,
+                                           int rows, int col0, int cols) {
+  constexpr int PIT = C::WN + 16 / (int)sizeof(O), V = 16 / (int)sizeof(O), LPR = C::WN / V;  // lanes a row
+  const int lane = threadIdx.x & 63;
+  O* w = stage + (lane & 31) * PIT + 4 * (lane >> 5);
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4_t v = {acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
+      if constexpr (sizeof(O) == 4) *reinterpret_cast<f32x4_t*>(w + 32 * j + 8 * g) = v;
+      else *reinterpret_cast<u32x2_t*>(w + 32 * j + 8 * g) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    }
+  // the wave's lanes exchange through LDS: nothing moves across this point
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  const int cl = lane % LPR * V, left = cols - (col0 + cl);
+#pragma unroll
+  for (int r = 0; r < 32; r += 64 / LPR) {
+    const int rr = r + lane / LPR;
+    if (row0 + rr >= rows || left <= 0) continue;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stage + rr * PIT + cl);
+    O* d = c + (int64_t)(row0 + rr) * ldc + col0 + cl;
+    if (left >= V) {
+      if constexpr (sizeof(O) == 2) *reinterpret_cast<u32x4_a2*>(d) = v;
+      else *reinterpret_cast<u32x4_a4*>(d) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V - 1; ++j)
+        if (j < left) {
+          if constexpr (sizeof(O) == 2) d[j] = (O)(v[j >> 1] >> (16 * (j & 1)));
+          else d[j] = __uint_as_float(v[j]);
+        }
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The same products on pipelined tiles.  Blocks are persistent: the first k
+// tile of a block's next item is loaded before the item's results are stored.
+template <class C, int FORM, typename O, bool SPLIT>
+__global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_tile_kernel(GroupedParams p) {
+  typedef typename C::E E;
+  constexpr bool AK = a_kc(FORM), BK_ = b_kc(FORM);
+  constexpr int SA = C::size(AK, C::BM), ST = SA + C::size(BK_, C::BN);
+  // two k tiles; the waves' 32-row stages of C take their place
+  constexpr int STAGE = 32 * (C::WN + 16 / (int)sizeof(O)) * (int)sizeof(O);
+  constexpr int LDS = STAGE * C::WAVES / (int)sizeof(E) > 2 * ST ? STAGE * C::WAVES / (int)sizeof(E) : 2 * ST;
+  __shared__ __attribute__((aligned(16))) E smem[LDS];
+  __shared__ Table T;
+  const int tiles_n = (p.n + C::BN - 1) / C::BN;
+  const int tiles_m = FORM == TN ? (p.m + C::BM - 1) / C::BM : 0;
+  build_table(T, p, C::BM, tiles_n, FORM == TN ? tiles_m * tiles_n : 0);
+  const int wid = threadIdx.x >> 6;
+  constexpr int WGN = C::BN / C::WN;
+  const int wm = wid / WGN * C::WM, wn = wid % WGN * C::WN;
+  const int splits = SPLIT ? p.splits : 1;
+  if constexpr (FORM != TN) zero_outside<C, O, SPLIT>(T, p, splits);
+
+  const int items = T.tile[p.groups] * splits;
+  const int per = (items + 7) >> 3, x = blockIdx.x & 7, step = gridDim.x >> 3;
+  int jx = blockIdx.x >> 3;
+  struct Item {
+    int e, r0, m0, n0, K, M, kb, ke, sp;
+  };
+  auto next = [&](Item& it) -> bool {
+    const int q = x * per + jx;
+    if (jx >= per || q >= items) return false;
+    jx += step;
+    const int t = SPLIT ? q / splits : q;
+    it.sp = SPLIT ? q - t * splits : 0;
+    it.e = group_of(T, p.groups, t);
+    it.r0 = T.begin[it.e];
+    const int nr = T.begin[it.e + 1] - it.r0;
+    int tm, tn;
+    tile_of(t - T.tile[it.e], FORM == TN ? tiles_m : (nr + C::BM - 1) / C::BM, tiles_n, tm, tn);
+    it.m0 = tm * C::BM;
+    it.n0 = tn * C::BN;
+    it.K = FORM == TN ? nr : p.k;
+    it.M = FORM == TN ? p.m : nr;
+    const int nk = (it.K + C::BK - 1) / C::BK;
+    it.kb = SPLIT ? (int)((int64_t)nk * it.sp / splits) : 0;
+    it.ke = SPLIT ? (int)((int64_t)nk * (it.sp + 1) / splits) : nk;
+    return true;
+  };
+  Stream<C, AK, C::BM> A;
+  Stream<C, BK_, C::BN> B;
+  u32x4_t va[Stream<C, AK, C::BM>::N], vb[Stream<C, BK_, C::BN>::N];
+  // the item's operands, and its first whole k tile on the way
+  auto start = [&](const Item& it) {
+    const E* a = reinterpret_cast<const E*>(p.a) + (int64_t)it.r0 * p.lda;
+    const E* b = reinterpret_cast<const E*>(p.b) +
+                 (FORM == TN ? (int64_t)it.r0 * p.ldb : (int64_t)it.e * p.stride_b);
+    A.init(a, p.lda, it.m0, it.M);
+    B.init(b, p.ldb, it.n0, p.n);
+    if (it.kb < min(it.ke, it.K / C::BK)) {
+      A.load(va, it.kb);
+      B.load(vb, it.kb);
+    }
+  };
+  Item it;
+  if (!next(it)) return;
+  start(it);
+  for (;;) {
+    f32x16 acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    const int kw = min(it.ke, it.K / C::BK);  // end of the whole k tiles
+    if (it.kb < kw) {
+      const bool edge = (!AK && it.m0 + C::BM > it.M) || (!BK_ && it.n0 + C::BN > p.n);
+      if (edge) stream_loop<C, FORM, true>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
+      else stream_loop<C, FORM, false>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
+    }
+    if (kw < it.ke) {  // the rest of the contraction
+      const int k0 = (it.ke - 1) * C::BK;
+      A.tail(smem, k0, it.K);
+      B.tail(smem + SA, k0, it.K);
+      __syncthreads();
+      multiply<C, FORM>(acc, smem, smem + SA, wm, wn);
+      __syncthreads();
+    }
+    const Item done = it;
+    const bool more = next(it);
+    if (more) start(it);
+    const int lane = threadIdx.x & 63;
+    if (FORM == TN && !SPLIT && p.accumulate) {
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const int row = done.m0 + wm + 32 * i + (lane & 31);
+        if (row >= done.M) continue;
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int col = done.n0 + wn + 32 * j + 8 * g + 4 * (lane >> 5);
+            if (col >= p.n) continue;
+            const f32x4_t v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+            put4<O>(reinterpret_cast<O*>(p.c) + (int64_t)done.e * p.stride_c + (int64_t)row * p.ldc, col, p.n, v, true);
+          }
+      }
+    } else {
+      O* c;
+      int64_t ldc;
+      if constexpr (SPLIT) {
+        ldc = p.n;
+        c = reinterpret_cast<O*>(p.part) +
+            (FORM == TN ? ((int64_t)done.sp * p.groups + done.e) * done.M : (int64_t)done.sp * p.rows + done.r0) * ldc;
+      } else {
+        ldc = p.ldc;
+        c = reinterpret_cast<O*>(p.c) + (FORM == TN ? (int64_t)done.e * p.stride_c : (int64_t)done.r0 * ldc);
+      }
+      O* stage = reinterpret_cast<O*>(reinterpret_cast<char*>(smem) + wid * STAGE);
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+        store_rows<C, O>(acc[i], stage, c, ldc, done.m0 + wm + 32 * i, done.M, done.n0 + wn, p.n);
+    }
+    if (!more) return;
+    __syncthreads();  // the buffers are free
+  }
+}
+
 // C = (C +) the sum of the splits' partial results, in their order.  `rows`
 // rows of n in all; row r of C is at (r / m) stride_c + (r % m) ldc.
 template <typename O>
@@ -525,15 +828,17 @@ using FSmall = Cfg<float, 32, 128, 32, 32, 32, 2>;
 struct Choice {
   int cfg, bm, bn, bk;
 };
-Choice choose_product(int64_t rows, int n, int groups, int dtype) {
+// The small tile also has the sides under a 16-byte piece.
+Choice choose_product(int64_t rows, int k, int n, int groups, int dtype) {
   const int64_t avg = rows / groups;
-  if (avg <= 48) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
+  if (avg <= 48 || k < 8 || n < 8) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
   if (dtype == PMX_BF16 && avg >= 256 && n >= 256 && (rows / 256) * ((n + 255) / 256) >= kCU)
     return {2, 256, 256, 64};
   return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
 }
 Choice choose_outer(int64_t rows, int m, int n, int groups, int dtype) {
   const int64_t large = (int64_t)groups * ((m + 255) / 256) * ((n + 255) / 256);
+  if (m < 8 || n < 8) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
   if (dtype == PMX_BF16 && m >= 256 && n >= 256 && large >= kCU && rows / groups >= 64) return {2, 256, 256, 64};
   return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
 }
@@ -550,20 +855,27 @@ int64_t max_tiles_product(const Choice& c, int64_t rows, int n, int groups) {
   return (rows / c.bm + std::min<int64_t>(groups, rows)) * ((n + c.bn - 1) / c.bn);
 }
 
+#define PMX_LAUNCH(KERNEL)                                                                       \
+  if (p.splits > 1) {                                                                            \
+    hipLaunchKernelGGL((KERNEL<C, FORM, float, true>), grid, block, 0, s, p);                    \
+  } else if (p.out_dtype == PMX_F32) {                                                           \
+    hipLaunchKernelGGL((KERNEL<C, FORM, float, false>), grid, block, 0, s, p);                   \
+  } else {                                                                                       \
+    if constexpr (sizeof(typename C::E) == 2)                                                    \
+      hipLaunchKernelGGL((KERNEL<C, FORM, uint16_t, false>), grid, block, 0, s, p);              \
+    else return hipErrorInvalidValue;                                                            \
+  }
+
 template <class C, int FORM>
 hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s) {
   int64_t g = items < (int64_t)p.num_cu * C::MINB ? items : (int64_t)p.num_cu * C::MINB;
   g = (g + 7) / 8 * 8;
   if (g < 8) g = 8;
   const dim3 grid((unsigned)g), block(C::THREADS);
-  if (p.splits > 1) {
-    hipLaunchKernelGGL((grouped_kernel<C, FORM, float, true>), grid, block, 0, s, p);
-  } else if (p.out_dtype == PMX_F32) {
-    hipLaunchKernelGGL((grouped_kernel<C, FORM, float, false>), grid, block, 0, s, p);
+  if constexpr (C::BM == 32) {
+    PMX_LAUNCH(grouped_kernel)
   } else {
-    if constexpr (sizeof(typename C::E) == 2)
-      hipLaunchKernelGGL((grouped_kernel<C, FORM, uint16_t, false>), grid, block, 0, s, p);
-    else return hipErrorInvalidValue;
+    PMX_LAUNCH(grouped_tile_kernel)
   }
   return hipGetLastError();
 }
@@ -584,7 +896,7 @@ hipError_t launch_join(const GroupedParams& p, int64_t rows, int m, hipStream_t 
 }  // namespace
 
 int grouped_product_splits(int64_t rows, int k, int n, int groups, int dtype) {
-  const Choice c = choose_product(rows, n, groups, dtype);
+  const Choice c = choose_product(rows, k, n, groups, dtype);
   return splits_for(max_tiles_product(c, rows, n, groups), (k + c.bk - 1) / c.bk);
 }
 
@@ -596,7 +908,7 @@ int grouped_outer_splits(int64_t rows, int m, int n, int groups, int dtype) {
 
 hipError_t launch_grouped_product(const GroupedParams& p, hipStream_t s) {
   if (p.rows == 0) return hipSuccess;
-  const Choice c = choose_product(p.rows, p.n, p.groups, p.dtype);
+  const Choice c = choose_product(p.rows, p.k, p.n, p.groups, p.dtype);
   const int64_t items = max_tiles_product(c, p.rows, p.n, p.groups) * p.splits;
   hipError_t e;
   if (p.dtype == PMX_BF16) {
@@ -616,9 +928,11 @@ hipError_t launch_grouped_outer(const GroupedParams& p, hipStream_t s) {
       (int64_t)p.groups * ((p.m + c.bm - 1) / c.bm) * ((p.n + c.bn - 1) / c.bn) * p.splits;
   hipError_t e;
   if (p.dtype == PMX_BF16)
-    e = c.cfg == 1 ? launch_form<BMid, TN>(p, items, s) : launch_form<BLarge, TN>(p, items, s);
+    e = c.cfg == 0   ? launch_form<BSmall, TN>(p, items, s)
+        : c.cfg == 1 ? launch_form<BMid, TN>(p, items, s)
+                     : launch_form<BLarge, TN>(p, items, s);
   else
-    e = launch_form<FMid, TN>(p, items, s);
+    e = c.cfg == 0 ? launch_form<FSmall, TN>(p, items, s) : launch_form<FMid, TN>(p, items, s);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_join(p, (int64_t)p.groups * p.m, p.m, s);
 }

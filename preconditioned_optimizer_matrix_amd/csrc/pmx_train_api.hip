@@ -16,6 +16,7 @@ size_t index_size(pmx_itype t) { return t == PMX_I32 ? 4 : 8; }
 
 constexpr int64_t kMaxRows = 0x7fffffff;
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
+constexpr int64_t kMaxGroupedLd = (int64_t)1 << 22;  // offsets inside a tile are 32-bit
 
 // rows x cols with row distance ld >= cols; 0 rows: nothing.
 bool layout_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t elem) {
@@ -168,7 +169,7 @@ pmx_status pmx_grouped_product(pmx_handle h, const void* A, pmx_dtype dtype, int
   if (stride_b < 0 || stride_b > kMaxLd || (groups > 1 && stride_b > 0 && stride_b < (int64_t)(br - 1) * ldb + bc))
     return PMX_ERR_INVALID_VALUE;
   if (!offsets || (uintptr_t)offsets % index_size(itype) != 0) return PMX_ERR_INVALID_VALUE;
-  if (!grouped_items_ok(rows, n, groups)) return PMX_ERR_NOT_SUPPORTED;
+  if (!grouped_items_ok(rows, n, groups) || lda > kMaxGroupedLd || ldb > kMaxGroupedLd) return PMX_ERR_NOT_SUPPORTED;
   const Extent out = extent(C, rows, n, ldc, os);
   const size_t need = product_ws(rows, k, n, groups, dtype);
   const Extent in[] = {extent(A, rows, k, lda, es), extent_batch(B, groups, stride_b, br, bc, ldb, es),
@@ -223,7 +224,8 @@ pmx_status pmx_grouped_outer(pmx_handle h, const void* A, pmx_dtype dtype, int64
   if (stride_c < 0 || stride_c > kMaxLd || (groups > 1 && stride_c < (int64_t)(m - 1) * ldc + n))
     return PMX_ERR_INVALID_VALUE;
   if (!offsets || (uintptr_t)offsets % index_size(itype) != 0) return PMX_ERR_INVALID_VALUE;
-  if (!grouped_items_ok((int64_t)groups * m, n, groups)) return PMX_ERR_NOT_SUPPORTED;
+  if (!grouped_items_ok((int64_t)groups * m, n, groups) || lda > kMaxGroupedLd || ldb > kMaxGroupedLd)
+    return PMX_ERR_NOT_SUPPORTED;
   const Extent out = extent_batch(C, groups, stride_c, m, n, ldc, os);
   const size_t need = outer_ws(rows, m, n, groups, dtype);
   const Extent in[] = {extent(A, rows, m, lda, es), extent(B, rows, n, ldb, es),
