@@ -487,6 +487,79 @@ __device__ __forceinline__ void stream_loop(f32x16 (&acc)[C::FM][C::FN], typenam
   }
 }
 
+// The same for the large bf16 tile, whose 8 waves are two to a SIMD: the two
+// groups of four waves take turns.  While one runs the MFMAs of half a k tile
+// (16 a wave, all operands in registers), the other reads its next half's
+// fragments from LDS, puts its pieces of the next k tile there and issues its
+// global loads; a barrier ends each turn.  The matrix cores of a SIMD thus
+// have one wave's MFMAs to issue at any time, instead of both waves waiting for
+// LDS at the same place.
+template <class C, int FORM, bool EDGE>
+__device__ __forceinline__ void turns_loop(f32x16 (&acc)[C::FM][C::FN], typename C::E* smem,
+                                           const Stream<C, a_kc(FORM), C::BM>& A,
+                                           const Stream<C, b_kc(FORM), C::BN>& B,
+                                           u32x4_t (&va)[Stream<C, a_kc(FORM), C::BM>::N],
+                                           u32x4_t (&vb)[Stream<C, b_kc(FORM), C::BN>::N], int kb, int ke,
+                                           int wm, int wn, int group) {
+  constexpr int SA = C::size(a_kc(FORM), C::BM), ST = SA + C::size(b_kc(FORM), C::BN);
+  static_assert(C::WAVES == 8 && C::BK == 64 && sizeof(typename C::E) == 2, "two waves a SIMD");
+  A.template store<EDGE>(smem, va);
+  B.template store<EDGE>(smem + SA, vb);
+  {
+    const int k1 = min(kb + 1, ke - 1);  // past the last tile: the last one again
+    A.load(va, k1);
+    B.load(vb, k1);
+  }
+  __syncthreads();
+  // the second group is one turn behind
+  if (group) __builtin_amdgcn_s_barrier();
+  for (int kt = kb; kt < ke; ++kt) {
+    const int cur = (kt - kb) & 1;
+    const typename C::E* s = smem + cur * ST;
+    typename C::E* d = smem + (cur ^ 1) * ST;
+    const int k2 = min(kt + 2, ke - 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // this turn's operands; half of the next k tile on its way.  (The other
+      // buffer's last reader, the second group's turn before the first group's
+      // present one, is done; its next reader is four turns away.)
+      bf16x8 fa[2][C::FM], fb[2][C::FN];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) fa[t][i] = frag<C, a_kc(FORM), C::BM>(s, wm + 32 * i, 2 * h + t);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) fb[t][j] = frag<C, b_kc(FORM), C::BN>(s + SA, wn + 32 * j, 2 * h + t);
+      }
+      if (h == 0) {
+        A.template store<EDGE>(d, va);
+        A.load(va, k2);
+      } else {
+        B.template store<EDGE>(d + SA, vb);
+        B.load(vb, k2);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[t][j], fa[t][i], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (!group) __builtin_amdgcn_s_barrier();
+}
+
 // Four columns of a row of C at c (row length n): plain, or added to.
 template <typename O>
 __device__ __forceinline__ void put4(O* row, int c, int n, f32x4_t v, bool add) {
@@ -618,6 +691,9 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void grouped_kernel(GroupedPar
   }
 }
 
+template <class C>
+constexpr bool kTurns = C::WAVES == 8 && C::BK == 64 && sizeof(typename C::E) == 2;
+
 // Rows of C leave through LDS: a wave writes 32 rows of its tile, then stores
 // them as 16-byte pieces, whole 128-byte lines, instead of 8- and 16-byte ones
 // of 32 rows at a time.  `stage`: the wave's own 32 x (WN + 8 or 4) elements.
@@ -684,16 +760,18 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
   const int splits = SPLIT ? p.splits : 1;
   if constexpr (FORM != TN) zero_outside<C, O, SPLIT>(T, p, splits);
 
+  // Blocks are dealt to the 8 XCDs round-robin.  Each round of gridDim.x items
+  // gives every XCD a contiguous share, neighbouring tiles for its L2, and the
+  // rounds spread long and short groups over all of them.
   const int items = T.tile[p.groups] * splits;
-  const int per = (items + 7) >> 3, x = blockIdx.x & 7, step = gridDim.x >> 3;
-  int jx = blockIdx.x >> 3;
+  int q0 = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   struct Item {
     int e, r0, m0, n0, K, M, kb, ke, sp;
   };
   auto next = [&](Item& it) -> bool {
-    const int q = x * per + jx;
-    if (jx >= per || q >= items) return false;
-    jx += step;
+    if (q0 >= items) return false;
+    const int q = q0;
+    q0 += gridDim.x;
     const int t = SPLIT ? q / splits : q;
     it.sp = SPLIT ? q - t * splits : 0;
     it.e = group_of(T, p.groups, t);
@@ -739,8 +817,14 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
     const int kw = min(it.ke, it.K / C::BK);  // end of the whole k tiles
     if (it.kb < kw) {
       const bool edge = (!AK && it.m0 + C::BM > it.M) || (!BK_ && it.n0 + C::BN > p.n);
-      if (edge) stream_loop<C, FORM, true>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
-      else stream_loop<C, FORM, false>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
+      if constexpr (kTurns<C>) {
+        const int group = __builtin_amdgcn_readfirstlane(wid >> 2);
+        if (edge) turns_loop<C, FORM, true>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn, group);
+        else turns_loop<C, FORM, false>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn, group);
+      } else {
+        if (edge) stream_loop<C, FORM, true>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
+        else stream_loop<C, FORM, false>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
+      }
     }
     if (kw < it.ke) {  // the rest of the contraction
       const int k0 = (it.ke - 1) * C::BK;
@@ -817,7 +901,10 @@ __global__ __launch_bounds__(256) void grouped_join_kernel(GroupedParams p, int6
 }
 
 // ------------------------------------------------------------ launchers
-using BLarge = Cfg<uint16_t, 256, 256, 64, 128, 64, 1>;  // 8 waves
+#ifndef LCFG
+#define LCFG 256, 256, 64, 128, 64, 1
+#endif
+using BLarge = Cfg<uint16_t, LCFG>;  // 8 waves
 using BMid = Cfg<uint16_t, 128, 128, 64, 64, 64, 2>;     // 4 waves
 using BSmall = Cfg<uint16_t, 32, 128, 64, 32, 32, 2>;    // 4 waves
 using FMid = Cfg<float, 128, 128, 16, 64, 64, 2>;
@@ -833,13 +920,13 @@ Choice choose_product(int64_t rows, int k, int n, int groups, int dtype) {
   const int64_t avg = rows / groups;
   if (avg <= 48 || k < 8 || n < 8) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
   if (dtype == PMX_BF16 && avg >= 256 && n >= 256 && (rows / 256) * ((n + 255) / 256) >= kCU)
-    return {2, 256, 256, 64};
+    return {2, BLarge::BM, BLarge::BN, BLarge::BK};
   return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
 }
 Choice choose_outer(int64_t rows, int m, int n, int groups, int dtype) {
   const int64_t large = (int64_t)groups * ((m + 255) / 256) * ((n + 255) / 256);
   if (m < 8 || n < 8) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
-  if (dtype == PMX_BF16 && m >= 256 && n >= 256 && large >= kCU && rows / groups >= 64) return {2, 256, 256, 64};
+  if (dtype == PMX_BF16 && m >= 256 && n >= 256 && large >= kCU && rows / groups >= 64) return {2, BLarge::BM, BLarge::BN, BLarge::BK};
   return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
 }
 
