@@ -697,14 +697,14 @@ constexpr bool kTurns = C::WAVES == 8 && C::BK == 64 && sizeof(typename C::E) ==
 // Rows of C leave through LDS: a wave writes 32 rows of its tile, then stores
 // them as 16-byte pieces, whole 128-byte lines, instead of 8- and 16-byte ones
 // of 32 rows at a time.  `stage`: the wave's own 32 x (WN + 8 or 4) elements.
-template <class C, typename O>
-__device__ __forceinline__ void store_rows(const f32x16 (&acc)[C::FN], O* stage, O* c, int64_t ldc, int row0,
+template <int WN, typename O>
+__device__ __forceinline__ void store_rows(const f32x16* acc, O* stage, O* c, int64_t ldc, int row0,
                                            int rows, int col0, int cols) {
-  constexpr int PIT = C::WN + 16 / (int)sizeof(O), V = 16 / (int)sizeof(O), LPR = C::WN / V;  // lanes a row
+  constexpr int PIT = WN + 16 / (int)sizeof(O), V = 16 / (int)sizeof(O), LPR = WN / V;  // lanes a row
   const int lane = threadIdx.x & 63;
   O* w = stage + (lane & 31) * PIT + 4 * (lane >> 5);
 #pragma unroll
-  for (int j = 0; j < C::FN; ++j)
+  for (int j = 0; j < WN / 32; ++j)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const f32x4_t v = {acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
@@ -867,10 +867,274 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
       O* stage = reinterpret_cast<O*>(reinterpret_cast<char*>(smem) + wid * STAGE);
 #pragma unroll
       for (int i = 0; i < C::FM; ++i)
-        store_rows<C, O>(acc[i], stage, c, ldc, done.m0 + wm + 32 * i, done.M, done.n0 + wn, p.n);
+        store_rows<C::WN, O>(acc[i], stage, c, ldc, done.m0 + wm + 32 * i, done.M, done.n0 + wn, p.n);
     }
     if (!more) return;
     __syncthreads();  // the buffers are free
+  }
+}
+
+// ------------------------------------------------------------ outer form, large tile, aligned operands
+// 256 x 256 tiles of the outer form, 8 waves of 128 x 64, k tiles of 32 rows that
+// go from memory to a ring of 4 LDS stages without passing through registers (a
+// load instruction writes its wave's 64 x 16 bytes in lane order: two k rows of
+// 512 bytes).  The turns are those of turns_loop, one k tile each; a stage is
+// refilled three k tiles ahead, six turns before it is read.  LDS is not
+// padded; the 32-byte block c of k row k lies at c ^ 2 (k & 3), which puts the
+// four k rows and two blocks of a transpose read's 32 lanes on distinct banks.
+// (The product forms have operands with 64 bytes a row and k tile; loaded like
+// this, by half lines, they were slower than through registers: 333 against 292
+// us forward, 378 against 328 us input gradient, 32768 rows, 32 experts of 4096 x
+// 1024.  The outer form takes 357 us, 393 through registers.)
+constexpr int kStage = 32 * 1024, kStageB = 16 * 1024;  // bytes of a stage, of A's part
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+struct Dma {
+  const uint16_t* base;
+  int64_t step;
+  uint32_t off[2];  // of this lane's piece, for the wave's two instructions
+  // columns r0 .. of `limit` (a multiple of 8), read past the end from the last 8
+  __device__ __forceinline__ void init(const uint16_t* b, int64_t ld, int r0, int limit, int wid) {
+    base = b;
+    step = 32 * ld;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      off[j] = (uint32_t)(row(j, wid) * (int)ld + min(r0 + column(j, wid), limit - 8));
+  }
+  // k row and column of this lane's piece of instruction j
+  static __device__ __forceinline__ int row(int j, int wid) { return 2 * (2 * wid + j) + ((threadIdx.x & 63) >> 5); }
+  static __device__ __forceinline__ int column(int j, int wid) {
+    const int pc = threadIdx.x & 31;
+    return (((pc >> 1) ^ (2 * (row(j, wid) & 3))) * 2 + (pc & 1)) * 8;
+  }
+  __device__ __forceinline__ void issue(char* part, int kt, int wid) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      __builtin_amdgcn_global_load_lds((const void*)(base + kt * step + off[j]), (lds_ptr)(part + (2 * wid + j) * 1024),
+                                       16, 0, 0);
+  }
+};
+
+// A wave's fragments of one k tile of a stage, F of 32 rows and two 16-wide
+// steps.  The reads are written out, with their wait in the same block: the
+// compiler takes any LDS read it sees to depend on the loads to LDS under way
+// and would wait for all of them.
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+__device__ __forceinline__ bf16x8 join(i16x4 lo, i16x4 hi) {
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int F>
+struct DmaFrag {
+  uint32_t at[F];  // of each fragment in step 0
+  __device__ __forceinline__ DmaFrag(int row) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+      at[i] = (8 * (g >> 1) + (j >> 2)) * 512 + ((((row >> 4) + 2 * i + (g & 1)) ^ (2 * (j >> 2))) * 32) + 8 * (j & 3);
+  }
+};
+
+// Two fragments of both steps; k rows 0 .. 3 and 4 .. 7 of a step are 2048 bytes
+// apart, the steps 8192.
+__device__ __forceinline__ void read_frags_tr(bf16x8 (&f)[2][2], uint32_t a0, uint32_t a1) {
+  i16x4 x[8];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n\t"
+      "ds_read_b64_tr_b16 %1, %8 offset:2048\n\t"
+      "ds_read_b64_tr_b16 %2, %9\n\t"
+      "ds_read_b64_tr_b16 %3, %9 offset:2048\n\t"
+      "ds_read_b64_tr_b16 %4, %8 offset:8192\n\t"
+      "ds_read_b64_tr_b16 %5, %8 offset:10240\n\t"
+      "ds_read_b64_tr_b16 %6, %9 offset:8192\n\t"
+      "ds_read_b64_tr_b16 %7, %9 offset:10240\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+      : "v"(a0), "v"(a1)
+      : "memory");
+  f[0][0] = join(x[0], x[1]);
+  f[0][1] = join(x[2], x[3]);
+  f[1][0] = join(x[4], x[5]);
+  f[1][1] = join(x[6], x[7]);
+}
+__device__ __forceinline__ void read_frags(bf16x8 (&f)[2][2], const DmaFrag<2>& F, uint32_t p) {
+  read_frags_tr(f, p + F.at[0], p + F.at[1]);
+}
+__device__ __forceinline__ void read_frags(bf16x8 (&f)[2][4], const DmaFrag<4>& F, uint32_t p) {
+  bf16x8 g[2][2];
+  read_frags_tr(g, p + F.at[0], p + F.at[1]);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    f[s][0] = g[s][0];
+    f[s][1] = g[s][1];
+  }
+  read_frags_tr(g, p + F.at[2], p + F.at[3]);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    f[s][2] = g[s][0];
+    f[s][3] = g[s][1];
+  }
+}
+
+template <typename O>
+__global__ __launch_bounds__(512, 2) void grouped_dma_kernel(GroupedParams p) {
+  __shared__ __attribute__((aligned(1024))) char smem[4 * kStage];
+  __shared__ Table T;
+  const int tiles_n = (p.n + 255) / 256;
+  const int tiles_m = (p.m + 255) / 256;
+  build_table(T, p, 256, tiles_n, tiles_m * tiles_n);
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = wid >> 2;
+  const int wm = (wid >> 2) * 128, wn = (wid & 3) * 64;
+  const int items = T.tile[p.groups];
+  int q0 = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  struct Item {
+    int e, r0, m0, n0, K;
+  };
+  auto next = [&](Item& it) -> bool {
+    if (q0 >= items) return false;
+    const int q = q0;
+    q0 += gridDim.x;
+    it.e = __builtin_amdgcn_readfirstlane(group_of(T, p.groups, q));
+    it.r0 = __builtin_amdgcn_readfirstlane(T.begin[it.e]);
+    it.K = __builtin_amdgcn_readfirstlane(T.begin[it.e + 1]) - it.r0;
+    int tm, tn;
+    tile_of(q - it.e * tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+    it.m0 = tm * 256;
+    it.n0 = tn * 256;
+    return true;
+  };
+  Dma A, B;
+  const uint32_t lds0 = lds_address(smem);
+  const DmaFrag<4> FA(wm);
+  const DmaFrag<2> FB(wn);
+  // k tile kt into its stage (past the item's last whole k tile: the last one again)
+  auto issue = [&](const Item& it, int kt) {
+    char* st = smem + (kt & 3) * kStage;
+    const int k = min(kt, it.K / 32 - 1);
+    A.issue(st, k, wid);
+    B.issue(st + kStageB, k, wid);
+  };
+  // the item's operands and its first two k tiles on the way (stages 0 and 1)
+  auto start = [&](const Item& it) {
+    A.init(reinterpret_cast<const uint16_t*>(p.a) + (int64_t)it.r0 * p.lda, p.lda, it.m0, p.m, wid);
+    B.init(reinterpret_cast<const uint16_t*>(p.b) + (int64_t)it.r0 * p.ldb, p.ldb, it.n0, p.n, wid);
+    if (it.K >= 32) {
+      issue(it, 0);
+      issue(it, 1);
+    }
+  };
+  Item it;
+  if (!next(it)) return;
+  start(it);
+  for (;;) {
+    f32x16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    const int kw = it.K / 32;
+    if (kw > 0) {
+      issue(it, 2);
+      // k tile 0 has landed for this wave (the 8 loads of k tiles 1 and 2 may be
+      // under way), then for every wave
+      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      if (group) __builtin_amdgcn_s_barrier();  // the second group is one turn behind
+      for (int kt = 0; kt < kw; ++kt) {
+        const uint32_t st = lds0 + (kt & 3) * kStage;
+        issue(it, kt + 3);  // the stage of k tile kt - 1, whose last reader (the second group) is done
+        bf16x8 fa[2][4], fb[2][2];
+        read_frags(fb, FB, st + kStageB);
+        read_frags(fa, FA, st);
+        // k tile kt + 1 has landed before the first group's next turn: the second
+        // group waits for its loads here, the first after its MFMAs
+        if (group) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[s][j], fa[s][i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (!group) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (!group) __builtin_amdgcn_s_barrier();
+      // the loads past the last k tile have landed before the stages are used again
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+    }
+    if (kw * 32 < it.K) {  // the rest of the contraction, zeros past its end
+      const int k0 = kw * 32;
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        const bool isa = j < 2;
+        const int k = Dma::row(j & 1, wid), c = Dma::column(j & 1, wid);
+        u32x4_t v = {0u, 0u, 0u, 0u};
+        if (k0 + k < it.K)
+          v = load_win((isa ? A.base : B.base) + (int64_t)(k0 + k) * (isa ? p.lda : p.ldb), (isa ? it.m0 : it.n0) + c,
+                       isa ? p.m : p.n);
+        *reinterpret_cast<u32x4_t*>(smem + (isa ? 0 : kStageB) + (2 * wid + (j & 1)) * 1024 + 16 * (threadIdx.x & 63)) = v;
+      }
+      __syncthreads();
+      bf16x8 fa[2][4], fb[2][2];
+      read_frags(fb, FB, lds0 + kStageB);
+      read_frags(fa, FA, lds0);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[s][j], fa[s][i], acc[i][j], 0, 0, 0);
+      __syncthreads();
+    }
+    const Item done = it;
+    const bool more = next(it);
+    if (more) start(it);  // stages 0 and 1; the results leave through the others
+    const int lane = threadIdx.x & 63;
+    if (p.accumulate) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = done.m0 + wm + 32 * i + (lane & 31);
+        if (row >= p.m) continue;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int col = done.n0 + wn + 32 * j + 8 * g + 4 * (lane >> 5);
+            if (col >= p.n) continue;
+            const f32x4_t v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+            put4<O>(reinterpret_cast<O*>(p.c) + (int64_t)done.e * p.stride_c + (int64_t)row * p.ldc, col, p.n, v, true);
+          }
+      }
+    } else {
+      O* c = reinterpret_cast<O*>(p.c) + (int64_t)done.e * p.stride_c;
+      // 128 bytes of a row at a time: 64 columns of bf16, 32 of fp32
+      constexpr int COLS = 128 / (int)sizeof(O), PASS = COLS / 32;
+      constexpr int STAGE = 32 * (COLS + 16 / (int)sizeof(O)) * (int)sizeof(O);
+      static_assert(8 * STAGE <= 2 * kStage, "the waves' stages fit two of the ring's");
+      O* stage = reinterpret_cast<O*>(smem + 2 * kStage + wid * STAGE);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; j += PASS)
+          store_rows<COLS, O>(&acc[i][j], stage, c, p.ldc, done.m0 + wm + 32 * i, p.m, done.n0 + wn + 32 * j, p.n);
+    }
+    if (!more) return;
+    __syncthreads();  // the stages are free
   }
 }
 
@@ -901,10 +1165,7 @@ __global__ __launch_bounds__(256) void grouped_join_kernel(GroupedParams p, int6
 }
 
 // ------------------------------------------------------------ launchers
-#ifndef LCFG
-#define LCFG 256, 256, 64, 128, 64, 1
-#endif
-using BLarge = Cfg<uint16_t, LCFG>;  // 8 waves
+using BLarge = Cfg<uint16_t, 256, 256, 64, 128, 64, 1>;  // 8 waves
 using BMid = Cfg<uint16_t, 128, 128, 64, 64, 64, 2>;     // 4 waves
 using BSmall = Cfg<uint16_t, 32, 128, 64, 32, 32, 2>;    // 4 waves
 using FMid = Cfg<float, 128, 128, 16, 64, 64, 2>;
@@ -920,13 +1181,13 @@ Choice choose_product(int64_t rows, int k, int n, int groups, int dtype) {
   const int64_t avg = rows / groups;
   if (avg <= 48 || k < 8 || n < 8) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
   if (dtype == PMX_BF16 && avg >= 256 && n >= 256 && (rows / 256) * ((n + 255) / 256) >= kCU)
-    return {2, BLarge::BM, BLarge::BN, BLarge::BK};
+    return {2, 256, 256, 64};
   return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
 }
 Choice choose_outer(int64_t rows, int m, int n, int groups, int dtype) {
   const int64_t large = (int64_t)groups * ((m + 255) / 256) * ((n + 255) / 256);
   if (m < 8 || n < 8) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
-  if (dtype == PMX_BF16 && m >= 256 && n >= 256 && large >= kCU && rows / groups >= 64) return {2, BLarge::BM, BLarge::BN, BLarge::BK};
+  if (dtype == PMX_BF16 && m >= 256 && n >= 256 && large >= kCU && rows / groups >= 64) return {2, 256, 256, 64};
   return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
 }
 
@@ -942,9 +1203,23 @@ int64_t max_tiles_product(const Choice& c, int64_t rows, int n, int groups) {
   return (rows / c.bm + std::min<int64_t>(groups, rows)) * ((n + c.bn - 1) / c.bn);
 }
 
+// Every 16-byte piece of the outer form's operands aligned and whole: what the
+// direct loads to LDS take.
+bool dma_ok(const GroupedParams& p) {
+  return !(((uintptr_t)p.a | (uintptr_t)p.b) & 15) && p.lda % 8 == 0 && p.ldb % 8 == 0 && p.m % 8 == 0 && p.n % 8 == 0;
+}
+
+hipError_t launch_dma(const GroupedParams& p, dim3 grid, hipStream_t s) {
+  if (p.out_dtype == PMX_F32) hipLaunchKernelGGL(grouped_dma_kernel<float>, grid, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL(grouped_dma_kernel<uint16_t>, grid, dim3(512), 0, s, p);
+  return hipGetLastError();
+}
+
 #define PMX_LAUNCH(KERNEL)                                                                       \
-  if (p.splits > 1) {                                                                            \
-    hipLaunchKernelGGL((KERNEL<C, FORM, float, true>), grid, block, 0, s, p);                    \
+  if (p.splits > 1) { /* never with the large tile: there are tiles enough */                    \
+    if constexpr (C::BM != 256)                                                                  \
+      hipLaunchKernelGGL((KERNEL<C, FORM, float, true>), grid, block, 0, s, p);                  \
+    else return hipErrorInvalidValue;                                                            \
   } else if (p.out_dtype == PMX_F32) {                                                           \
     hipLaunchKernelGGL((KERNEL<C, FORM, float, false>), grid, block, 0, s, p);                   \
   } else {                                                                                       \
@@ -959,6 +1234,9 @@ hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s) {
   g = (g + 7) / 8 * 8;
   if (g < 8) g = 8;
   const dim3 grid((unsigned)g), block(C::THREADS);
+  if constexpr (C::BM == 256 && FORM == TN) {
+    if (dma_ok(p)) return launch_dma(p, grid, s);
+  }
   if constexpr (C::BM == 32) {
     PMX_LAUNCH(grouped_kernel)
   } else {

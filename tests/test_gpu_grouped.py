@@ -344,3 +344,24 @@ def test_refusals(env):
     assert args(p(small) + 4, big) == pmx.ERR_WORKSPACE
     torch.cuda.synchronize()
     assert (C == 5).all()  # nothing was enqueued
+
+
+@pytest.mark.parametrize("rows,groups,m,n", [(5000, 40, 520, 768), (3000, 33, 512, 1032), (2600, 65, 256, 512)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_outer_of_large_aligned_tiles(env, rows, groups, m, n, out, accumulate):
+    """Large tiles of aligned operands: groups of every length modulo the k tile,
+    sides that end inside a tile, both result types."""
+    torch, pmx, dev = env
+    print("large aligned outer", rows, groups, m, n, out, accumulate, flush=True)
+    off = _offsets(rows, groups, 91)
+    A, An = _make(torch, dev, torch.bfloat16, (rows, m), 21)
+    B, Bn = _make(torch, dev, torch.bfloat16, (rows, n), 22)
+    C, C0 = _make(torch, dev, {"bf16": torch.bfloat16, "f32": torch.float32}[out], (groups, m, n), 23)
+    pmx.grouped_outer(A, B, torch.from_numpy(off).to(dev), out=C, accumulate=accumulate)
+    Cn = C.double().cpu().numpy()
+    for e in range(groups):
+        a, b = off[e], off[e + 1]
+        ref = An[a:b].T @ Bn[a:b] + (C0[e] if accumulate else 0.0)
+        s = np.abs(An[a:b]).T @ np.abs(Bn[a:b]) + (np.abs(C0[e]) if accumulate else 0.0)
+        assert (np.abs(Cn[e] - ref) <= _bound(ref, s, b - a + 1, out == "bf16")).all(), e
