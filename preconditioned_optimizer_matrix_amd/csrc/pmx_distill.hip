@@ -29,6 +29,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -INFINITY;
+constexpr int kFewRows = 128;  // at most so many rows are cut over several blocks
 
 // exponentials per element: one (a single temperature is in play), two, or
 // one and squarings
@@ -255,13 +256,13 @@ __device__ __forceinline__ void teacher_sums(Listed& L, const DistillParams& p, 
 
 // The row's loss from its sums.
 template <int EX>
-__device__ __forceinline__ float row_loss(const DistillParams& p, const Listed& L, const Expo<EX>& ex,
+__device__ __forceinline__ float row_loss(const DistillParams& p, bool label, float z_label, const Expo<EX>& ex,
                                           const float (&v)[5]) {
   float loss = 0.f;
   if (v[3] != 0.f) {  // a row of nothing but -inf has none
     if (p.mix != 0.f && v[0] != 0.f)
       loss += p.mix * p.tau * p.tau * ((v[1] - v[2]) / v[0] - logf(v[0]) + logf(v[3]));
-    if (p.mix != 1.f && L.id[p.top] >= 0) loss += (1.f - p.mix) * (logf(v[4]) - (L.z[p.top] - ex.m));
+    if (p.mix != 1.f && label) loss += (1.f - p.mix) * (logf(v[4]) - (z_label - ex.m));
   }
   return loss;
 }
@@ -437,7 +438,7 @@ __global__ __launch_bounds__(NT, waves_for(NC)) void distill_row_kernel(DistillP
     if (more) f.fetch(p, tn);
     block_sum<NT>(sum, red);
     if (tid == 0) {
-      p.rows_loss[t] = row_loss(p, L, ex, sum);
+      p.rows_loss[t] = row_loss(p, L.id[p.top] >= 0, L.z[p.top], ex, sum);
       if (p.stats) {
         p.stats[3 * t] = ex.m;
         p.stats[3 * t + 1] = inverse(sum[3]);
@@ -510,7 +511,7 @@ __global__ __launch_bounds__(1024) void distill_long_kernel(DistillParams p) {
     if (EX == EXP_ONE) sum[4] = sum[3];
     block_sum<NT>(sum, red);
     if (tid == 0) {
-      p.rows_loss[t] = row_loss(p, L, ex, sum);
+      p.rows_loss[t] = row_loss(p, L.id[p.top] >= 0, L.z[p.top], ex, sum);
       if (p.stats) {
         p.stats[3 * t] = ex.m;
         p.stats[3 * t + 1] = inverse(sum[3]);
@@ -537,13 +538,13 @@ __global__ __launch_bounds__(1024) void distill_long_kernel(DistillParams p) {
   }
 }
 
-// Few rows: block (x, y) has slab x of gridDim.x of row y.  A slab is a range
+// Block (x, y) has slab x of row y.  A slab is a range
 // of whole chunks; the row's edges belong to slab 0.
 template <typename T>
 struct Slab {
   int c0, c1, edges;
-  __device__ __forceinline__ Slab(const Row<T>& r) {
-    const int per = (r.chunks + (int)gridDim.x - 1) / (int)gridDim.x;
+  __device__ __forceinline__ Slab(const Row<T>& r, int slabs) {
+    const int per = (r.chunks + slabs - 1) / slabs;
     c0 = min((int)blockIdx.x * per, r.chunks);
     c1 = min(c0 + per, r.chunks);
     edges = blockIdx.x == 0 ? r.edges : 0;
@@ -566,7 +567,7 @@ __global__ __launch_bounds__(256) void distill_part_kernel(DistillParams p) {
   if (weight_of(p, t) == 0.f) return;
   const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
   const Row<T> r(z, p.vocab);
-  const Slab<T> b(r);
+  const Slab<T> b(r, (int)gridDim.x);
   if (blockIdx.x == 0) {
     Fetched<T, NT> f;
     f.fetch(p, t);
@@ -607,105 +608,157 @@ __global__ __launch_bounds__(256) void distill_part_kernel(DistillParams p) {
   }
 }
 
-// The row's maximum and sums from its slabs' (in their order), or from the
-// saved statistics.
+// The row's maximum and sums from its slabs' (at most 64, one a lane), in every
+// wave.
 template <int EX>
 __device__ __forceinline__ float join_parts(const DistillParams& p, int64_t t, float& st, float& s1) {
-  const float* q = p.part + t * p.splits * 3;
-  float m = kNegInf;
-  for (int i = 0; i < p.splits; ++i) m = fmaxf(m, q[3 * i]);
+  const int lane = threadIdx.x & 63;
+  const float* q = p.part + (t * p.splits + min(lane, p.splits - 1)) * 3;
+  const bool in = lane < p.splits;
+  const float mi = in ? q[0] : kNegInf, ti = in ? q[1] : 0.f, oi = in ? q[2] : 0.f;
+  float m = wave_max(mi);
   if (m == kNegInf) m = 0.f;
   const Expo<EX> ex(p, m);
-  st = s1 = 0.f;
-  for (int i = 0; i < p.splits; ++i) {
-    // a slab of nothing but -inf has zero sums (NaN ones stay NaN)
-    const float d = (q[3 * i] == kNegInf ? 0.f : q[3 * i]) - m;
-    const float ft = __builtin_amdgcn_exp2f(d * ex.a);
-    const float f1 = EX == EXP_ONE ? ft : __builtin_amdgcn_exp2f(d * kLog2e);
-    if (q[3 * i + 1] != 0.f) st += q[3 * i + 1] * ft;
-    if (q[3 * i + 2] != 0.f) s1 += q[3 * i + 2] * f1;
-  }
+  // a slab of nothing but -inf has zero sums (NaN ones stay NaN)
+  const float d = (mi == kNegInf ? 0.f : mi) - m;
+  const float ft = __builtin_amdgcn_exp2f(d * ex.a);
+  const float f1 = EX == EXP_ONE ? ft : __builtin_amdgcn_exp2f(d * kLog2e);
+  st = wave_sum(ti != 0.f ? ti * ft : 0.f);
+  s1 = wave_sum(oi != 0.f ? oi * f1 : 0.f);
   return m;
 }
 
-// One slab of one row at a time: the gradient from the saved statistics
-// (JOIN false), or the whole rest of a row cut over blocks (JOIN; slab 0 also
-// writes the loss; without dz there is only slab 0).
+// Losses, statistics and the total of few rows from the slabs' sums: one block,
+// a wave a row.
+template <int EX>
+__device__ void few_rows_loss(const DistillParams& p) {
+  __shared__ double part[kFewRows];
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const float rt = 1.f / p.tau;
+  for (int64_t t = wid; t < p.rows; t += waves) {
+    const float w = weight_of(p, t);
+    float m = 0.f, st = 0.f, s1 = 0.f, loss = 0.f;
+    if (w != 0.f) {
+      const float* z = saved_of(p, t);
+      m = join_parts<EX>(p, t, st, s1);
+      const Expo<EX> ex(p, m);
+      auto entry = [&](int i) {  // teacher logit / tau, -inf outside the vocabulary
+        const int64_t id = load_index(p.ids, t * p.ld_ids + i, p.ids64), o = t * p.ld_teacher + i;
+        if (id < 0 || id >= p.vocab) return kNegInf;
+        return rt * (p.teacher_dtype == PMX_F32
+                         ? reinterpret_cast<const float*>(p.teacher)[o]
+                         : Elem<uint16_t>::load(reinterpret_cast<const uint16_t*>(p.teacher) + o));
+      };
+      float am = kNegInf;
+      for (int i = lane; i < p.top; i += 64) am = fmaxf(am, entry(i));
+      am = wave_max(am);
+      if (am == kNegInf) am = 0.f;
+      float sum[5] = {0.f, 0.f, 0.f, st, s1};
+      for (int i = lane; i < p.top; i += 64) {
+        const float a = entry(i) - am, e = __builtin_amdgcn_exp2f(a * kLog2e);
+        sum[0] += e;
+        if (e != 0.f) {
+          sum[1] += e * a;
+          sum[2] += e * (z[i] - m) * ex.rt;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) sum[i] = wave_sum(sum[i]);
+      const int64_t y = p.labels ? load_index(p.labels, t, p.labels64) : -1;
+      loss = row_loss(p, y >= 0 && y < p.vocab, z[p.top], ex, sum);
+    }
+    if (lane == 0) {
+      p.rows_loss[t] = loss;
+      if (p.stats) {
+        p.stats[3 * t] = m;
+        p.stats[3 * t + 1] = inverse(st);
+        p.stats[3 * t + 2] = inverse(s1);
+      }
+      part[t] = w != 0.f ? (p.weights ? (double)w : 1.0 / (double)p.rows) * (double)loss : 0.0;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    for (int t = 0; t < (int)p.rows; ++t) s += part[t];
+    *p.total = (float)s;
+  }
+}
+
+// One slab of one row at a time: the gradient from the saved statistics, or
+// (JOIN) from the slabs' sums of distill_part_kernel; then one more block has
+// the losses.  A thread's first four chunks are loaded before the teacher's
+// list is worked through.
 template <typename T, int EX, bool JOIN>
-__global__ __launch_bounds__(256) void distill_grad_kernel(DistillParams p) {
-  constexpr int VEC = Elem<T>::VEC, NT = 256;
+__global__ __launch_bounds__(256) void distill_grad_kernel(DistillParams p, int slabs) {
+  constexpr int VEC = Elem<T>::VEC, NT = 256, NC = 4;
   __shared__ Listed L;
   __shared__ float red[5][16];
+  if (JOIN && (int)blockIdx.x == slabs) {
+    if (blockIdx.y == 0) few_rows_loss<EX>(p);
+    return;
+  }
   const int n = p.vocab, tid = threadIdx.x;
   for (int64_t t = blockIdx.y; t < p.rows; t += gridDim.y) {
     const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
     T* dz = reinterpret_cast<T*>(p.dz) + t * p.lddz;
     const Row<T> r(z, n);
-    const Slab<T> b(r);
+    const Slab<T> b(r, slabs);
     const float wt = weight_of(p, t);
-    const bool first = JOIN && blockIdx.x == 0 && tid == 0;
     if (wt == 0.f) {
-      if (first) {
-        p.rows_loss[t] = 0.f;
-        if (p.stats) p.stats[3 * t] = p.stats[3 * t + 1] = p.stats[3 * t + 2] = 0.f;
-      }
-      if (p.dz) {
-        const float zero[VEC] = {};
-        for (int c = b.c0 + tid; c < b.c1; c += NT) store_chunk<T>(dz + r.head, c, zero);
-        if (tid < b.edges) Elem<T>::store(dz + r.edge(tid), 0.f);
-      }
+      const float zero[VEC] = {};
+      for (int c = b.c0 + tid; c < b.c1; c += NT) store_chunk<T>(dz + r.head, c, zero);
+      if (tid < b.edges) Elem<T>::store(dz + r.edge(tid), 0.f);
       continue;
     }
     Fetched<T, NT> f;
     f.fetch(p, t, JOIN ? saved_of(p, t) : nullptr);
-    float m, inv_t, inv_1, sum[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
-    float st = 0.f, s1 = 0.f;
+    u32x4_t u[NC];
+    auto load = [&](int c0) {
+#pragma unroll
+      for (int k = 0; k < NC; ++k)
+        if (c0 + k * NT < b.c1) u[k] = load_chunk<T>(z + r.head, c0 + k * NT);
+    };
+    load(b.c0 + tid);
+    const float edge = tid < b.edges ? Elem<T>::load(z + r.edge(tid)) : 0.f;
+    float m, inv_t, inv_1;
     if (JOIN) {
-      m = join_parts<EX>(p, t, st, s1);
-      inv_t = inverse(st);
-      inv_1 = inverse(s1);
+      m = join_parts<EX>(p, t, inv_t, inv_1);
+      inv_t = inverse(inv_t);
+      inv_1 = inverse(inv_1);
     } else {
       m = p.stats[3 * t];
       inv_t = p.stats[3 * t + 1];
       inv_1 = p.stats[3 * t + 2];
     }
     const Expo<EX> ex(p, m);
-    float am[1];
+    float am[1], sum[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
     am[0] = f.put(L, p);
     block_max<NT>(am, red);
     teacher_sums<NT>(L, p, ex, am[0] == kNegInf ? 0.f : am[0], sum);
-    block_sum<NT>(sum, red);
-    if (first) {
-      sum[3] = st;
-      sum[4] = s1;
-      p.rows_loss[t] = row_loss(p, L, ex, sum);
-      if (p.stats) {
-        p.stats[3 * t] = m;
-        p.stats[3 * t + 1] = inv_t;
-        p.stats[3 * t + 2] = inv_1;
-      }
-    }
-    if (p.dz) {
-      const float w = wt * (p.upstream ? *p.upstream : 1.f);
-      const Scales s = grad_scales<EX>(p, w, inv_t, inv_1, sum[0], L.id[p.top] >= 0);
-#pragma unroll 4
-      for (int c = b.c0 + tid; c < b.c1; c += NT) {
-        const u32x4_t u = load_chunk<T>(z + r.head, c);
-        float x[VEC];
+    float sum_e[1] = {sum[0]};
+    block_sum<NT>(sum_e, red);
+    const float w = wt * (p.upstream ? *p.upstream : 1.f);
+    const Scales s = grad_scales<EX>(p, w, inv_t, inv_1, sum_e[0], L.id[p.top] >= 0);
+    for (int c0 = b.c0 + tid;;) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) x[j] = grad_of(Elem<T>::get(u, j), ex, s);
-        store_chunk<T>(dz + r.head, c, x);
-      }
-      if (tid < b.edges) {
-        const int i = r.edge(tid);
-        Elem<T>::store(dz + i, grad_of(Elem<T>::load(z + i), ex, s));
-      }
-      __syncthreads();
-      if (b.c1 > b.c0) fix_listed<T, NT>(L, p, dz, ex, s, r.head + b.c0 * VEC, r.head + b.c1 * VEC);
-      if (b.edges) {
-        fix_listed<T, NT>(L, p, dz, ex, s, 0, r.head);
-        fix_listed<T, NT>(L, p, dz, ex, s, r.head + r.chunks * VEC, n);
-      }
+      for (int k = 0; k < NC; ++k)
+        if (c0 + k * NT < b.c1) {
+          float x[VEC];
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) x[j] = grad_of(Elem<T>::get(u[k], j), ex, s);
+          store_chunk<T>(dz + r.head, c0 + k * NT, x);
+        }
+      c0 += NC * NT;
+      if (c0 >= b.c1) break;
+      load(c0);
+    }
+    if (tid < b.edges) Elem<T>::store(dz + r.edge(tid), grad_of(edge, ex, s));
+    __syncthreads();
+    if (b.c1 > b.c0) fix_listed<T, NT>(L, p, dz, ex, s, r.head + b.c0 * VEC, r.head + b.c1 * VEC);
+    if (b.edges) {
+      fix_listed<T, NT>(L, p, dz, ex, s, 0, r.head);
+      fix_listed<T, NT>(L, p, dz, ex, s, r.head + r.chunks * VEC, n);
     }
     __syncthreads();
   }
@@ -733,8 +786,18 @@ __global__ __launch_bounds__(1024) void distill_total_kernel(DistillParams p) {
 // blocks a compute unit, slabs of at least 1024 chunks.
 int splits_of(int64_t rows, int vocab, int dtype) {
   const int chunks = vocab / (dtype == PMX_F32 ? 4 : 8);
-  if (rows > 128 || rows == 0 || chunks < 2048) return 1;
+  if (rows > kFewRows || rows == 0 || chunks < 2048) return 1;
   return (int)std::min<int64_t>(std::min<int64_t>(512 / rows, chunks / 1024), 64);
+}
+
+// Slabs of a row in distill_grad_kernel: enough for about four blocks a compute
+// unit in all, of at least 1024 chunks (four a thread).  A block works through
+// the row's list before it writes, so more blocks than run at once cost more
+// than they gain (1023 rows of 32003 bf16: 4 slabs 29.2 us, 3 26.5 us).
+int grad_slabs(const DistillParams& p) {
+  const int64_t chunks = p.vocab / (p.dtype == PMX_F32 ? 4 : 8);
+  const int64_t want = (4 * (int64_t)p.num_cu + p.rows - 1) / p.rows;
+  return (int)std::max<int64_t>(1, std::min(want, (chunks + 1023) / 1024));
 }
 
 template <typename T, int EX, bool GRAD>
@@ -744,8 +807,9 @@ hipError_t launch_rows(const DistillParams& p, hipStream_t s) {
     hipLaunchKernelGGL((distill_part_kernel<T, EX>), dim3(p.splits, (unsigned)p.rows), dim3(256), 0, s, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((distill_grad_kernel<T, EX, true>), dim3(GRAD ? p.splits : 1, (unsigned)p.rows),
-                       dim3(256), 0, s, p);
+    const int slabs = GRAD ? grad_slabs(p) : 0;
+    hipLaunchKernelGGL((distill_grad_kernel<T, EX, true>), dim3(slabs + 1, GRAD ? (unsigned)p.rows : 1), dim3(256), 0,
+                       s, p, slabs);
     return hipGetLastError();
   }
   // the smallest block whose registers hold the row's chunks; a row shorter
@@ -786,15 +850,14 @@ hipError_t launch_loss_t(const DistillParams& p, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_grad_t(const DistillParams& p, hipStream_t s) {
-  // slabs of at least 1024 chunks (four a thread); in place one block owns the
-  // row: it reads the listed logits before it overwrites them
-  int slabs = p.vocab / Elem<T>::VEC / 1024;
-  if (slabs < 1 || p.z == p.dz) slabs = 1;
+  // in place one block owns the row: it reads the listed logits before it
+  // overwrites them
+  const int slabs = p.z == p.dz ? 1 : grad_slabs(p);
   const dim3 grid((unsigned)slabs, (unsigned)(p.rows < 65535 ? p.rows : 65535));
   switch (exps_of(p)) {
-    case EXP_ONE: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_ONE, false>), grid, dim3(256), 0, s, p); break;
-    case EXP_TWO: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_TWO, false>), grid, dim3(256), 0, s, p); break;
-    default: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_SQ, false>), grid, dim3(256), 0, s, p); break;
+    case EXP_ONE: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_ONE, false>), grid, dim3(256), 0, s, p, slabs); break;
+    case EXP_TWO: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_TWO, false>), grid, dim3(256), 0, s, p, slabs); break;
+    default: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_SQ, false>), grid, dim3(256), 0, s, p, slabs); break;
   }
   return hipGetLastError();
 }
@@ -813,7 +876,7 @@ hipError_t launch_distill_loss(DistillParams p, hipStream_t s) {
     if (p.dtype == PMX_F32) e = p.dz ? launch_loss_t<float, true>(p, s) : launch_loss_t<float, false>(p, s);
     else e = p.dz ? launch_loss_t<uint16_t, true>(p, s) : launch_loss_t<uint16_t, false>(p, s);
   }
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || p.splits > 1) return e;  // (with the losses of rows cut over blocks)
   hipLaunchKernelGGL(distill_total_kernel, dim3(1), dim3(1024), 0, s, p);
   return hipGetLastError();
 }

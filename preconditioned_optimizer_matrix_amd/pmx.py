@@ -251,10 +251,6 @@ def _stream_of(device):
     return _vp(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _raw_stream(device):
-    return _torch().cuda.current_stream(device).cuda_stream
-
-
 def _dtype_code(t):
     torch = _torch()
     if t.dtype == torch.float32:
@@ -585,31 +581,60 @@ def trace_collect(device=None):
 # themselves go (device, type, shape agreement, unit column stride); sizes,
 # strides, alignment and overlap are checked by the library.
 
-def _index_code(t):
+_codes = {}
+
+
+def _fill_codes():
     torch = _torch()
-    if t.dtype == torch.int32:
-        return I32
-    if t.dtype == torch.int64:
-        return I64
-    raise TypeError("index tensors are int32 or int64, not %s" % t.dtype)
+    _codes.update({torch.float32: F32, torch.bfloat16: BF16, torch.int32: I32, torch.int64: I64})
+    _codes["stream"] = torch._C._cuda_getCurrentRawStream
+    _codes["empty"] = torch.empty
+    _codes["f32"] = torch.float32
 
 
-def _same_device(first, *rest):
-    if not first.is_cuda:
+def _elem_code(t):
+    c = _codes.get(t.dtype)
+    if c is None or not t.is_floating_point():
+        raise TypeError("unsupported dtype %s" % t.dtype)
+    return c
+
+
+def _index_code(t):
+    c = _codes.get(t.dtype)
+    if c is None or t.is_floating_point():
+        raise TypeError("index tensors are int32 or int64, not %s" % t.dtype)
+    return c
+
+
+def _on(first, *rest):
+    """The GPU all the tensors live on."""
+    if not _codes:
+        _fill_codes()
+    d = first.get_device()
+    if d < 0:
         raise ValueError("tensors live on the GPU")
     for t in rest:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != d:
             raise ValueError("tensors on different devices")
+    return d
+
+
+def _call(d):
+    """Handle and current stream of GPU d."""
+    h = _handles.get(d)
+    return (h if h is not None else handle(d)), _codes["stream"](d)
 
 
 def _rows_of(t, what):
     """(rows, columns, row distance) of a 2-D tensor with unit column stride."""
-    if t.dim() != 2:
+    s = t.shape
+    if len(s) != 2:
         raise ValueError("%s must be 2-D" % what)
-    r, c = t.shape
-    if c > 1 and t.stride(1) != 1:
+    r, c = s
+    ld, one = t.stride()
+    if one != 1 and c > 1:
         raise ValueError("%s must have unit column stride" % what)
-    return r, c, (t.stride(0) if r > 1 else max(c, 1))
+    return r, c, (ld if r > 1 else max(c, 1))
 
 
 def _vector(t, what):
@@ -620,13 +645,16 @@ def _vector(t, what):
 
 def _matrices_of(t, what):
     """(batch, rows, columns, row distance, matrix distance) of a 3-D tensor."""
-    if t.dim() != 3:
+    s = t.shape
+    if len(s) != 3:
         raise ValueError("%s must be 3-D" % what)
-    b, r, c = t.shape
-    if c > 1 and t.stride(2) != 1:
+    b, r, c = s
+    sb, ld, one = t.stride()
+    if one != 1 and c > 1:
         raise ValueError("%s must have unit column stride" % what)
-    ld = t.stride(1) if r > 1 else max(c, 1)
-    return b, r, c, ld, (t.stride(0) if b > 1 else r * ld)
+    if r <= 1:
+        ld = max(c, 1)
+    return b, r, c, ld, (sb if b > 1 else r * ld)
 
 
 _sizes = {}
@@ -639,9 +667,14 @@ def _need(query, *args):
     if n is None:
         sz = _sz()
         check(getattr(lib, query)(*args, ctypes.byref(sz)), query)
-        if len(_sizes) >= 4096:
-            _sizes.clear()
-        n = _sizes[key] = sz.value
+        n = _keep_size(key, sz.value)
+    return n
+
+
+def _keep_size(key, n):
+    if len(_sizes) >= 4096:
+        _sizes.clear()
+    _sizes[key] = n
     return n
 
 
@@ -650,7 +683,7 @@ def _ws_for(need, ws, device):
         return None, 0
     if ws is None or ws.numel() < need:
         ws = workspace(need, device)
-    return ws.data_ptr(), ws.numel()
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def grouped_product(A, B, offsets, trans_b=False, out=None, out_dtype=None, ws=None):
@@ -658,8 +691,7 @@ def grouped_product(A, B, offsets, trans_b=False, out=None, out_dtype=None, ws=N
     offsets[e + 1] of group e; rows in no group are zeros.  A (rows x k), B
     (groups x k x n, or groups x n x k with trans_b) bf16 or fp32, offsets
     (groups + 1) int32 or int64 on the device; C in A's type or fp32."""
-    torch = _torch()
-    _same_device(A, B, offsets, out)
+    d = _on(A, B, offsets, out)
     rows, k, lda = _rows_of(A, "A")
     groups, br, bc, ldb, sb = _matrices_of(B, "B")
     n = br if trans_b else bc
@@ -670,17 +702,18 @@ def grouped_product(A, B, offsets, trans_b=False, out=None, out_dtype=None, ws=N
     if _vector(offsets, "offsets") != groups + 1:
         raise ValueError("one offset per group and one more")
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype or A.dtype, device=A.device)
+        out = _codes["empty"]((rows, n), dtype=out_dtype or A.dtype, device=A.device)
     elif tuple(out.shape) != (rows, n) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out has another shape or type")
     _, _, ldc = _rows_of(out, "out")
-    dt = _dtype_code(A)
+    dt = _elem_code(A)
     need = _need("pmx_grouped_product_workspace_size", rows, k, n, groups, dt)
     wp, wn = _ws_for(need, ws, A.device)
+    h, st = _call(d)
     check(lib.pmx_grouped_product(
-        handle(A.device.index), A.data_ptr(), dt, rows, k, lda, B.data_ptr(), n, ldb, sb,
+        h, A.data_ptr(), dt, rows, k, lda, B.data_ptr(), n, ldb, sb,
         1 if trans_b else 0, offsets.data_ptr(), _index_code(offsets), groups, out.data_ptr(),
-        _dtype_code(out), ldc, wp, wn, _raw_stream(A.device)), "grouped_product")
+        _elem_code(out), ldc, wp, wn, st), "grouped_product")
     return out
 
 
@@ -688,8 +721,7 @@ def grouped_outer(A, B, offsets, out=None, out_dtype=None, accumulate=False, ws=
     """C[e] = A_e^T B_e over the rows of group e (accumulate: C[e] += ...):
     with A = dY and B = X the gradient of out x in weights.  A (rows x m), B
     (rows x n); C (groups x m x n) in A's type or fp32."""
-    torch = _torch()
-    _same_device(A, B, offsets, out)
+    d = _on(A, B, offsets, out)
     rows, m, lda = _rows_of(A, "A")
     rb, n, ldb = _rows_of(B, "B")
     if rb != rows:
@@ -702,31 +734,31 @@ def grouped_outer(A, B, offsets, out=None, out_dtype=None, accumulate=False, ws=
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((groups, m, n), dtype=out_dtype or A.dtype, device=A.device)
+        out = _codes["empty"]((groups, m, n), dtype=out_dtype or A.dtype, device=A.device)
     elif tuple(out.shape) != (groups, m, n) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out has another shape or type")
     _, _, _, ldc, sc = _matrices_of(out, "out")
-    dt = _dtype_code(A)
+    dt = _elem_code(A)
     need = _need("pmx_grouped_outer_workspace_size", rows, m, n, groups, dt)
     wp, wn = _ws_for(need, ws, A.device)
+    h, st = _call(d)
     check(lib.pmx_grouped_outer(
-        handle(A.device.index), A.data_ptr(), dt, rows, m, lda, B.data_ptr(), n, ldb,
-        offsets.data_ptr(), _index_code(offsets), groups, out.data_ptr(), _dtype_code(out), ldc, sc,
-        1 if accumulate else 0, wp, wn, _raw_stream(A.device)), "grouped_outer")
+        h, A.data_ptr(), dt, rows, m, lda, B.data_ptr(), n, ldb,
+        offsets.data_ptr(), _index_code(offsets), groups, out.data_ptr(), _elem_code(out), ldc, sc,
+        1 if accumulate else 0, wp, wn, st), "grouped_outer")
     return out
 
 
 def embedding(W, ids, scale=1.0, out=None):
     """scale W[ids] for a table W (vocab x dim) and ids of any shape; an id
     outside the table gives zeros."""
-    torch = _torch()
-    _same_device(W, ids, out)
+    d = _on(W, ids, out)
     vocab, dim, ldt = _rows_of(W, "W")
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
     shape = tuple(ids.shape) + (dim,)
     if out is None:
-        out = torch.empty(shape, dtype=W.dtype, device=W.device)
+        out = _codes["empty"](shape, dtype=W.dtype, device=W.device)
         ldy = dim
     else:
         if tuple(out.shape) != shape or out.dtype != W.dtype:
@@ -737,9 +769,10 @@ def embedding(W, ids, scale=1.0, out=None):
             ldy = dim
         else:
             raise ValueError("out must be contiguous")
-    check(lib.pmx_embedding(handle(W.device.index), W.data_ptr(), _dtype_code(W), vocab, dim, ldt,
+    h, st = _call(d)
+    check(lib.pmx_embedding(h, W.data_ptr(), _elem_code(W), vocab, dim, ldt,
                             ids.data_ptr(), _index_code(ids), ids.numel(), scale, out.data_ptr(),
-                            ldy, _raw_stream(W.device)), "embedding")
+                            ldy, st), "embedding")
     return out
 
 
@@ -749,8 +782,7 @@ def embedding_grad(dY, ids, vocab, scale=1.0, padding_idx=-1, out=None, out_dtyp
     of id v, zeros elsewhere (accumulate: added to out instead).  Tokens of
     padding_idx, or of ids outside the table, are left out.  dY is tokens x dim
     (or ids' shape x dim, contiguous); dW in dY's type or out_dtype."""
-    torch = _torch()
-    _same_device(dY, ids, out)
+    d = _on(dY, ids, out)
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
     if tuple(dY.shape[:-1]) != tuple(ids.shape):
@@ -764,52 +796,49 @@ def embedding_grad(dY, ids, vocab, scale=1.0, padding_idx=-1, out=None, out_dtyp
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((vocab, dim), dtype=out_dtype or dY.dtype, device=dY.device)
+        out = _codes["empty"]((vocab, dim), dtype=out_dtype or dY.dtype, device=dY.device)
     elif tuple(out.shape) != (vocab, dim) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out has another shape or type")
     _, _, lddw = _rows_of(out, "out")
     need = _need("pmx_embedding_grad_workspace_size", tokens, vocab, dim)
     wp, wn = _ws_for(need, ws, dY.device)
+    h, st = _call(d)
     check(lib.pmx_embedding_grad(
-        handle(dY.device.index), dY.data_ptr(), _dtype_code(dY), tokens, dim, lddy, ids.data_ptr(),
-        _index_code(ids), vocab, scale, padding_idx, out.data_ptr(), _dtype_code(out), lddw,
-        1 if accumulate else 0, wp, wn, _raw_stream(dY.device)), "embedding_grad")
+        h, dY.data_ptr(), _elem_code(dY), tokens, dim, lddy, ids.data_ptr(),
+        _index_code(ids), vocab, scale, padding_idx, out.data_ptr(), _elem_code(out), lddw,
+        1 if accumulate else 0, wp, wn, st), "embedding_grad")
     return out
 
 
 def _distill_problem(Z, teacher_ids, teacher, tau, mix, labels, weights):
-    torch = _torch()
-    _same_device(Z, teacher_ids, teacher, labels, weights)
+    _on(Z, teacher_ids, teacher, labels, weights)
     rows, vocab, ldz = _rows_of(Z, "Z")
-    q = DistillProblem()
-    q.struct_version = 1
-    q.dtype = _dtype_code(Z)
-    q.rows, q.vocab, q.z, q.ldz = rows, vocab, Z.data_ptr(), ldz
+    top = ids = ld_ids = te = ld_te = it = td = 0
     if teacher_ids is not None:
-        ri, top, q.ld_ids = _rows_of(teacher_ids, "teacher_ids")
-        rt, tt, q.ld_teacher = _rows_of(teacher, "teacher")
-        if (ri, rt) != (rows, rows) or tt != top:
+        ri, top, ld_ids = _rows_of(teacher_ids, "teacher_ids")
+        rt, tt, ld_te = _rows_of(teacher, "teacher")
+        if ri != rows or rt != rows or tt != top:
             raise ValueError("teacher_ids and teacher are rows x top")
-        q.top, q.teacher_ids, q.teacher = top, teacher_ids.data_ptr(), teacher.data_ptr()
-        q.ids_type, q.teacher_dtype = _index_code(teacher_ids), _dtype_code(teacher)
+        ids, te = teacher_ids.data_ptr(), teacher.data_ptr()
+        it, td = _index_code(teacher_ids), _elem_code(teacher)
+    lab = lt = wp = None
     if labels is not None:
         if _vector(labels, "labels") != rows:
             raise ValueError("one label per row")
-        q.labels, q.labels_type = labels.data_ptr(), _index_code(labels)
+        lab, lt = labels.data_ptr(), _index_code(labels)
     if weights is not None:
         if _vector(weights, "weights") != rows:
             raise ValueError("one weight per row")
-        if weights.dtype != torch.float32:
+        if weights.dtype != _codes["f32"]:
             raise TypeError("weights are fp32")
-        q.weights = weights.data_ptr()
-    q.tau, q.mix = tau, mix
-    return q
+        wp = weights.data_ptr()
+    return DistillProblem(1, _elem_code(Z), rows, vocab, top, Z.data_ptr(), ldz, ids, ld_ids, te, ld_te,
+                          lab, wp, it, lt or 0, td, tau, mix, 0)
 
 
 def _dz_of(Z, out):
     if out is None:
-        torch = _torch()
-        out = torch.empty(Z.shape, dtype=Z.dtype, device=Z.device)
+        out = _codes["empty"](Z.shape, dtype=Z.dtype, device=Z.device)
     elif out.shape != Z.shape or out.dtype != Z.dtype or out.device != Z.device:
         raise ValueError("out has another shape, type or device")
     return out, _rows_of(out, "out")[2]
@@ -823,23 +852,28 @@ def distill_loss(Z, teacher_ids, teacher, tau=1.0, mix=1.0, labels=None, weights
     default to 1 / rows.  Returns (total, rows, stats, dZ): the weighted sum,
     every row's loss, what distill_grad needs, and with grad (or out, which
     may be Z itself) the gradient of total."""
-    torch = _torch()
     q = _distill_problem(Z, teacher_ids, teacher, tau, mix, labels, weights)
-    res = torch.empty(q.rows + 1, dtype=torch.float32, device=Z.device)
-    dz, lddz, stats = None, max(q.vocab, 1), None
+    empty, dev, n = _codes["empty"], Z.device, q.rows
+    f32 = _codes["f32"]
+    total, rows = empty((), dtype=f32, device=dev), empty((n,), dtype=f32, device=dev)
     if grad or out is not None:
         dz, lddz = _dz_of(Z, out)
+        stats, sp, zp = None, None, dz.data_ptr()
     else:
-        stats = torch.empty((q.rows, 3), dtype=torch.float32, device=Z.device)
-    sz = _sz()
-    check(lib.pmx_distill_workspace_size(ctypes.byref(q), ctypes.byref(sz)), "distill_workspace_size")
-    wp, wn = _ws_for(sz.value, ws, Z.device)
-    base = res.data_ptr()
-    check(lib.pmx_distill_loss(
-        handle(Z.device.index), ctypes.byref(q), base + 4, base,
-        stats.data_ptr() if stats is not None else None, dz.data_ptr() if dz is not None else None,
-        lddz, wp, wn, _raw_stream(Z.device)), "distill_loss")
-    return res[0], res[1:], stats, dz
+        stats = empty((n, 3), dtype=f32, device=dev)
+        dz, lddz, sp, zp = None, 0, stats.data_ptr(), None
+    ref = ctypes.byref(q)
+    key = ("distill", n, q.vocab, q.top, q.dtype)
+    need = _sizes.get(key)
+    if need is None:
+        sz = _sz()
+        check(lib.pmx_distill_workspace_size(ref, ctypes.byref(sz)), "distill_workspace_size")
+        need = _keep_size(key, sz.value)
+    wp, wn = _ws_for(need, ws, dev)
+    h, st = _call(Z.get_device())
+    check(lib.pmx_distill_loss(h, ref, rows.data_ptr(), total.data_ptr(), sp, zp, lddz, wp, wn, st),
+          "distill_loss")
+    return total, rows, stats, dz
 
 
 def distill_grad(Z, teacher_ids, teacher, stats, upstream=None, tau=1.0, mix=1.0, labels=None,
@@ -849,14 +883,15 @@ def distill_grad(Z, teacher_ids, teacher, stats, upstream=None, tau=1.0, mix=1.0
     may be Z itself."""
     torch = _torch()
     q = _distill_problem(Z, teacher_ids, teacher, tau, mix, labels, weights)
-    _same_device(Z, stats, upstream)
+    _on(Z, stats, upstream)
     if tuple(stats.shape) != (q.rows, 3) or stats.dtype != torch.float32 or not stats.is_contiguous():
         raise ValueError("stats are those distill_loss returned")
     if upstream is not None and (upstream.numel() != 1 or upstream.dtype != torch.float32):
         raise ValueError("upstream is one fp32 value")
     dz, lddz = _dz_of(Z, out)
+    h, st = _call(Z.get_device())
     check(lib.pmx_distill_grad(
-        handle(Z.device.index), ctypes.byref(q), stats.data_ptr(),
+        h, ctypes.byref(q), stats.data_ptr(),
         upstream.data_ptr() if upstream is not None else None, dz.data_ptr(), lddz,
-        _raw_stream(Z.device)), "distill_grad")
+        st), "distill_grad")
     return dz
