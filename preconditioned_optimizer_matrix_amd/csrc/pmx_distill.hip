@@ -31,9 +31,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -INFINITY;
 constexpr int kFewRows = 128;  // at most so many rows are cut over several blocks
 
-// exponentials per element: one (a single temperature is in play), two, or
-// one and squarings
-enum Exps : int { EXP_ONE = 0, EXP_TWO = 1, EXP_SQ = 2 };
+// exponentials per element: one (a single temperature is in play), two, or one
+// and 1, 2 or 3 squarings
+enum Exps : int { EXP_ONE = 0, EXP_TWO = 1, EXP_SQ1 = 2, EXP_SQ2 = 3, EXP_SQ3 = 4 };
 
 typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
 
@@ -107,24 +107,20 @@ __device__ __forceinline__ void store_chunk(T* base, uint32_t i, const float (&x
 template <int EX>
 struct Expo {
   float m, a, rt;
-  int sq;  // EXP_SQ: tau = 2^sq
   __device__ __forceinline__ Expo(const DistillParams& p, float m_) {
     m = m_;
     // the only temperature of EXP_ONE: tau, or 1 where only the label counts
     rt = 1.f / (EX == EXP_ONE && p.mix == 0.f ? 1.f : p.tau);
     a = kLog2e * rt;
-    sq = p.tau == 2.f ? 1 : p.tau == 4.f ? 2 : 3;
   }
   __device__ __forceinline__ void operator()(float z, float& et, float& e1) const {
     const float d = z - m;
     et = __builtin_amdgcn_exp2f(d * a);
     if (EX == EXP_ONE) e1 = et;
     if (EX == EXP_TWO) e1 = __builtin_amdgcn_exp2f(d * kLog2e);
-    if (EX == EXP_SQ) {
-      e1 = et * et;
-      if (sq > 1) e1 *= e1;
-      if (sq > 2) e1 *= e1;
-    }
+    if (EX >= EXP_SQ1) e1 = et * et;
+    if (EX >= EXP_SQ2) e1 *= e1;
+    if (EX >= EXP_SQ3) e1 *= e1;
   }
 };
 
@@ -295,6 +291,23 @@ __device__ __forceinline__ float grad_of(float z, const Expo<EX>& ex, const Scal
   return EX == EXP_ONE ? s.gt * et : s.gt * et + s.g1 * e1;
 }
 
+template <typename T, int EX>
+__device__ __forceinline__ void add_chunk(const Expo<EX>& ex, const u32x4_t& u, float& st, float& s1) {
+#pragma unroll
+  for (int j = 0; j < Elem<T>::VEC; ++j) {
+    float et, e1;
+    ex(Elem<T>::get(u, j), et, e1);
+    st += et;
+    if (EX != EXP_ONE) s1 += e1;
+  }
+}
+template <typename T, int EX>
+__device__ __forceinline__ void grad_chunk(const Expo<EX>& ex, const Scales& s, const u32x4_t& u,
+                                           float (&x)[Elem<T>::VEC]) {
+#pragma unroll
+  for (int j = 0; j < Elem<T>::VEC; ++j) x[j] = grad_of(Elem<T>::get(u, j), ex, s);
+}
+
 // Corrections of the gradient at the listed columns [lo, hi), over dense
 // values already written by this block.  Every entry naming the same column
 // writes the same value.
@@ -416,13 +429,7 @@ __global__ __launch_bounds__(NT, waves_for(NC)) void distill_row_kernel(DistillP
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float et, e1;
-        ex(Elem<T>::get(v[c], j), et, e1);
-        sum[3] += et;
-        if (EX != EXP_ONE) sum[4] += e1;
-      }
+      add_chunk<T>(ex, v[c], sum[3], sum[4]);
       if (GRAD) {
         stay_packed(v[c]);
       } else {
@@ -452,8 +459,7 @@ __global__ __launch_bounds__(NT, waves_for(NC)) void distill_row_kernel(DistillP
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float x[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) x[j] = grad_of(Elem<T>::get(v[c], j), ex, s);
+        grad_chunk<T>(ex, s, v[c], x);
         if (tid < r.chunks - c * NT) store_chunk<T>(dz + r.head + c * NT * VEC, tid, x);
         load_one(body, last, c);
       }
@@ -500,13 +506,7 @@ __global__ __launch_bounds__(1024) void distill_long_kernel(DistillParams p) {
 #pragma unroll 4
     for (int c = tid; c < r.chunks; c += NT) {
       const u32x4_t u = load_chunk<T>(body, c);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float et, e1;
-        ex(Elem<T>::get(u, j), et, e1);
-        sum[3] += et;
-        if (EX != EXP_ONE) sum[4] += e1;
-      }
+      add_chunk<T>(ex, u, sum[3], sum[4]);
     }
     if (EX == EXP_ONE) sum[4] = sum[3];
     block_sum<NT>(sum, red);
@@ -526,8 +526,7 @@ __global__ __launch_bounds__(1024) void distill_long_kernel(DistillParams p) {
       for (int c = tid; c < r.chunks; c += NT) {
         const u32x4_t u = load_chunk<T>(body, c);
         float x[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) x[j] = grad_of(Elem<T>::get(u, j), ex, s);
+        grad_chunk<T>(ex, s, u, x);
         store_chunk<T>(dz + r.head, c, x);
       }
       if (tid < r.edges) Elem<T>::store(dz + r.edge(tid), grad_of(edge, ex, s));
@@ -591,14 +590,9 @@ __global__ __launch_bounds__(256) void distill_part_kernel(DistillParams p) {
 #pragma unroll 4
   for (int c = b.c0 + tid; c < b.c1; c += NT) {
     const u32x4_t u = load_chunk<T>(z + r.head, c);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      float et, e1;
-      ex(Elem<T>::get(u, j), et, e1);
-      sum[0] += et;
-      sum[1] += e1;
-    }
+    add_chunk<T>(ex, u, sum[0], sum[1]);
   }
+  if (EX == EXP_ONE) sum[1] = sum[0];
   block_sum<NT>(sum, red);
   if (tid == 0) {
     float* q = p.part + (t * gridDim.x + blockIdx.x) * 3;
@@ -745,8 +739,7 @@ __global__ __launch_bounds__(256) void distill_grad_kernel(DistillParams p, int 
       for (int k = 0; k < NC; ++k)
         if (c0 + k * NT < b.c1) {
           float x[VEC];
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) x[j] = grad_of(Elem<T>::get(u[k], j), ex, s);
+          grad_chunk<T>(ex, s, u[k], x);
           store_chunk<T>(dz + r.head, c0 + k * NT, x);
         }
       c0 += NC * NT;
@@ -835,8 +828,7 @@ hipError_t launch_rows(const DistillParams& p, hipStream_t s) {
 
 int exps_of(const DistillParams& p) {
   if (p.mix == 0.f || p.mix == 1.f || p.tau == 1.f) return EXP_ONE;
-  if (p.tau == 2.f || p.tau == 4.f || p.tau == 8.f) return EXP_SQ;
-  return EXP_TWO;
+  return p.tau == 2.f ? EXP_SQ1 : p.tau == 4.f ? EXP_SQ2 : p.tau == 8.f ? EXP_SQ3 : EXP_TWO;
 }
 
 template <typename T, bool GRAD>
@@ -844,7 +836,9 @@ hipError_t launch_loss_t(const DistillParams& p, hipStream_t s) {
   switch (exps_of(p)) {
     case EXP_ONE: return launch_rows<T, EXP_ONE, GRAD>(p, s);
     case EXP_TWO: return launch_rows<T, EXP_TWO, GRAD>(p, s);
-    default: return launch_rows<T, EXP_SQ, GRAD>(p, s);
+    case EXP_SQ1: return launch_rows<T, EXP_SQ1, GRAD>(p, s);
+    case EXP_SQ2: return launch_rows<T, EXP_SQ2, GRAD>(p, s);
+    default: return launch_rows<T, EXP_SQ3, GRAD>(p, s);
   }
 }
 
@@ -854,11 +848,16 @@ hipError_t launch_grad_t(const DistillParams& p, hipStream_t s) {
   // overwrites them
   const int slabs = p.z == p.dz ? 1 : grad_slabs(p);
   const dim3 grid((unsigned)slabs, (unsigned)(p.rows < 65535 ? p.rows : 65535));
+#define PMX_GRAD(EX) \
+  case EX: hipLaunchKernelGGL((distill_grad_kernel<T, EX, false>), grid, dim3(256), 0, s, p, slabs); break;
   switch (exps_of(p)) {
-    case EXP_ONE: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_ONE, false>), grid, dim3(256), 0, s, p, slabs); break;
-    case EXP_TWO: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_TWO, false>), grid, dim3(256), 0, s, p, slabs); break;
-    default: hipLaunchKernelGGL((distill_grad_kernel<T, EXP_SQ, false>), grid, dim3(256), 0, s, p, slabs); break;
+    PMX_GRAD(EXP_ONE)
+    PMX_GRAD(EXP_TWO)
+    PMX_GRAD(EXP_SQ1)
+    PMX_GRAD(EXP_SQ2)
+    PMX_GRAD(EXP_SQ3)
   }
+#undef PMX_GRAD
   return hipGetLastError();
 }
 
