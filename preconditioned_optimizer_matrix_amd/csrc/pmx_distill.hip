@@ -337,20 +337,24 @@ __device__ __forceinline__ void clear_row(T* row, int n) {
   for (int i = threadIdx.x; i < r.edges; i += NT) Elem<T>::store(row + r.edge(i), 0.f);
 }
 
-// The next row from t on (stride `step`) that counts; ignored rows on the way
-// get their zeros.  p.rows: none.
-template <typename T, int NT, bool GRAD>
-__device__ __forceinline__ int64_t next_live(const DistillParams& p, int64_t t, int64_t step) {
-  for (; t < p.rows; t += step) {
+// The next row from t on that counts; ignored rows on the way get their zeros.
+// p.rows: none.  `after(t)` is the row that follows t for this block.
+template <typename T, int NT, bool GRAD, typename F>
+__device__ __forceinline__ int64_t next_live(const DistillParams& p, int64_t t, F&& after) {
+  while (t < p.rows) {
     if (weight_of(p, t) != 0.f) return t;
     if (threadIdx.x == 0) {
       p.rows_loss[t] = 0.f;
       if (p.stats) p.stats[3 * t] = p.stats[3 * t + 1] = p.stats[3 * t + 2] = 0.f;
     }
     if (GRAD) clear_row<T, NT>(reinterpret_cast<T*>(p.dz) + t * p.lddz, p.vocab);
+    t = after(t);
   }
   return p.rows;
 }
+
+// First row of the rows that blocks claim (the first gridDim.x are dealt out).
+__global__ void distill_claim_kernel(uint32_t* next, uint32_t first) { *next = first; }
 
 // Waves a SIMD for NC chunks a thread: registers for the row (4 NC) and 50
 // to 60 more.
@@ -386,7 +390,22 @@ __global__ __launch_bounds__(NT, waves_for(NC)) void distill_row_kernel(DistillP
   auto load_edge = [&](const T* z, const Row<T>& r) {
     edge = tid < r.edges ? Elem<T>::load(z + r.edge(tid)) : kNegInf;
   };
-  int64_t t = next_live<T, NT, GRAD>(p, blockIdx.x, gridDim.x);
+  // CLAIM: after its first row a block takes the next one nobody has taken, so
+  // that blocks with many ignored rows do not finish early (with 10% of 8192
+  // rows ignored, the block with most rows to do had 32 where the mean is 28.8)
+  constexpr bool CLAIM = NT == 1024;
+  __shared__ uint32_t claimed;
+  auto after = [&](int64_t t) -> int64_t {
+    if constexpr (CLAIM) {
+      __syncthreads();
+      if (threadIdx.x == 0) claimed = atomicAdd(p.next_row, 1u);
+      __syncthreads();
+      return claimed;
+    } else {
+      return t + gridDim.x;
+    }
+  };
+  int64_t t = next_live<T, NT, GRAD>(p, blockIdx.x, after);
   if (t >= p.rows) return;
   {
     const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
@@ -398,6 +417,7 @@ __global__ __launch_bounds__(NT, waves_for(NC)) void distill_row_kernel(DistillP
   }
   for (;;) {
     const Row<T> r(reinterpret_cast<const T*>(p.z) + t * p.ldz, n);
+    if (CLAIM && tid == 0) claimed = atomicAdd(p.next_row, 1u);  // read after block_max
     float mx[2];
     mx[0] = edge;
     mx[1] = f.put(L, p);
@@ -412,7 +432,7 @@ __global__ __launch_bounds__(NT, waves_for(NC)) void distill_row_kernel(DistillP
     block_max<NT>(mx, red);
     const float am = mx[1] == kNegInf ? 0.f : mx[1];
     const Expo<EX> ex(p, mx[0] == kNegInf ? 0.f : mx[0]);  // -inf - 0 stays -inf
-    const int64_t tn = next_live<T, NT, GRAD>(p, t + gridDim.x, gridDim.x);
+    const int64_t tn = next_live<T, NT, GRAD>(p, CLAIM ? (int64_t)claimed : t + gridDim.x, after);
     // without a next row every lane loads this row's first chunk again
     const bool more = tn < p.rows;
     const T* zn = reinterpret_cast<const T*>(p.z) + (more ? tn : t) * p.ldz;
@@ -481,7 +501,8 @@ __global__ __launch_bounds__(1024) void distill_long_kernel(DistillParams p) {
   __shared__ Listed L;
   __shared__ float red[5][16];
   const int n = p.vocab, tid = threadIdx.x;
-  for (int64_t t = blockIdx.x; (t = next_live<T, NT, GRAD>(p, t, gridDim.x)) < p.rows; t += gridDim.x) {
+  auto after = [](int64_t t) -> int64_t { return t + gridDim.x; };
+  for (int64_t t = blockIdx.x; (t = next_live<T, NT, GRAD>(p, t, after)) < p.rows; t += gridDim.x) {
     const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;
     const Row<T> r(z, n);
     const T* body = z + r.head;
@@ -811,6 +832,11 @@ hipError_t launch_rows(const DistillParams& p, hipStream_t s) {
 #define PMX_ROWS(NT, NC)                                                                          \
   if (chunks >= 2 && chunks <= (int64_t)NT * NC) {                                                               \
     const int64_t g = std::min<int64_t>(p.rows, (int64_t)p.num_cu * waves_for(NC) * 256 / NT);    \
+    if (NT == 1024) {                                                                             \
+      hipLaunchKernelGGL(distill_claim_kernel, dim3(1), dim3(1), 0, s, p.next_row, (uint32_t)g);  \
+      hipError_t e = hipGetLastError();                                                           \
+      if (e != hipSuccess) return e;                                                              \
+    }                                                                                             \
     hipLaunchKernelGGL((distill_row_kernel<T, NT, NC, EX, GRAD>), dim3((unsigned)g), dim3(NT), 0, s, p); \
     return hipGetLastError();                                                                     \
   }
@@ -863,13 +889,19 @@ hipError_t launch_grad_t(const DistillParams& p, hipStream_t s) {
 
 }  // namespace
 
+// Chunks of a row that fit one block's registers.
+constexpr int kLongRow = 1024 * 16, kMiddleRow = 512 * 16;
+
 int64_t distill_part_floats(int64_t rows, int vocab, int top, int dtype) {
   const int k = splits_of(rows, vocab, dtype);
-  return k > 1 ? rows * (k * 3 + top + 1) : 0;
+  if (k > 1) return rows * (k * 3 + top + 1);
+  const int chunks = vocab / (dtype == PMX_F32 ? 4 : 8);
+  return rows > 0 && chunks > kMiddleRow && chunks <= kLongRow ? 1 : 0;  // next_row
 }
 
 hipError_t launch_distill_loss(DistillParams p, hipStream_t s) {
   p.splits = splits_of(p.rows, p.vocab, p.dtype);
+  p.next_row = reinterpret_cast<uint32_t*>(p.part);
   hipError_t e = hipSuccess;
   if (p.rows > 0) {  // (no rows: total = 0)
     if (p.dtype == PMX_F32) e = p.dz ? launch_loss_t<float, true>(p, s) : launch_loss_t<float, false>(p, s);

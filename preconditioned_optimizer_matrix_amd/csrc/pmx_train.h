@@ -50,6 +50,7 @@ struct DistillParams {
   float* stats;          // [rows][3]: max, 1 / sum exp((z - max) / tau), 1 / sum exp(z - max)
   float* part;           // rows cut over blocks: [rows][splits][3], then [rows][top + 1]
   int splits;
+  uint32_t* next_row;    // rows taken by blocks as they go (same memory as part)
   int64_t rows;
   int vocab, top;
   int dtype, teacher_dtype;
@@ -58,7 +59,8 @@ struct DistillParams {
   int num_cu;
 };
 
-// Floats of workspace (rows cut over blocks only).
+// Floats of workspace: partial sums of rows cut over blocks, or the counter of
+// claimed rows.
 int64_t distill_part_floats(int64_t rows, int vocab, int top, int dtype);
 hipError_t launch_distill_loss(DistillParams p, hipStream_t s);
 hipError_t launch_distill_grad(const DistillParams& p, hipStream_t s);

@@ -332,3 +332,31 @@ def test_refusals(env):
         setattr(q, field, old)
     torch.cuda.synchronize()
     assert (out == 5).all()
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(700, 4097, "f32"), (2100, 515, "bf16"), (300, 33001, "bf16"), (140, 16500, "f32"),
+                                              (530, 66001, "bf16"), (270, 40003, "f32"), (131, 131100, "bf16"), (600, 7, "f32")])
+@pytest.mark.parametrize("ignored", [0.0, 0.4, 1.0])
+def test_many_rows(env, rows, vocab, dtype, ignored):
+    """More rows than blocks, so that a block works through several, in each
+    class of row length; some, or all, of the rows ignored (and full of NaN)."""
+    torch, pmx, dev = env
+    print("many rows", rows, vocab, dtype, ignored, flush=True)
+    top = min(vocab, 6)
+    z, _, teacher, labels, weights = _inputs(torch, dev, rows, vocab, 0, dtype, 31)
+    ids = torch.randint(0, vocab, (rows, top), device=dev)  # some listed twice
+    teacher = torch.randn(rows, top, device=dev).to(z.dtype)
+    off = torch.rand(rows, device=dev) < ignored
+    weights[off] = 0.0
+    z[off] = float("nan")
+    kw = dict(tau=2.0, mix=0.75, labels=labels, weights=weights)
+    ref = reference(_np(z), _np(ids), _np(teacher), 2.0, 0.75, _np(labels), _np(weights))
+    total, r, _, dz = pmx.distill_loss(z, ids, teacher, grad=True, **kw)
+    _compare(torch, total, r, dz, ref, dtype == "bf16")
+    total, r, stats, _ = pmx.distill_loss(z, ids, teacher, **kw)
+    _compare(torch, total, r, None, ref, False)
+    late = pmx.distill_grad(z, ids, teacher, stats, **kw)
+    _compare(torch, None, None, late, ref, dtype == "bf16")
+    inplace = z.clone()
+    pmx.distill_loss(inplace, ids, teacher, out=inplace, **kw)
+    assert torch.equal(inplace, dz)
