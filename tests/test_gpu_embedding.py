@@ -111,6 +111,18 @@ def test_grad_accumulated_padded_strided(env, kind, dtype, out):
         _check_grad(torch, pmx, dev, kind, tokens, vocab, dim, dtype, out, False, pad=vocab - 1, ldp=1)
 
 
+@pytest.mark.parametrize("tokens,vocab,dim", [(2, 9, 5), (13, 3000, 200), (17, 2200000, 3), (65, 16, 515), (255, 130, 260), (256, 20000, 64),
+                                              (257, 20000, 64)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f32", "bf16")])
+def test_grad_few(env, tokens, vocab, dim, dtype, out):
+    """Few tokens: rows past a block's share, groups that end past the table, runs that a block shares out."""
+    torch, pmx, dev = env
+    print("few", tokens, vocab, dim, dtype, out, flush=True)
+    for kind in ("one", "zipf", "outside"):
+        _check_grad(torch, pmx, dev, kind, tokens, vocab, dim, dtype, out, False, pad=vocab // 2, ldp=1)
+        _check_grad(torch, pmx, dev, kind, tokens, vocab, dim, dtype, out, True, it=None if kind == "outside" else torch.int32, ldp=2)  # 2^40 is no int32
+
+
 def test_grad_long(env):
     """Several sort tiles a block and chunks of more than 32 tokens."""
     torch, pmx, dev = env
