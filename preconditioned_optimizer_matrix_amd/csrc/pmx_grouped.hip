@@ -442,48 +442,50 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
-// k tiles [kb, ke) of whole pieces; `va`, `vb` hold k tile kb on entry.  A k
-// tile is one block of instructions: its fragments are read a 16-wide step
-// ahead of the MFMAs, the next tile goes from the registers to the other LDS
-// buffer under the last step's, and the loads of the tile after that are issued
-// before the barrier.
-template <class C, int FORM, bool EDGE>
+// k tiles [kb, ke) of whole pieces; on entry va[d], vb[d] hold k tile kb + d (the
+// last one where there are fewer).  A k tile is one block of instructions: its
+// fragments are read a 16-wide step ahead of the MFMAs, the next tile goes from
+// the registers to the other LDS buffer under the last step's, and the loads of
+// the tile D after that are issued before the barrier.
+template <class C, int FORM, bool EDGE, int D>
 __device__ __forceinline__ void stream_loop(f32x16 (&acc)[C::FM][C::FN], typename C::E* smem,
                                             const Stream<C, a_kc(FORM), C::BM>& A,
                                             const Stream<C, b_kc(FORM), C::BN>& B,
-                                            u32x4_t (&va)[Stream<C, a_kc(FORM), C::BM>::N],
-                                            u32x4_t (&vb)[Stream<C, b_kc(FORM), C::BN>::N], int kb, int ke,
+                                            u32x4_t (&va)[D][Stream<C, a_kc(FORM), C::BM>::N],
+                                            u32x4_t (&vb)[D][Stream<C, b_kc(FORM), C::BN>::N], int kb, int ke,
                                             int wm, int wn) {
   constexpr int SA = C::size(a_kc(FORM), C::BM), ST = SA + C::size(b_kc(FORM), C::BN);
   constexpr int NA = Stream<C, a_kc(FORM), C::BM>::N, NB = Stream<C, b_kc(FORM), C::BN>::N;
-  A.template store<EDGE>(smem, va);
-  B.template store<EDGE>(smem + SA, vb);
-  {
-    const int k1 = min(kb + 1, ke - 1);  // past the last tile: the last one again
-    A.load(va, k1);
-    B.load(vb, k1);
-  }
+  A.template store<EDGE>(smem, va[0]);
+  B.template store<EDGE>(smem + SA, vb[0]);
+  A.load(va[0], min(kb + D, ke - 1));  // past the last tile: the last one again
+  B.load(vb[0], min(kb + D, ke - 1));
   __syncthreads();
-  for (int kt = kb; kt < ke; ++kt) {
-    const int cur = (kt - kb) & 1;
-    typename C::E* s = smem + cur * ST;
-    typename C::E* d = smem + (cur ^ 1) * ST;
-    multiply<C, FORM>(acc, s, s + SA, wm, wn);
-    A.template store<EDGE>(d, va);
-    B.template store<EDGE>(d + SA, vb);
-    const int k2 = min(kt + 2, ke - 1);
-    A.load(va, k2);
-    B.load(vb, k2);
-    if constexpr (!EDGE && sizeof(typename C::E) == 2) {
-      constexpr int MF = C::FM * C::FN, STEPS = C::BK / 16;
-      constexpr int NF = C::FM * (a_kc(FORM) ? 1 : 2) + C::FN * (b_kc(FORM) ? 1 : 2);
-      __builtin_amdgcn_sched_group_barrier(0x100, NF, 0);
+  for (int k0 = kb; k0 < ke; k0 += D) {
 #pragma unroll
-      for (int st = 0; st + 1 < STEPS; ++st) interleave<MF, NF, 0x100, (NF + MF - 1) / MF>();
-      interleave<MF, NA + NB, 0x200, (NA + NB + MF - 1) / MF>();
-      __builtin_amdgcn_sched_group_barrier(0x020, NA + NB, 0);
+    for (int i = 0; i < D; ++i) {
+      if (i > 0 && k0 + i >= ke) return;
+      const int n = (i + 1) % D;
+      const int cur = D % 2 ? (k0 - kb) & 1 : i & 1;
+      typename C::E* s = smem + cur * ST;
+      typename C::E* d = smem + (cur ^ 1) * ST;
+      multiply<C, FORM>(acc, s, s + SA, wm, wn);
+      A.template store<EDGE>(d, va[n]);
+      B.template store<EDGE>(d + SA, vb[n]);
+      const int kn = min(k0 + i + 1 + D, ke - 1);
+      A.load(va[n], kn);
+      B.load(vb[n], kn);
+      if constexpr (!EDGE && sizeof(typename C::E) == 2) {
+        constexpr int MF = C::FM * C::FN, STEPS = C::BK / 16;
+        constexpr int NF = C::FM * (a_kc(FORM) ? 1 : 2) + C::FN * (b_kc(FORM) ? 1 : 2);
+        __builtin_amdgcn_sched_group_barrier(0x100, NF, 0);
+#pragma unroll
+        for (int st = 0; st + 1 < STEPS; ++st) interleave<MF, NF, 0x100, (NF + MF - 1) / MF>();
+        interleave<MF, NA + NB, 0x200, (NA + NB + MF - 1) / MF>();
+        __builtin_amdgcn_sched_group_barrier(0x020, NA + NB, 0);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -691,6 +693,15 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void grouped_kernel(GroupedPar
   }
 }
 
+// k tiles on their way in registers.  The small tile multiplies for a fraction
+// of the 2 us that a load takes, so it keeps four (779 fp32 rows, 21 experts of
+// 4032 x 336, input gradient: 75 us, with one 166; 16 bf16 rows, 49 experts of
+// 1233 x 635, a step: 89, with one 102).  The middle one with two, fp32 four,
+// has no registers left: 112 us instead of 101 (5075 bf16 rows, 17 experts of
+// 1075 x 289, a step), 166 instead of 159 (2011 fp32 rows, 7 of 1001 x 500).
+template <class C>
+constexpr int kDepth = C::BM == 32 ? 4 : 1;
+
 template <class C>
 constexpr bool kTurns = C::WAVES == 8 && C::BK == 64 && sizeof(typename C::E) == 2;
 
@@ -790,17 +801,22 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
   };
   Stream<C, AK, C::BM> A;
   Stream<C, BK_, C::BN> B;
-  u32x4_t va[Stream<C, AK, C::BM>::N], vb[Stream<C, BK_, C::BN>::N];
-  // the item's operands, and its first whole k tile on the way
+  constexpr int D = kDepth<C>;
+  u32x4_t va[D][Stream<C, AK, C::BM>::N], vb[D][Stream<C, BK_, C::BN>::N];
+  // the item's operands, and its first whole k tiles on the way
   auto start = [&](const Item& it) {
     const E* a = reinterpret_cast<const E*>(p.a) + (int64_t)it.r0 * p.lda;
     const E* b = reinterpret_cast<const E*>(p.b) +
                  (FORM == TN ? (int64_t)it.r0 * p.ldb : (int64_t)it.e * p.stride_b);
     A.init(a, p.lda, it.m0, it.M);
     B.init(b, p.ldb, it.n0, p.n);
-    if (it.kb < min(it.ke, it.K / C::BK)) {
-      A.load(va, it.kb);
-      B.load(vb, it.kb);
+    const int kw = min(it.ke, it.K / C::BK);
+    if (it.kb < kw) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        A.load(va[d], min(it.kb + d, kw - 1));
+        B.load(vb[d], min(it.kb + d, kw - 1));
+      }
     }
   };
   Item it;
@@ -819,11 +835,11 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
       const bool edge = (!AK && it.m0 + C::BM > it.M) || (!BK_ && it.n0 + C::BN > p.n);
       if constexpr (kTurns<C>) {
         const int group = __builtin_amdgcn_readfirstlane(wid >> 2);
-        if (edge) turns_loop<C, FORM, true>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn, group);
-        else turns_loop<C, FORM, false>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn, group);
+        if (edge) turns_loop<C, FORM, true>(acc, smem, A, B, va[0], vb[0], it.kb, kw, wm, wn, group);
+        else turns_loop<C, FORM, false>(acc, smem, A, B, va[0], vb[0], it.kb, kw, wm, wn, group);
       } else {
-        if (edge) stream_loop<C, FORM, true>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
-        else stream_loop<C, FORM, false>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
+        if (edge) stream_loop<C, FORM, true, D>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
+        else stream_loop<C, FORM, false, D>(acc, smem, A, B, va, vb, it.kb, kw, wm, wn);
       }
     }
     if (kw < it.ke) {  // the rest of the contraction
@@ -1191,10 +1207,13 @@ Choice choose_outer(int64_t rows, int m, int n, int groups, int dtype) {
   return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
 }
 
-// Splits so that the items come to two a compute unit, a split keeping at
-// least 8 k tiles.
+// Splits so that the items come to at most two a compute unit, a split keeping
+// at least 8 k tiles.  (8289 fp32 rows, 11 experts of 152 x 848, a step: 170 us,
+// 242 with nothing split from 129 tiles on.  Four or eight a unit: 199 us
+// instead of 166 for 2011 rows, 7 of 1001 x 500, 51 instead of 47 for 16 bf16
+// rows, 32 of 4096 x 1024.)
 int splits_for(int64_t tiles, int64_t nk) {
-  if (tiles * 2 > kCU || tiles == 0) return 1;
+  if (tiles == 0) return 1;
   const int64_t want = (2 * kCU) / tiles, most = nk / 8;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 64));
 }
@@ -1229,7 +1248,7 @@ hipError_t launch_dma(const GroupedParams& p, dim3 grid, hipStream_t s) {
   }
 
 template <class C, int FORM>
-hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s) {
+hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s, bool any_side = false) {
   int64_t g = items < (int64_t)p.num_cu * C::MINB ? items : (int64_t)p.num_cu * C::MINB;
   g = (g + 7) / 8 * 8;
   if (g < 8) g = 8;
@@ -1238,16 +1257,20 @@ hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s) {
     if (dma_ok(p)) return launch_dma(p, grid, s);
   }
   if constexpr (C::BM == 32) {
-    PMX_LAUNCH(grouped_kernel)
-  } else {
+    if (any_side) {
+      PMX_LAUNCH(grouped_kernel)
+      return hipGetLastError();
+    }
+  }
+  if constexpr (C::BM != 32 || FORM != TN) {
     PMX_LAUNCH(grouped_tile_kernel)
   }
   return hipGetLastError();
 }
 
 template <class C>
-hipError_t launch_product_cfg(const GroupedParams& p, int64_t items, hipStream_t s) {
-  return p.trans_b ? launch_form<C, NT>(p, items, s) : launch_form<C, NN>(p, items, s);
+hipError_t launch_product_cfg(const GroupedParams& p, int64_t items, hipStream_t s, bool any_side = false) {
+  return p.trans_b ? launch_form<C, NT>(p, items, s, any_side) : launch_form<C, NN>(p, items, s, any_side);
 }
 
 hipError_t launch_join(const GroupedParams& p, int64_t rows, int m, hipStream_t s) {
@@ -1277,11 +1300,11 @@ hipError_t launch_grouped_product(const GroupedParams& p, hipStream_t s) {
   const int64_t items = max_tiles_product(c, p.rows, p.n, p.groups) * p.splits;
   hipError_t e;
   if (p.dtype == PMX_BF16) {
-    e = c.cfg == 0   ? launch_product_cfg<BSmall>(p, items, s)
+    e = c.cfg == 0   ? launch_product_cfg<BSmall>(p, items, s, p.k < 8 || p.n < 8)
         : c.cfg == 1 ? launch_product_cfg<BMid>(p, items, s)
                      : launch_product_cfg<BLarge>(p, items, s);
   } else {
-    e = c.cfg == 0 ? launch_product_cfg<FSmall>(p, items, s) : launch_product_cfg<FMid>(p, items, s);
+    e = c.cfg == 0 ? launch_product_cfg<FSmall>(p, items, s, p.k < 8 || p.n < 8) : launch_product_cfg<FMid>(p, items, s);
   }
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_join(p, p.rows, (int)p.rows, s);
@@ -1293,11 +1316,11 @@ hipError_t launch_grouped_outer(const GroupedParams& p, hipStream_t s) {
       (int64_t)p.groups * ((p.m + c.bm - 1) / c.bm) * ((p.n + c.bn - 1) / c.bn) * p.splits;
   hipError_t e;
   if (p.dtype == PMX_BF16)
-    e = c.cfg == 0   ? launch_form<BSmall, TN>(p, items, s)
+    e = c.cfg == 0   ? launch_form<BSmall, TN>(p, items, s, true)
         : c.cfg == 1 ? launch_form<BMid, TN>(p, items, s)
                      : launch_form<BLarge, TN>(p, items, s);
   else
-    e = c.cfg == 0 ? launch_form<FSmall, TN>(p, items, s) : launch_form<FMid, TN>(p, items, s);
+    e = c.cfg == 0 ? launch_form<FSmall, TN>(p, items, s, true) : launch_form<FMid, TN>(p, items, s);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_join(p, (int64_t)p.groups * p.m, p.m, s);
 }
