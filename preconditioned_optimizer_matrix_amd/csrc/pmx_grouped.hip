@@ -750,9 +750,24 @@ __device__ __forceinline__ void store_rows(const f32x16* acc, O* stage, O* c, in
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The large tiles that the large tiles' launch runs: whole rounds of them where
+// quarters of the rest find a unit each, which a second launch gives them, and
+// the contraction is long enough to pay for that.  (16384 rows, 8 experts of
+// 2048 x 2048, 2.16 rounds: forward 160 -> 149 us, input gradient 180 -> 162;
+// 32768 rows, 32 of 4096 x 1024: input gradient, k = 4096, 2.23 rounds, 343 -> 304,
+// but forward, k = 1024, 9.06 rounds, 327 -> 338.)
+constexpr int kLarge = 256, kQuartersK = 2048;
+__device__ __forceinline__ int whole_rounds(int items, int round, int k) {
+  const int rest = items % round;
+  return k >= kQuartersK && rest * 4 <= round ? items - rest : items;
+}
+
 // The same products on pipelined tiles.  Blocks are persistent: the first k
 // tile of a block's next item is loaded before the item's results are stored.
-template <class C, int FORM, typename O, bool SPLIT>
+// QUARTERS: the large tiles after the whole rounds, as 128 x 128 ones, a block a
+// unit with four k tiles on their way (two blocks a unit and two k tiles: 165 and
+// 178 us where this takes 150 and 161).
+template <class C, int FORM, typename O, bool SPLIT, bool QUARTERS = false>
 __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_tile_kernel(GroupedParams p) {
   typedef typename C::E E;
   constexpr bool AK = a_kc(FORM), BK_ = b_kc(FORM);
@@ -762,19 +777,26 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
   constexpr int LDS = STAGE * C::WAVES / (int)sizeof(E) > 2 * ST ? STAGE * C::WAVES / (int)sizeof(E) : 2 * ST;
   __shared__ __attribute__((aligned(16))) E smem[LDS];
   __shared__ Table T;
-  const int tiles_n = (p.n + C::BN - 1) / C::BN;
-  const int tiles_m = FORM == TN ? (p.m + C::BM - 1) / C::BM : 0;
-  build_table(T, p, C::BM, tiles_n, FORM == TN ? tiles_m * tiles_n : 0);
+  constexpr int TM = QUARTERS ? kLarge : C::BM, TN_ = QUARTERS ? kLarge : C::BN;  // of the table's tiles
+  const int tiles_n = (p.n + TN_ - 1) / TN_;
+  const int tiles_m = FORM == TN ? (p.m + TM - 1) / TM : 0;
+  build_table(T, p, TM, tiles_n, FORM == TN ? tiles_m * tiles_n : 0);
   const int wid = threadIdx.x >> 6;
   constexpr int WGN = C::BN / C::WN;
   const int wm = wid / WGN * C::WM, wn = wid % WGN * C::WN;
   const int splits = SPLIT ? p.splits : 1;
-  if constexpr (FORM != TN) zero_outside<C, O, SPLIT>(T, p, splits);
+  if constexpr (FORM != TN && !QUARTERS) zero_outside<C, O, SPLIT>(T, p, splits);
 
   // Blocks are dealt to the 8 XCDs round-robin.  Each round of gridDim.x items
   // gives every XCD a contiguous share, neighbouring tiles for its L2, and the
   // rounds spread long and short groups over all of them.
-  const int items = T.tile[p.groups] * splits;
+  int items = T.tile[p.groups] * splits, first = 0;
+  if constexpr (QUARTERS) {
+    first = whole_rounds(items, p.round, p.k);
+    items = (items - first) * 4;
+  } else if constexpr (C::BM == kLarge && FORM != TN) {
+    items = whole_rounds(items, gridDim.x, p.k);
+  }
   int q0 = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   struct Item {
     int e, r0, m0, n0, K, M, kb, ke, sp;
@@ -783,17 +805,18 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
     if (q0 >= items) return false;
     const int q = q0;
     q0 += gridDim.x;
-    const int t = SPLIT ? q / splits : q;
+    const int t = QUARTERS ? first + q / 4 : SPLIT ? q / splits : q;
     it.sp = SPLIT ? q - t * splits : 0;
     it.e = group_of(T, p.groups, t);
     it.r0 = T.begin[it.e];
     const int nr = T.begin[it.e + 1] - it.r0;
     int tm, tn;
-    tile_of(t - T.tile[it.e], FORM == TN ? tiles_m : (nr + C::BM - 1) / C::BM, tiles_n, tm, tn);
-    it.m0 = tm * C::BM;
-    it.n0 = tn * C::BN;
+    tile_of(t - T.tile[it.e], FORM == TN ? tiles_m : (nr + TM - 1) / TM, tiles_n, tm, tn);
+    it.m0 = tm * TM + (QUARTERS ? (q >> 1 & 1) * C::BM : 0);
+    it.n0 = tn * TN_ + (QUARTERS ? (q & 1) * C::BN : 0);
     it.K = FORM == TN ? nr : p.k;
     it.M = FORM == TN ? p.m : nr;
+    if (QUARTERS && (it.m0 >= it.M || it.n0 >= p.n)) return false;  // a block has no second one
     const int nk = (it.K + C::BK - 1) / C::BK;
     it.kb = SPLIT ? (int)((int64_t)nk * it.sp / splits) : 0;
     it.ke = SPLIT ? (int)((int64_t)nk * (it.sp + 1) / splits) : nk;
@@ -801,7 +824,7 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
   };
   Stream<C, AK, C::BM> A;
   Stream<C, BK_, C::BN> B;
-  constexpr int D = kDepth<C>;
+  constexpr int D = QUARTERS ? 4 : kDepth<C>;
   u32x4_t va[D][Stream<C, AK, C::BM>::N], vb[D][Stream<C, BK_, C::BN>::N];
   // the item's operands, and its first whole k tiles on the way
   auto start = [&](const Item& it) {
@@ -1268,6 +1291,16 @@ hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s, boo
   return hipGetLastError();
 }
 
+using BQuarter = Cfg<uint16_t, 128, 128, 64, 64, 64, 1>;
+template <int FORM>
+hipError_t launch_quarters(GroupedParams p, hipStream_t s) {
+  p.round = (p.num_cu + 7) / 8 * 8;  // the first launch's grid
+  const dim3 grid((unsigned)p.round), block(BQuarter::THREADS);
+  if (p.out_dtype == PMX_F32) hipLaunchKernelGGL((grouped_tile_kernel<BQuarter, FORM, float, false, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((grouped_tile_kernel<BQuarter, FORM, uint16_t, false, true>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
 template <class C>
 hipError_t launch_product_cfg(const GroupedParams& p, int64_t items, hipStream_t s, bool any_side = false) {
   return p.trans_b ? launch_form<C, NT>(p, items, s, any_side) : launch_form<C, NN>(p, items, s, any_side);
@@ -1306,6 +1339,7 @@ hipError_t launch_grouped_product(const GroupedParams& p, hipStream_t s) {
   } else {
     e = c.cfg == 0 ? launch_product_cfg<FSmall>(p, items, s, p.k < 8 || p.n < 8) : launch_product_cfg<FMid>(p, items, s);
   }
+  if (e == hipSuccess && c.cfg == 2 && p.k >= kQuartersK) e = p.trans_b ? launch_quarters<NT>(p, s) : launch_quarters<NN>(p, s);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_join(p, p.rows, (int)p.rows, s);
 }

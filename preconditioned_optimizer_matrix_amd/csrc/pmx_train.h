@@ -109,6 +109,7 @@ struct GroupedParams {
   float* part;         // split contraction: partial results
   int splits;
   int num_cu;
+  int round;           // quarters: blocks of the large tiles' launch
 };
 // Splits of the contraction (1: none) and the floats of workspace they need.
 int grouped_product_splits(int64_t rows, int k, int n, int groups, int dtype);

@@ -365,3 +365,23 @@ def test_outer_of_large_aligned_tiles(env, rows, groups, m, n, out, accumulate):
         ref = An[a:b].T @ Bn[a:b] + (C0[e] if accumulate else 0.0)
         s = np.abs(An[a:b]).T @ np.abs(Bn[a:b]) + (np.abs(C0[e]) if accumulate else 0.0)
         assert (np.abs(Cn[e] - ref) <= _bound(ref, s, b - a + 1, out == "bf16")).all(), e
+
+
+@pytest.mark.parametrize("k,n", [(2048, 1000), (2051, 1021)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_last_tiles_in_quarters(env, k, n, out):
+    """A few tiles more than whole rounds: 68 rows of tiles by 4, the last ones cut, quarters of them outside."""
+    torch, pmx, dev = env
+    off = np.cumsum([0, 4000, 300, 0, 6000, 6500])
+    rows, groups = int(off[-1]), len(off) - 1
+    t = torch.from_numpy(off).to(dev)
+    odt = torch.float32 if out == "f32" else torch.bfloat16
+    A, a = _make(torch, dev, torch.bfloat16, (rows, k), 3)
+    for trans in (True, False):
+        print("quarters", k, n, out, trans, flush=True)
+        B, b = _make(torch, dev, torch.bfloat16, (groups, n, k) if trans else (groups, k, n), 4)
+        C = torch.full((rows, n + 3), 7.0, device=dev).to(odt)
+        pmx.grouped_product(A, B, t, trans_b=trans, out=C[:, :n])
+        ref, mag = _ref_product(a, b, off, trans)
+        assert (np.abs(C[:, :n].double().cpu().numpy() - ref) <= _bound(ref, mag, k, out == "bf16")).all()
+        assert (C[:, n:] == 7).all()
