@@ -696,11 +696,21 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void grouped_kernel(GroupedPar
 // k tiles on their way in registers.  The small tile multiplies for a fraction
 // of the 2 us that a load takes, so it keeps four (779 fp32 rows, 21 experts of
 // 4032 x 336, input gradient: 75 us, with one 166; 16 bf16 rows, 49 experts of
-// 1233 x 635, a step: 89, with one 102).  The middle one with two, fp32 four,
-// has no registers left: 112 us instead of 101 (5075 bf16 rows, 17 experts of
-// 1075 x 289, a step), 166 instead of 159 (2011 fp32 rows, 7 of 1001 x 500).
+// 1233 x 635, a step: 89, with one 102).  The middle one has no registers left
+// for a second: 112 us instead of 101 (5075 bf16 rows, 17 experts of 1075 x 289,
+// a step).
 template <class C>
-constexpr int kDepth = C::BM == 32 ? 4 : 1;
+constexpr int kDepth = C::BM == 32 ? 4 : C::BM == 64 ? 2 : 1;
+
+// Blocks a compute unit, and items of a window (0: as many as blocks).  The
+// larger tiles are persistent; of the 64 x 64 ones about five fit a unit, the
+// hardware deals out more as they end, and windows of 256 items keep groups of
+// unequal length from piling up on one XCD (fp32, 8 experts of 1024 x 1024, 8192
+// rows, weight gradient: 183 us, 309 with one window).
+template <class C>
+constexpr int kBlocks = C::BM == 64 ? 8 : C::MINB;
+template <class C>
+constexpr int kWindow = C::BM == 64 ? 256 : 0;
 
 template <class C>
 constexpr bool kTurns = C::WAVES == 8 && C::BK == 64 && sizeof(typename C::E) == 2;
@@ -787,9 +797,9 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
   const int splits = SPLIT ? p.splits : 1;
   if constexpr (FORM != TN && !QUARTERS) zero_outside<C, O, SPLIT>(T, p, splits);
 
-  // Blocks are dealt to the 8 XCDs round-robin.  Each round of gridDim.x items
-  // gives every XCD a contiguous share, neighbouring tiles for its L2, and the
-  // rounds spread long and short groups over all of them.
+  // Blocks are dealt to the 8 XCDs round-robin.  Each window of items gives every
+  // XCD a contiguous share, neighbouring tiles for its L2, and the windows spread
+  // long and short groups over all of them.
   int items = T.tile[p.groups] * splits, first = 0;
   if constexpr (QUARTERS) {
     first = whole_rounds(items, p.round, p.k);
@@ -797,7 +807,9 @@ __global__ __launch_bounds__(C::THREADS, C::MINB * C::WAVES / 4) void grouped_ti
   } else if constexpr (C::BM == kLarge && FORM != TN) {
     items = whole_rounds(items, gridDim.x, p.k);
   }
-  int q0 = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  const int window = kWindow<C> ? kWindow<C> : (int)gridDim.x, w0 = (int)blockIdx.x / window * window;
+  const int size = min(window, (int)gridDim.x - w0), in = (int)blockIdx.x - w0;
+  int q0 = w0 + (in & 7) * (size >> 3) + (in >> 3);
   struct Item {
     int e, r0, m0, n0, K, M, kb, ke, sp;
   };
@@ -1207,27 +1219,41 @@ __global__ __launch_bounds__(256) void grouped_join_kernel(GroupedParams p, int6
 using BLarge = Cfg<uint16_t, 256, 256, 64, 128, 64, 1>;  // 8 waves
 using BMid = Cfg<uint16_t, 128, 128, 64, 64, 64, 2>;     // 4 waves
 using BSmall = Cfg<uint16_t, 32, 128, 64, 32, 32, 2>;    // 4 waves
-using FMid = Cfg<float, 128, 128, 16, 64, 64, 2>;
+using BHalf = Cfg<uint16_t, 64, 64, 64, 32, 32, 2>;      // 4 waves
+using FHalf = Cfg<float, 64, 64, 16, 32, 32, 4>;
 using FSmall = Cfg<float, 32, 128, 32, 32, 32, 2>;
 
-// Tile sizes by the average group: 0 small (32 x 128), 1 middle (128 x 128),
-// 2 large (256 x 256, bf16).
+// Tile sizes: 0 small (32 x 128), 1 half (64 x 64), 2 middle (128 x 128, bf16),
+// 3 large (256 x 256, bf16).  The small tile is for groups of few rows, and has
+// the sides under a 16-byte piece.  fp32's matrix instructions take 16 times as
+// long a product as bf16's, so its 64 x 64 tiles ask little enough of LDS and
+// L2, and their number is worth more: 7 experts of 1001 x 500, 2011 rows, 44
+// (forward), 52 and 44 us (gradients), with 128 x 128 ones 61, 56 and 74; 8 of
+// 2048 x 2048, 16384 rows, 1200 and 1290; the one loss 8192 rows, 64 of 2048 x
+// 1024, weight gradient, 407 and 390.  bf16 takes them where fewer than three
+// in four units would have a 128 x 128 one: 1907 rows, 11 of 144 x 1357, forward,
+// 52 such tiles, 24 us instead of 31; 5075 rows, 17 of 1075 x 289, input
+// gradient, 171, 32 instead of 45; but 23489 rows, 13 of 165 x 432, forward, 392,
+// 29 instead of 25.
 struct Choice {
   int cfg, bm, bn, bk;
 };
-// The small tile also has the sides under a 16-byte piece.
+Choice choose_wide(int64_t tiles128, bool large, int dtype) {
+  if (dtype == PMX_F32) return {1, 64, 64, 16};
+  if (large) return {3, 256, 256, 64};
+  if (tiles128 * 4 < kCU * 3) return {1, 64, 64, 64};
+  return {2, 128, 128, 64};
+}
 Choice choose_product(int64_t rows, int k, int n, int groups, int dtype) {
   const int64_t avg = rows / groups;
   if (avg <= 48 || k < 8 || n < 8) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
-  if (dtype == PMX_BF16 && avg >= 256 && n >= 256 && (rows / 256) * ((n + 255) / 256) >= kCU)
-    return {2, 256, 256, 64};
-  return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
+  return choose_wide((rows / 128 + groups) * ((n + 127) / 128),
+                     avg >= 256 && n >= 256 && (rows / 256) * ((n + 255) / 256) >= kCU, dtype);
 }
 Choice choose_outer(int64_t rows, int m, int n, int groups, int dtype) {
-  const int64_t large = (int64_t)groups * ((m + 255) / 256) * ((n + 255) / 256);
   if (m < 8 || n < 8) return {0, 32, 128, dtype == PMX_BF16 ? 64 : 32};
-  if (dtype == PMX_BF16 && m >= 256 && n >= 256 && large >= kCU && rows / groups >= 64) return {2, 256, 256, 64};
-  return {1, 128, 128, dtype == PMX_BF16 ? 64 : 16};
+  auto tiles = [&](int side) { return (int64_t)groups * ((m + side - 1) / side) * ((n + side - 1) / side); };
+  return choose_wide(tiles(128), m >= 256 && n >= 256 && tiles(256) >= kCU && rows / groups >= 64, dtype);
 }
 
 // Splits so that the items come to at most two a compute unit, a split keeping
@@ -1272,7 +1298,8 @@ hipError_t launch_dma(const GroupedParams& p, dim3 grid, hipStream_t s) {
 
 template <class C, int FORM>
 hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s, bool any_side = false) {
-  int64_t g = items < (int64_t)p.num_cu * C::MINB ? items : (int64_t)p.num_cu * C::MINB;
+  const int64_t slots = (int64_t)p.num_cu * kBlocks<C>;
+  int64_t g = items < slots ? items : slots;
   g = (g + 7) / 8 * 8;
   if (g < 8) g = 8;
   const dim3 grid((unsigned)g), block(C::THREADS);
@@ -1334,12 +1361,14 @@ hipError_t launch_grouped_product(const GroupedParams& p, hipStream_t s) {
   hipError_t e;
   if (p.dtype == PMX_BF16) {
     e = c.cfg == 0   ? launch_product_cfg<BSmall>(p, items, s, p.k < 8 || p.n < 8)
-        : c.cfg == 1 ? launch_product_cfg<BMid>(p, items, s)
+        : c.cfg == 1 ? launch_product_cfg<BHalf>(p, items, s)
+        : c.cfg == 2 ? launch_product_cfg<BMid>(p, items, s)
                      : launch_product_cfg<BLarge>(p, items, s);
   } else {
-    e = c.cfg == 0 ? launch_product_cfg<FSmall>(p, items, s, p.k < 8 || p.n < 8) : launch_product_cfg<FMid>(p, items, s);
+    e = c.cfg == 0 ? launch_product_cfg<FSmall>(p, items, s, p.k < 8 || p.n < 8)
+                   : launch_product_cfg<FHalf>(p, items, s);
   }
-  if (e == hipSuccess && c.cfg == 2 && p.k >= kQuartersK) e = p.trans_b ? launch_quarters<NT>(p, s) : launch_quarters<NN>(p, s);
+  if (e == hipSuccess && c.cfg == 3 && p.k >= kQuartersK) e = p.trans_b ? launch_quarters<NT>(p, s) : launch_quarters<NN>(p, s);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_join(p, p.rows, (int)p.rows, s);
 }
@@ -1351,10 +1380,12 @@ hipError_t launch_grouped_outer(const GroupedParams& p, hipStream_t s) {
   hipError_t e;
   if (p.dtype == PMX_BF16)
     e = c.cfg == 0   ? launch_form<BSmall, TN>(p, items, s, true)
-        : c.cfg == 1 ? launch_form<BMid, TN>(p, items, s)
+        : c.cfg == 1 ? launch_form<BHalf, TN>(p, items, s)
+        : c.cfg == 2 ? launch_form<BMid, TN>(p, items, s)
                      : launch_form<BLarge, TN>(p, items, s);
   else
-    e = c.cfg == 0 ? launch_form<FSmall, TN>(p, items, s, true) : launch_form<FMid, TN>(p, items, s);
+    e = c.cfg == 0 ? launch_form<FSmall, TN>(p, items, s, true)
+                   : launch_form<FHalf, TN>(p, items, s);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_join(p, (int64_t)p.groups * p.m, p.m, s);
 }

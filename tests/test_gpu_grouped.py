@@ -385,3 +385,17 @@ def test_last_tiles_in_quarters(env, k, n, out):
         ref, mag = _ref_product(a, b, off, trans)
         assert (np.abs(C[:, :n].double().cpu().numpy() - ref) <= _bound(ref, mag, k, out == "bf16")).all()
         assert (C[:, n:] == 7).all()
+
+
+# groups of middle size: enough 128 x 128 tiles, too few larger ones; the last sizes also split the contraction
+@pytest.mark.parametrize("rows,groups,k,n", [(6000, 30, 200, 1000), (5001, 21, 131, 1029), (1500, 5, 1100, 1500)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_middle_products(env, rows, groups, k, n, dtype):
+    test_larger_products(env, rows, groups, k, n, dtype)
+
+
+@pytest.mark.parametrize("rows,groups,m,n", [(3000, 50, 260, 390), (3001, 50, 129, 515), (2200, 2, 1200, 1201)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_middle_outer(env, rows, groups, m, n, dtype, accumulate):
+    test_larger_outer(env, rows, groups, m, n, dtype, accumulate)
