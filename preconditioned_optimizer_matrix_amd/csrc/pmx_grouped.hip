@@ -693,24 +693,22 @@ __global__ __launch_bounds__(C::THREADS, C::MINB) void grouped_kernel(GroupedPar
   }
 }
 
-// k tiles on their way in registers.  The small tile multiplies for a fraction
-// of the 2 us that a load takes, so it keeps four (779 fp32 rows, 21 experts of
-// 4032 x 336, input gradient: 75 us, with one 166; 16 bf16 rows, 49 experts of
-// 1233 x 635, a step: 89, with one 102).  The middle one has no registers left
-// for a second: 112 us instead of 101 (5075 bf16 rows, 17 experts of 1075 x 289,
-// a step).
+// k tiles on their way in registers.  The tiles up to 64 rows keep two; the
+// middle one has no registers left for a second: 112 us instead of 101 (5075
+// bf16 rows, 17 experts of 1075 x 289, a step).
 template <class C>
-constexpr int kDepth = C::BM == 32 ? 4 : C::BM == 64 ? 2 : 1;
+constexpr int kDepth = C::BM <= 64 ? 2 : 1;
 
 // Blocks a compute unit, and items of a window (0: as many as blocks).  The
-// larger tiles are persistent; of the 64 x 64 ones about five fit a unit, the
+// larger tiles are persistent.  Of the others two to five fit a unit, the
 // hardware deals out more as they end, and windows of 256 items keep groups of
-// unequal length from piling up on one XCD (fp32, 8 experts of 1024 x 1024, 8192
-// rows, weight gradient: 183 us, 309 with one window).
+// unequal length from piling up on one XCD.  (fp32, 8 experts of 1024 x 1024,
+// 8192 rows, weight gradient: 183 us, 309 with one window; bf16, 32 of 4096 x
+// 1024, 256 rows, input gradient: 50 us, 66 with three persistent blocks a unit.)
 template <class C>
-constexpr int kBlocks = C::BM == 64 ? 8 : C::MINB;
+constexpr int kBlocks = C::BM <= 64 ? 8 : C::MINB;
 template <class C>
-constexpr int kWindow = C::BM == 64 ? 256 : 0;
+constexpr int kWindow = C::BM <= 64 ? 256 : 0;
 
 template <class C>
 constexpr bool kTurns = C::WAVES == 8 && C::BK == 64 && sizeof(typename C::E) == 2;
@@ -1218,10 +1216,10 @@ __global__ __launch_bounds__(256) void grouped_join_kernel(GroupedParams p, int6
 // ------------------------------------------------------------ launchers
 using BLarge = Cfg<uint16_t, 256, 256, 64, 128, 64, 1>;  // 8 waves
 using BMid = Cfg<uint16_t, 128, 128, 64, 64, 64, 2>;     // 4 waves
-using BSmall = Cfg<uint16_t, 32, 128, 64, 32, 32, 2>;    // 4 waves
+using BSmall = Cfg<uint16_t, 32, 128, 64, 32, 32, 3>;    // 4 waves
 using BHalf = Cfg<uint16_t, 64, 64, 64, 32, 32, 2>;      // 4 waves
 using FHalf = Cfg<float, 64, 64, 16, 32, 32, 4>;
-using FSmall = Cfg<float, 32, 128, 32, 32, 32, 2>;
+using FSmall = Cfg<float, 32, 128, 32, 32, 32, 3>;
 
 // Tile sizes: 0 small (32 x 128), 1 half (64 x 64), 2 middle (128 x 128, bf16),
 // 3 large (256 x 256, bf16).  The small tile is for groups of few rows, and has
