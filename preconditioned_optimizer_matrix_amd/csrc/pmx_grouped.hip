@@ -1254,14 +1254,17 @@ Choice choose_outer(int64_t rows, int m, int n, int groups, int dtype) {
   return choose_wide(tiles(128), m >= 256 && n >= 256 && tiles(256) >= kCU && rows / groups >= 64, dtype);
 }
 
-// Splits so that the items come to at most two a compute unit, a split keeping
-// at least 8 k tiles.  (8289 fp32 rows, 11 experts of 152 x 848, a step: 170 us,
-// 242 with nothing split from 129 tiles on.  Four or eight a unit: 199 us
-// instead of 166 for 2011 rows, 7 of 1001 x 500, 51 instead of 47 for 16 bf16
-// rows, 32 of 4096 x 1024.)
-int splits_for(int64_t tiles, int64_t nk) {
+// Splits so that the items come to at most `unit` a compute unit, a split
+// keeping at least `least` k tiles.  (8289 fp32 rows, 11 experts of 152 x 848, a
+// step: 170 us, 242 with nothing split from 129 tiles on.  Four a unit for the
+// small tile: 51 instead of 47 for 16 bf16 rows, 32 experts of 4096 x 1024.  The
+// 64 x 64 tile takes four, in the outer form from 8 k tiles on: 23489 bf16 rows,
+// 13 of 165 x 432, 41 us, 62 with two; 21648 fp32 rows, 7 of 184 x 648, 95 and
+// 139.  In the products, whose partial results are many, from 16: 3384 bf16
+// rows, 2 of 1925 x 328, input gradient, 34 us, 41 from 8 on.)
+int splits_for(int64_t tiles, int64_t nk, int unit, int least) {
   if (tiles == 0) return 1;
-  const int64_t want = (2 * kCU) / tiles, most = nk / 8;
+  const int64_t want = unit * kCU / tiles, most = nk / least;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 64));
 }
 
@@ -1343,13 +1346,14 @@ hipError_t launch_join(const GroupedParams& p, int64_t rows, int m, hipStream_t 
 
 int grouped_product_splits(int64_t rows, int k, int n, int groups, int dtype) {
   const Choice c = choose_product(rows, k, n, groups, dtype);
-  return splits_for(max_tiles_product(c, rows, n, groups), (k + c.bk - 1) / c.bk);
+  return splits_for(max_tiles_product(c, rows, n, groups), (k + c.bk - 1) / c.bk,
+                    c.cfg == 1 ? 4 : 2, c.cfg == 1 ? 16 : 8);
 }
 
 int grouped_outer_splits(int64_t rows, int m, int n, int groups, int dtype) {
   const Choice c = choose_outer(rows, m, n, groups, dtype);
   const int64_t tiles = (int64_t)groups * ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
-  return splits_for(tiles, rows / groups / c.bk);
+  return splits_for(tiles, rows / groups / c.bk, c.cfg == 1 ? 4 : 2, 8);
 }
 
 hipError_t launch_grouped_product(const GroupedParams& p, hipStream_t s) {
