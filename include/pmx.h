@@ -474,7 +474,8 @@ enum { PMX_I32 = 0, PMX_I64 = 1 };
  * made non-decreasing, so none leads outside the matrices.  A and B have
  * `dtype`; C has out_dtype: PMX_F32, or PMX_BF16 for bf16 operands (fp32
  * operands with a bf16 C: PMX_ERR_NOT_SUPPORTED).  Accumulation is fp32 with
- * one rounding.  No alignment beyond the element's is asked for.  rows may be
+ * one rounding.  No alignment beyond the element's is asked for; row distances
+ * of A and B above 2^22 elements are PMX_ERR_NOT_SUPPORTED.  rows may be
  * 0 (nothing is enqueued); 1 <= k, n <= 2^20, 1 <= groups <= PMX_MAX_GROUPS.
  * The workspace may be NULL when the query says 0.
  */
