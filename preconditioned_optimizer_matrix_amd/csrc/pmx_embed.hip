@@ -11,6 +11,11 @@
 // dW: their other blocks write zeros to every row, the rows that have tokens
 // are written again afterwards.  Up to kSmallSort tokens one block sorts them
 // in LDS in one launch; up to kFew tokens one launch does everything.
+//
+// Measured, 32768 tokens of 1024 bf16 into 50000 fp32 rows (272 MB, 53 us at a
+// copy's rate): 95 us, digit counts 10 and 8, scatters 14 and 14 (the clearing
+// under these four), sums 31, joins 9.  4097 tokens of 515 fp32 into 10007 rows:
+// sort and clearing 15, sums 5, joins 9.  A lookup of 8 rows takes 2.4 us.
 #include <algorithm>
 
 #include "pmx_train.h"
