@@ -716,13 +716,13 @@ hipError_t lookup_t(const EmbedParams& p, int vb, hipStream_t s) {
 }
 
 // `blocks` sorting blocks and, unless dW is added to, blocks that clear its
-// rows [from, to) of `tenths` tenths.
-dim3 with_clear(const EmbedParams& p, int blocks, int from, int to, int tenths, Clear* z) {
+// rows [from, to) of `tenths` tenths, `most` at most.
+dim3 with_clear(const EmbedParams& p, int blocks, int from, int to, int tenths, Clear* z, int most = 2048) {
   z->r0 = (int)((int64_t)p.vocab * from / tenths);
   z->r1 = (int)((int64_t)p.vocab * to / tenths);
   z->first_block = blocks;
   const int rows = p.accumulate ? 0 : z->r1 - z->r0;
-  return dim3((unsigned)(blocks + std::min(rows, 2048)));
+  return dim3((unsigned)(blocks + std::min(rows, most)));
 }
 
 template <typename T, typename O>
@@ -750,7 +750,9 @@ hipError_t grad_t(const EmbedParams& p, hipStream_t st) {
   Clear z;
   const dim3 b(kSortThreads);
   if (p.tokens <= kSmallSort) {
-    const dim3 g = with_clear(p, 1, 0, 1, 1, &z);
+    // one of these blocks fits a unit, and each is 16 waves to start (1000 tokens
+    // into 10007 x 515: 28 us, 31 with up to 2048 blocks)
+    const dim3 g = with_clear(p, 1, 0, 1, 1, &z, 512);
     hipLaunchKernelGGL(embed_sort_small_kernel, g, dim3(1024), 0, st, p, s, w.a, z);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   } else {
