@@ -212,10 +212,10 @@ __global__ __launch_bounds__(1024) void embed_sort_small_kernel(EmbedParams p, S
         // one wave's counters: the first lane of each digit reads and adds
         int old = 0;
         if (live && lane == first) {
-          volatile uint16_t* c = &wcnt[wid][d];
-          old = *c;
-          *c = (uint16_t)(old + __popcll(m));
+          old = wcnt[wid][d];
+          wcnt[wid][d] = (uint16_t)(old + __popcll(m));
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the next step's lanes see it
         old = __shfl(old, first);
         rank[i] = old + __popcll(m & ((1ull << lane) - 1));
       }

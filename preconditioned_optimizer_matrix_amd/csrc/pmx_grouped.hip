@@ -83,13 +83,14 @@ __device__ __forceinline__ void build_table(Table& T, const GroupedParams& p, in
       if (i <= p.groups) T.begin[i] = v;
       carry = __shfl(v, 63);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave reads what its other lanes wrote
     __builtin_amdgcn_wave_barrier();
     carry = 0;
     for (int b = 0; b <= p.groups; b += 64) {
       const int i = b + lane;
       int n = 0;
       if (i < p.groups) {
-        const int rows = *(volatile int*)&T.begin[i + 1] - *(volatile int*)&T.begin[i];
+        const int rows = T.begin[i + 1] - T.begin[i];
         n = fixed ? fixed : (rows + bm - 1) / bm * tiles_n;
       }
       int v = n;
