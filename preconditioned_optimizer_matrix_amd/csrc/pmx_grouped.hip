@@ -1329,12 +1329,16 @@ hipError_t launch_dma(const GroupedParams& p, dim3 grid, hipStream_t s) {
     else return hipErrorInvalidValue;                                                            \
   }
 
+// Blocks of a launch over `items` items, a multiple of 8.
+template <class C>
+int64_t grid_of(const GroupedParams& p, int64_t items) {
+  const int64_t g = (std::min(items, (int64_t)p.num_cu * kBlocks<C>) + 7) / 8 * 8;
+  return g < 8 ? 8 : g;
+}
+
 template <class C, int FORM>
 hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s, bool any_side = false) {
-  const int64_t slots = (int64_t)p.num_cu * kBlocks<C>;
-  int64_t g = items < slots ? items : slots;
-  g = (g + 7) / 8 * 8;
-  if (g < 8) g = 8;
+  const int64_t g = grid_of<C>(p, items);
   const dim3 grid((unsigned)g), block(C::THREADS);
   if constexpr (C::BM == 256 && FORM == TN) {
     if (dma_ok(p)) return launch_dma(p, grid, s);
@@ -1353,8 +1357,8 @@ hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s, boo
 
 using BQuarter = Cfg<uint16_t, 128, 128, 64, 64, 64, 1>;
 template <int FORM>
-hipError_t launch_quarters(GroupedParams p, hipStream_t s) {
-  p.round = (p.num_cu + 7) / 8 * 8;  // the first launch's grid
+hipError_t launch_quarters(GroupedParams p, int64_t items, hipStream_t s) {
+  p.round = (int)grid_of<BLarge>(p, items);
   const dim3 grid((unsigned)p.round), block(BQuarter::THREADS);
   if (p.out_dtype == PMX_F32) hipLaunchKernelGGL((grouped_tile_kernel<BQuarter, FORM, float, false, true>), grid, block, 0, s, p);
   else hipLaunchKernelGGL((grouped_tile_kernel<BQuarter, FORM, uint16_t, false, true>), grid, block, 0, s, p);
@@ -1402,7 +1406,7 @@ hipError_t launch_grouped_product(const GroupedParams& p, hipStream_t s) {
     e = c.cfg == 0 ? launch_product_cfg<FSmall>(p, items, s, p.k < 8 || p.n < 8)
                    : launch_product_cfg<FHalf>(p, items, s);
   }
-  if (e == hipSuccess && c.cfg == 3 && p.k >= kQuartersK) e = p.trans_b ? launch_quarters<NT>(p, s) : launch_quarters<NN>(p, s);
+  if (e == hipSuccess && c.cfg == 3 && p.k >= kQuartersK) e = p.trans_b ? launch_quarters<NT>(p, items, s) : launch_quarters<NN>(p, items, s);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_join(p, p.rows, (int)p.rows, s);
 }
