@@ -1293,9 +1293,10 @@ Choice choose_outer(int64_t rows, int m, int n, int groups, int dtype) {
 // 64 x 64 tile takes four, in the outer form from 8 k tiles on: 23489 bf16 rows,
 // 13 of 165 x 432, 41 us, 62 with two; 21648 fp32 rows, 7 of 184 x 648, 95 and
 // 139.  In the products, whose partial results are many, from 16: 3384 bf16
-// rows, 2 of 1925 x 328, input gradient, 34 us, 41 from 8 on.)
-int splits_for(int64_t tiles, int64_t nk, int unit, int least) {
-  if (tiles == 0) return 1;
+// rows, 2 of 1925 x 328, input gradient, 34 us, 41 from 8 on.)  The large tile's
+// kernels write whole results only: it is chosen where there are tiles enough.
+int splits_for(const Choice& c, int64_t tiles, int64_t nk, int unit, int least) {
+  if (tiles == 0 || c.cfg == 3) return 1;
   const int64_t want = unit * kCU / tiles, most = nk / least;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 64));
 }
@@ -1317,7 +1318,7 @@ hipError_t launch_dma(const GroupedParams& p, dim3 grid, hipStream_t s) {
 }
 
 #define PMX_LAUNCH(KERNEL)                                                                       \
-  if (p.splits > 1) { /* never with the large tile: there are tiles enough */                    \
+  if (p.splits > 1) { /* never with the large tile (splits_for) */                               \
     if constexpr (C::BM != 256)                                                                  \
       hipLaunchKernelGGL((KERNEL<C, FORM, float, true>), grid, block, 0, s, p);                  \
     else return hipErrorInvalidValue;                                                            \
@@ -1341,7 +1342,7 @@ hipError_t launch_form(const GroupedParams& p, int64_t items, hipStream_t s, boo
   const int64_t g = grid_of<C>(p, items);
   const dim3 grid((unsigned)g), block(C::THREADS);
   if constexpr (C::BM == 256 && FORM == TN) {
-    if (dma_ok(p)) return launch_dma(p, grid, s);
+    if (p.splits == 1 && dma_ok(p)) return launch_dma(p, grid, s);
   }
   if constexpr (C::BM == 32) {
     if (any_side) {
@@ -1382,14 +1383,14 @@ hipError_t launch_join(const GroupedParams& p, int64_t rows, int m, hipStream_t 
 
 int grouped_product_splits(int64_t rows, int k, int n, int groups, int dtype) {
   const Choice c = choose_product(rows, k, n, groups, dtype);
-  return splits_for(max_tiles_product(c, rows, n, groups), (k + c.bk - 1) / c.bk,
+  return splits_for(c, max_tiles_product(c, rows, n, groups), (k + c.bk - 1) / c.bk,
                     c.cfg == 1 ? 4 : 2, c.cfg == 1 ? 16 : 8);
 }
 
 int grouped_outer_splits(int64_t rows, int m, int n, int groups, int dtype) {
   const Choice c = choose_outer(rows, m, n, groups, dtype);
   const int64_t tiles = (int64_t)groups * ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
-  return splits_for(tiles, rows / groups / c.bk, c.cfg == 1 ? 4 : 2, 8);
+  return splits_for(c, tiles, rows / groups / c.bk, c.cfg == 1 ? 4 : 2, 8);
 }
 
 hipError_t launch_grouped_product(const GroupedParams& p, hipStream_t s) {

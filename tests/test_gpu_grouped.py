@@ -399,3 +399,28 @@ def test_middle_products(env, rows, groups, k, n, dtype):
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_middle_outer(env, rows, groups, m, n, dtype, accumulate):
     test_larger_outer(env, rows, groups, m, n, dtype, accumulate)
+
+
+# 256 large tiles, where they begin to be taken, a column of tiles more, and 255 (smaller tiles)
+@pytest.mark.parametrize("rows,groups,m,n", [(1100, 1, 4096, 4096), (4200, 4, 2048, 2048), (2100, 1, 4096, 4360), (2100, 1, 3840, 4344)])
+@pytest.mark.parametrize("out,accumulate", [("f32", False), ("f32", True), ("bf16", False)])
+def test_outer_where_large_tiles_begin(env, rows, groups, m, n, out, accumulate):
+    """Long groups and as many large tiles as units: whole results, nothing read from the workspace.  Operands that
+    are aligned, and rows at odd distances."""
+    torch, pmx, dev = env
+    off = _offsets(rows, groups, 92)
+    o = torch.from_numpy(off).to(dev)
+    odt = {"bf16": torch.bfloat16, "f32": torch.float32}[out]
+    for pad in (0, 3):
+        print("large tiles begin", rows, groups, m, n, out, accumulate, pad, flush=True)
+        A, An = _make(torch, dev, torch.bfloat16, (rows, m), 24, pad=pad)
+        B, Bn = _make(torch, dev, torch.bfloat16, (rows, n), 25, pad=pad)
+        C, C0 = _make(torch, dev, odt, (groups, m, n), 26)
+        ws = torch.full((1 << 28,), 0xFF, dtype=torch.uint8, device=dev)  # NaN
+        pmx.grouped_outer(A, B, o, out=C, accumulate=accumulate, ws=ws)
+        Cn = C.double().cpu().numpy()
+        for e in range(groups):
+            a, b = off[e], off[e + 1]
+            ref = An[a:b].T @ Bn[a:b] + (C0[e] if accumulate else 0.0)
+            s = np.abs(An[a:b]).T @ np.abs(Bn[a:b]) + (np.abs(C0[e]) if accumulate else 0.0)
+            assert (np.abs(Cn[e] - ref) <= _bound(ref, s, b - a + 1, out == "bf16")).all(), e

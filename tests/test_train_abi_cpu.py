@@ -50,6 +50,19 @@ def test_grouped_workspace_sizes(pmx):
     assert _size(pmx, "pmx_grouped_outer_workspace_size", 32768, 4096, 1024, 32, pmx.BF16) == (pmx.OK, 0)
 
 
+def test_large_tiles_are_never_split(pmx):
+    """The bf16 256 x 256 tiles are taken from 256 of them on; their kernels write whole results, so no workspace."""
+    f = "pmx_grouped_outer_workspace_size"
+    for rows, m, n, groups in ((1024, 4096, 4096, 1), (16384, 1024, 1024, 16), (8192, 2048, 1024, 8), (4096, 2048, 2048, 4),
+                               (65536, 4096, 4096, 1), (5000, 4096, 4352, 1), (5000, 257, 256, 128), (65536, 256, 256, 257)):
+        assert _size(pmx, f, rows, m, n, groups, pmx.BF16) == (pmx.OK, 0), (rows, m, n, groups)
+    # 255 of them: smaller tiles
+    assert _size(pmx, f, 65536, 256, 256, 255, pmx.BF16)[0] == pmx.OK
+    # products: (rows / 256) * columns of tiles from 256 on
+    for rows, k, n, groups in ((65536, 4096, 256, 1), (16384, 1 << 20, 1024, 4), (65536, 4096, 256, 256)):
+        assert _size(pmx, "pmx_grouped_product_workspace_size", rows, k, n, groups, pmx.BF16) == (pmx.OK, 0)
+
+
 def test_embedding_workspace_sizes(pmx):
     f = "pmx_embedding_grad_workspace_size"
     few, many = _size(pmx, f, 200, 1000, 64), _size(pmx, f, 20000, 1000, 64)
