@@ -411,6 +411,7 @@ __global__ __launch_bounds__(NT, waves_for(NC)) void distill_row_kernel(DistillP
     }
   };
   int64_t t = next_live<T, NT, GRAD>(p, blockIdx.x, after);
+  if constexpr (CLAIM) __syncthreads();  // every wave has read `claimed` before the first row's claim overwrites it
   if (t >= p.rows) return;
   {
     const T* z = reinterpret_cast<const T*>(p.z) + t * p.ldz;

@@ -360,3 +360,27 @@ def test_many_rows(env, rows, vocab, dtype, ignored):
     inplace = z.clone()
     pmx.distill_loss(inplace, ids, teacher, out=inplace, **kw)
     assert torch.equal(inplace, dz)
+
+
+@pytest.mark.parametrize("vocab,dtype", [(66001, "bf16"), (40003, "f32")])
+@pytest.mark.parametrize("first", [1, 257, 600])
+def test_claimed_rows_after_ignored_ones(env, vocab, dtype, first):
+    """Blocks that claim their rows, each beginning with ignored ones (a padded batch's leading rows): all waves of a
+    block go on with the row that it claimed."""
+    torch, pmx, dev = env
+    rows, top = 640, 5
+    print("claimed", vocab, dtype, first, flush=True)
+    z, _, teacher, labels, weights = _inputs(torch, dev, rows, vocab, 0, dtype, 37)
+    ids = torch.randint(0, vocab, (rows, top), device=dev)
+    teacher = torch.randn(rows, top, device=dev).to(z.dtype)
+    weights[:first] = 0.0
+    weights[first::3] = 0.0
+    z[weights == 0] = float("nan")
+    kw = dict(tau=2.0, mix=0.75, labels=labels, weights=weights)
+    ref = reference(_np(z), _np(ids), _np(teacher), 2.0, 0.75, _np(labels), _np(weights))
+    total, r, _, dz = pmx.distill_loss(z, ids, teacher, grad=True, **kw)
+    _compare(torch, total, r, dz, ref, dtype == "bf16")
+    total, r, _, _ = pmx.distill_loss(z, ids, teacher, **kw)
+    _compare(torch, total, r, None, ref, False)
+    pmx.distill_loss(z, ids, teacher, out=z, **kw)
+    assert torch.equal(z, dz)
