@@ -87,7 +87,10 @@ EmbedWs embed_ws(void* base, const SortPlan& s, int64_t tokens, int dim) {
 // ---------------------------------------------------------------- lookup
 // VB bytes a thread and step: the largest power of two up to 16 that divides
 // the row length, both row strides and both addresses.  threadIdx.x walks a
-// row, threadIdx.y the rows.
+// row, threadIdx.y the rows.  A grid has fewer than 2^32 threads in x, so blocks
+// beyond kLookupBlocks go on in y.
+constexpr int64_t kLookupBlocks = 1 << 23;
+
 template <int VB>
 struct Raw;
 template <> struct Raw<16> { typedef u32x4_t type; };
@@ -99,7 +102,7 @@ template <typename T, int VB>
 __global__ __launch_bounds__(256) void embed_lookup_kernel(EmbedParams p) {
   typedef typename Raw<VB>::type R;
   constexpr int NE = VB / (int)sizeof(T);
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
   if (t >= p.tokens) return;
   const int64_t id = load_index(p.ids, t, p.ids64);
   const bool row = id >= 0 && id < p.vocab;  // an id outside the table reads nothing: zeros
@@ -703,7 +706,8 @@ hipError_t lookup_t(const EmbedParams& p, int vb, hipStream_t s) {
   int tx = pow2_up(n < 256 ? n : 256);
   if (tx < 16) tx = 16;
   const dim3 block(tx, 256 / tx);
-  const dim3 grid((unsigned)((p.tokens + block.y - 1) / block.y));
+  const int64_t blocks = (p.tokens + block.y - 1) / block.y, gx = std::min(blocks, kLookupBlocks);
+  const dim3 grid((unsigned)gx, (unsigned)((blocks + gx - 1) / gx));
   switch (vb) {
     case 16: hipLaunchKernelGGL((embed_lookup_kernel<T, 16>), grid, block, 0, s, p); break;
     case 8: hipLaunchKernelGGL((embed_lookup_kernel<T, 8>), grid, block, 0, s, p); break;

@@ -229,3 +229,18 @@ def test_refusals(env):
     assert grad(wsp=p(ws) + 8) == pmx.ERR_WORKSPACE
     torch.cuda.synchronize()
     assert (G == 5).all()
+
+
+@pytest.mark.parametrize("tokens,dim", [((1 << 24) + 77, 129), ((1 << 23) + 5, 257)])
+def test_lookup_of_more_rows_than_blocks(env, tokens, dim):
+    """More rows of a whole block each than a grid has blocks, outputs beyond 2^31 elements."""
+    torch, pmx, dev = env
+    print("many rows", tokens, dim, flush=True)
+    W = torch.randn(1000, dim, device=dev).bfloat16()
+    ids = torch.randint(-2, 1002, (tokens,), device=dev, dtype=torch.int32)
+    Y = pmx.embedding(W, ids, scale=3.0)
+    table = torch.zeros(1004, dim, dtype=torch.bfloat16, device=dev)
+    table[2:1002] = (W.float() * 3.0).bfloat16()
+    for a in range(0, tokens, 1 << 21):
+        b = min(tokens, a + (1 << 21))
+        assert torch.equal(Y[a:b], table[ids[a:b].long() + 2])
