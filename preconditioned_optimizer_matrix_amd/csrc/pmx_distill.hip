@@ -185,7 +185,7 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[16]) {
 constexpr int kListed = PMX_MAX_TOP + 1;
 struct Listed {
   int id[kListed];
-  float e[kListed];  // teacher logit / tau, then exp(... - max)
+  float e[kListed];  // teacher logit, then exp((... - max) / tau)
   float z[kListed];  // the student's logit there
 };
 
@@ -200,7 +200,6 @@ struct Fetched {
   // (which other blocks may be overwriting with the gradient)
   __device__ __forceinline__ void fetch(const DistillParams& p, int64_t t, const float* saved = nullptr) {
     const T* row = reinterpret_cast<const T*>(p.z) + t * p.ldz;
-    const float rt = 1.f / p.tau;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int i = threadIdx.x + NT * k;
@@ -211,9 +210,8 @@ struct Fetched {
         d = load_index(p.ids, t * p.ld_ids + i, p.ids64);
         if (d >= 0 && d < p.vocab) {
           const int64_t o = t * p.ld_teacher + i;
-          a[k] = rt * (p.teacher_dtype == PMX_F32
-                           ? reinterpret_cast<const float*>(p.teacher)[o]
-                           : Elem<uint16_t>::load(reinterpret_cast<const uint16_t*>(p.teacher) + o));
+          a[k] = p.teacher_dtype == PMX_F32 ? reinterpret_cast<const float*>(p.teacher)[o]
+                                            : Elem<uint16_t>::load(reinterpret_cast<const uint16_t*>(p.teacher) + o);
         }
       } else if (i == p.top && p.labels) {
         d = load_index(p.labels, t, p.labels64);
@@ -239,12 +237,13 @@ struct Fetched {
   }
 };
 
-// L.e becomes exp(a - am); sum[0] += e, sum[1] += e (a - am), sum[2] += e (z - m) / tau.
+// L.e becomes e = exp((a - am) / tau); sum[0] += e, sum[1] += e (a - am) / tau,
+// sum[2] += e (z - m) / tau.  The difference comes before the temperature, as in Expo.
 template <int NT, int EX>
 __device__ __forceinline__ void teacher_sums(Listed& L, const DistillParams& p, const Expo<EX>& ex,
                                              float am, float (&sum)[5]) {
   for (int i = threadIdx.x; i < p.top; i += NT) {
-    const float a = L.e[i] - am;
+    const float a = (L.e[i] - am) * ex.rt;
     const float e = __builtin_amdgcn_exp2f(a * kLog2e);
     L.e[i] = e;
     sum[0] += e;
@@ -655,7 +654,6 @@ template <int EX>
 __device__ void few_rows_loss(const DistillParams& p) {
   __shared__ double part[kFewRows];
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  const float rt = 1.f / p.tau;
   for (int64_t t = wid; t < p.rows; t += waves) {
     const float w = weight_of(p, t);
     float m = 0.f, st = 0.f, s1 = 0.f, loss = 0.f;
@@ -663,12 +661,11 @@ __device__ void few_rows_loss(const DistillParams& p) {
       const float* z = saved_of(p, t);
       m = join_parts<EX>(p, t, st, s1);
       const Expo<EX> ex(p, m);
-      auto entry = [&](int i) {  // teacher logit / tau, -inf outside the vocabulary
+      auto entry = [&](int i) {  // teacher logit, -inf outside the vocabulary
         const int64_t id = load_index(p.ids, t * p.ld_ids + i, p.ids64), o = t * p.ld_teacher + i;
         if (id < 0 || id >= p.vocab) return kNegInf;
-        return rt * (p.teacher_dtype == PMX_F32
-                         ? reinterpret_cast<const float*>(p.teacher)[o]
-                         : Elem<uint16_t>::load(reinterpret_cast<const uint16_t*>(p.teacher) + o));
+        return p.teacher_dtype == PMX_F32 ? reinterpret_cast<const float*>(p.teacher)[o]
+                                          : Elem<uint16_t>::load(reinterpret_cast<const uint16_t*>(p.teacher) + o);
       };
       float am = kNegInf;
       for (int i = lane; i < p.top; i += 64) am = fmaxf(am, entry(i));
@@ -676,7 +673,7 @@ __device__ void few_rows_loss(const DistillParams& p) {
       if (am == kNegInf) am = 0.f;
       float sum[5] = {0.f, 0.f, 0.f, st, s1};
       for (int i = lane; i < p.top; i += 64) {
-        const float a = entry(i) - am, e = __builtin_amdgcn_exp2f(a * kLog2e);
+        const float a = (entry(i) - am) * ex.rt, e = __builtin_amdgcn_exp2f(a * kLog2e);
         sum[0] += e;
         if (e != 0.f) {
           sum[1] += e * a;

@@ -384,3 +384,28 @@ def test_claimed_rows_after_ignored_ones(env, vocab, dtype, first):
     _compare(torch, total, r, None, ref, False)
     pmx.distill_loss(z, ids, teacher, out=z, **kw)
     assert torch.equal(z, dz)
+
+
+@pytest.mark.parametrize("rows,vocab", [(9, 300), (9, 33001), (9, 140001), (200, 700)])
+@pytest.mark.parametrize("tau", [0.1, 0.3, 3.0])
+def test_large_teacher_logits(env, rows, vocab, tau):
+    """The teacher's logits count by their differences: a large common offset, values near the type's largest, and
+    a row of nothing but its lowest value (equal shares), at temperatures that are no powers of two."""
+    torch, pmx, dev = env
+    print("large teacher logits", rows, vocab, tau, flush=True)
+    z, ids, teacher, labels, weights = _inputs(torch, dev, rows, vocab, 7, "f32", 41)
+    teacher = teacher * 0.25
+    teacher[0] += 12345.0
+    teacher[1] -= 98765.0
+    teacher[2] = 3e38
+    teacher[2, 4:] = 2e38
+    teacher[3] = torch.finfo(torch.float32).min
+    teacher[4] = torch.finfo(torch.float32).min
+    teacher[4, 2] = 5.0
+    kw = dict(tau=tau, mix=0.8, labels=labels, weights=weights)
+    ref = reference(_np(z), _np(ids), _np(teacher), tau, 0.8, _np(labels), _np(weights))
+    total, r, _, dz = pmx.distill_loss(z, ids, teacher, grad=True, **kw)
+    _compare(torch, total, r, dz, ref, False)
+    total, r, stats, _ = pmx.distill_loss(z, ids, teacher, **kw)
+    _compare(torch, total, r, None, ref, False)
+    _compare(torch, None, None, pmx.distill_grad(z, ids, teacher, stats, **kw), ref, False)
