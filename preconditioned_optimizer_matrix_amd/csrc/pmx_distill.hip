@@ -321,9 +321,12 @@ __device__ __forceinline__ void fix_listed(const Listed& L, const DistillParams&
   for (int i = threadIdx.x; i <= p.top; i += NT) {
     const int id = L.id[i];
     if (id < 0 || id < lo || id >= hi) continue;
-    float ps = 0.f;
-    for (int j = 0; j < p.top; ++j) ps += L.id[j] == id ? L.e[j] : 0.f;
-    float v = grad_of(L.z[i], ex, s) - s.gp * ps;
+    float v = grad_of(L.z[i], ex, s);
+    if (p.mix != 0.f) {  // (without the teacher's part its logits may hold anything)
+      float ps = 0.f;
+      for (int j = 0; j < p.top; ++j) ps += L.id[j] == id ? L.e[j] : 0.f;
+      v -= s.gp * ps;
+    }
     if (L.id[p.top] == id) v -= s.gc;
     Elem<T>::store(dz + id, v);
   }

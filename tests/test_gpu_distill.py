@@ -409,3 +409,23 @@ def test_large_teacher_logits(env, rows, vocab, tau):
     total, r, stats, _ = pmx.distill_loss(z, ids, teacher, **kw)
     _compare(torch, total, r, None, ref, False)
     _compare(torch, None, None, pmx.distill_grad(z, ids, teacher, stats, **kw), ref, False)
+
+
+@pytest.mark.parametrize("rows,vocab", [(6, 300), (6, 33001), (6, 140001), (300, 515)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_teacher_part_whatever_it_holds(env, rows, vocab, dtype):
+    """mix = 0: a teacher's list full of NaN and infinities changes nothing."""
+    torch, pmx, dev = env
+    print("no teacher part", rows, vocab, dtype, flush=True)
+    z, ids, teacher, labels, weights = _inputs(torch, dev, rows, vocab, 7, dtype, 43)
+    ids[1, 2] = labels[1]
+    teacher[0:3] = float("nan")
+    teacher[3] = float("inf")
+    teacher[4] = -float("inf")
+    kw = dict(tau=3.0, mix=0.0, labels=labels, weights=weights)
+    ref = reference(_np(z), None, None, 3.0, 0.0, _np(labels), _np(weights))
+    total, r, _, dz = pmx.distill_loss(z, ids, teacher, grad=True, **kw)
+    _compare(torch, total, r, dz, ref, dtype == "bf16")
+    total, r, stats, _ = pmx.distill_loss(z, ids, teacher, **kw)
+    _compare(torch, total, r, None, ref, False)
+    _compare(torch, None, None, pmx.distill_grad(z, ids, teacher, stats, **kw), ref, dtype == "bf16")
