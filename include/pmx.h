@@ -538,8 +538,10 @@ pmx_status pmx_embedding_grad(pmx_handle handle, const void* dY, pmx_dtype dtype
  *   - a label outside [0, vocab): the row has no label term.
  *   - teacher ids outside [0, vocab), or logits of -inf: no weight; a row with
  *     none left has no distillation term.  An id listed twice counts twice.
- *   - logits z of -inf: masked, zero gradient (L_t = inf where the teacher
- *     gives them weight); a row of nothing but -inf: L_t = 0, zero gradient.
+ *   - logits z of -inf: masked, q = s = 0 there, so zero gradient unless the
+ *     teacher or the label gives them weight: then L_t = inf, and dZ is what the
+ *     formula leaves, -u w (mix tau p + (1 - mix) [label]).  A row of nothing but
+ *     -inf: L_t = 0, zero gradient.
  *   - NaN, or +inf, in a row that counts: NaN.
  * labels may be NULL when mix = 1; top may be 0 when mix = 0 (plain cross
  * entropy; a list given all the same does not count).  tau > 0, 0 <= mix <= 1, top <= PMX_MAX_TOP, vocab <= PMX_MAX_VOCAB.
