@@ -679,6 +679,9 @@ def _keep_size(key, n):
 
 
 def _ws_for(need, ws, device):
+    # numel elements from data_ptr on are the workspace's only when contiguous
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        raise ValueError("ws must be contiguous, on the other tensors' device")
     if not need:
         return None, 0
     if ws is None or ws.numel() < need:

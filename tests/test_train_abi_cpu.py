@@ -104,6 +104,18 @@ def test_no_handle_no_call(pmx):
     assert L.pmx_distill_grad(None, ctypes.byref(q), 256, None, 512, 8, None) == i
 
 
+@pytest.mark.skipif("SAN_CHILD" in os.environ, reason="torch is not for the sanitized child")
+def test_workspace_of_another_device_or_layout(pmx):
+    import torch
+    w = torch.empty(1024, dtype=torch.uint8)
+    assert pmx._ws_for(1000, w, w.device) == (w.data_ptr(), 1024)
+    assert pmx._ws_for(0, None, w.device) == (None, 0)
+    for bad, dev in ((w, torch.device("cuda:0")), (w[:1].expand(1024), w.device), (w[::2], w.device)):
+        for need in (0, 500):
+            with pytest.raises(ValueError):
+                pmx._ws_for(need, bad, dev)
+
+
 @pytest.mark.skipif("SAN_CHILD" in os.environ, reason="this is the child")
 def test_clean_under_host_sanitizers():
     from preconditioned_optimizer_matrix_amd import build
