@@ -349,6 +349,53 @@ __device__ __forceinline__ void multiply(f32x16 (&acc)[C::FM][C::FN], const type
   }
 }
 
+// fp32 sums over long contractions: what has come together over kFold values of k
+// goes to a second sum, so a result passes through kFold / 2 + K / kFold roundings
+// instead of K / 2 (a matrix instruction adds two products).  64 rows, 64 experts
+// of 1024 x 4096: 1.1e-6 relative in one chain, 2.3e-7 so.  The second sum's
+// registers cost the 64 x 64 tile one of five waves a SIMD where it matters most,
+// the weight gradient (8192 rows, 8 experts of 1024 x 1024: 147 -> 153 us; the
+// products 152 -> 153 and 154 -> 155); folding every 256 takes as long, every 64
+// 2% more.
+constexpr int kFold = 128;
+template <class C>
+struct Fold {
+  static constexpr bool ON = sizeof(typename C::E) == 4;
+  f32x16 sum[ON ? C::FM : 1][ON ? C::FN : 1];
+  __device__ __forceinline__ Fold() {
+    if constexpr (ON)
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) sum[i][j][v] = 0.f;
+  }
+  // before k tile `n` of a block's share
+  __device__ __forceinline__ void step(f32x16 (&acc)[C::FM][C::FN], int n) {
+    if constexpr (ON)
+      if (n > 0 && n % (kFold / C::BK) == 0)
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+              sum[i][j][v] += acc[i][j][v];
+              acc[i][j][v] = 0.f;
+            }
+  }
+  __device__ __forceinline__ void end(f32x16 (&acc)[C::FM][C::FN]) const {
+    if constexpr (ON)
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[i][j][v] += sum[i][j][v];
+  }
+};
+
 // Product of one tile over k tiles [kb, ke) of a contraction of `K`.
 template <class C, int FORM, bool EDGE>
 __device__ __forceinline__ void mainloop(f32x16 (&acc)[C::FM][C::FN], typename C::E* smem,
@@ -373,7 +420,9 @@ __device__ __forceinline__ void mainloop(f32x16 (&acc)[C::FM][C::FN], typename C
   B.store(smem + SA, vb);
   if (kb + 1 < ke) load(kb + 1);
   __syncthreads();
+  Fold<C> fold;
   for (int kt = kb; kt < ke; ++kt) {
+    fold.step(acc, kt - kb);
     const int cur = (kt - kb) & 1;
     typename C::E* s = smem + cur * ST;
     typename C::E* d = smem + (cur ^ 1) * ST;
@@ -385,6 +434,7 @@ __device__ __forceinline__ void mainloop(f32x16 (&acc)[C::FM][C::FN], typename C
     }
     __syncthreads();
   }
+  fold.end(acc);
 }
 
 // ------------------------------------------------------------ pipelined tiles
@@ -489,10 +539,13 @@ __device__ __forceinline__ void stream_loop(f32x16 (&acc)[C::FM][C::FN], typenam
   A.load(va[0], min(kb + D, ke - 1));  // past the last tile: the last one again
   B.load(vb[0], min(kb + D, ke - 1));
   __syncthreads();
+  static_assert(!Fold<C>::ON || kFold / C::BK % D == 0, "folds between steps");
+  Fold<C> fold;
   for (int k0 = kb; k0 < ke; k0 += D) {
+    fold.step(acc, k0 - kb);
 #pragma unroll
     for (int i = 0; i < D; ++i) {
-      if (i > 0 && k0 + i >= ke) return;
+      if (i > 0 && k0 + i >= ke) break;
       const int n = (i + 1) % D;
       const int cur = D % 2 ? (k0 - kb) & 1 : i & 1;
       typename C::E* s = smem + cur * ST;
@@ -515,6 +568,7 @@ __device__ __forceinline__ void stream_loop(f32x16 (&acc)[C::FM][C::FN], typenam
       __syncthreads();
     }
   }
+  fold.end(acc);
 }
 
 // The same for the large bf16 tile, whose 8 waves are two to a SIMD: the two

@@ -424,3 +424,28 @@ def test_outer_where_large_tiles_begin(env, rows, groups, m, n, out, accumulate)
             ref = An[a:b].T @ Bn[a:b] + (C0[e] if accumulate else 0.0)
             s = np.abs(An[a:b]).T @ np.abs(Bn[a:b]) + (np.abs(C0[e]) if accumulate else 0.0)
             assert (np.abs(Cn[e] - ref) <= _bound(ref, s, b - a + 1, out == "bf16")).all(), e
+
+
+@pytest.mark.parametrize("rows,groups,k,n", [(64, 64, 4096, 4096), (779, 21, 4032, 336), (900, 3, 16384, 1030), (3000, 40, 4100, 1100)])
+def test_long_fp32_contractions(env, rows, groups, k, n):
+    """The root mean square error of long fp32 sums.  Over n roundings of a sum of terms of random sign it is about
+    2^-24 sqrt(n / 6) of the result's; sums over 128 values of k, two to a matrix instruction, joined by a second sum
+    make n = 64 + K / 128.  Twice that is asked for; one chain of K / 2 would be off by 2.3 times as much at K = 4096
+    and 3.3 times at 16384."""
+    torch, pmx, dev = env
+    print("long fp32 contraction", rows, groups, k, n, flush=True)
+    off = np.linspace(0, rows, groups + 1).astype(np.int64)
+    o = torch.from_numpy(off).to(dev)
+
+    def check(got, ref, K):
+        d = got.double().cpu().numpy() - ref
+        tol = 2 * 2.0 ** -24 * ((64 + K / 128) / 6) ** 0.5
+        assert (d ** 2).sum() ** 0.5 <= tol * (ref ** 2).sum() ** 0.5
+
+    A, An = _make(torch, dev, torch.float32, (rows, k), 27)
+    for trans in (True, False):
+        B, Bn = _make(torch, dev, torch.float32, (groups, n, k) if trans else (groups, k, n), 28)
+        check(pmx.grouped_product(A, B, o, trans_b=trans), _ref_product(An, Bn, off, trans)[0], k)
+    # the same as rows of the outer form: one group of k rows
+    one = torch.tensor([0, k], device=dev)
+    check(pmx.grouped_outer(A.t().contiguous(), B[0].contiguous(), one)[0], An @ Bn[0], k)
