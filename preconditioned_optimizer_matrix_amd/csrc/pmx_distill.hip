@@ -34,7 +34,9 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -INFINITY;
-constexpr int kFewRows = 128;  // at most so many rows are cut over several blocks
+constexpr int kFewRows = 32;        // at most so many rows are cut over several blocks
+constexpr int kMiddleRow = 512 * 16;  // chunks of a row that fit a block's registers without 1024 threads
+constexpr int kLongRow = 1024 * 16;   // with them
 
 // exponentials per element: one (a single temperature is in play), two, or one
 // and 1, 2 or 3 squarings
@@ -802,11 +804,15 @@ __global__ __launch_bounds__(1024) void distill_total_kernel(DistillParams p) {
   }
 }
 
-// Slabs of a row when there are few rows (1: one block a row): about two
-// blocks a compute unit, slabs of at least 1024 chunks.
+// Slabs of a row when there are few long rows (1: one block a row): about two
+// blocks a compute unit, slabs of at least 1024 chunks.  Loss with gradient, cut
+// and whole rows: 8 x 128000 bf16 18 and 28 us, 32 of them 26 and 29, 64 of them
+// 48 and 30 (one block has all the losses); 8 x 128000 fp32 18 and 27, 32 of them
+// 29 and 29.  Rows of up to kMiddleRow chunks: 8 x 32000 bf16 18 and 16, 64 of
+// them 42 and 17; 8 x 64000 bf16 18 and 18.
 int splits_of(int64_t rows, int vocab, int dtype) {
   const int chunks = vocab / (dtype == PMX_F32 ? 4 : 8);
-  if (rows > kFewRows || rows == 0 || chunks < 2048) return 1;
+  if (rows > kFewRows || rows == 0 || chunks <= kMiddleRow) return 1;
   return (int)std::min<int64_t>(std::min<int64_t>(512 / rows, chunks / 1024), 64);
 }
 
@@ -894,9 +900,6 @@ hipError_t launch_grad_t(const DistillParams& p, hipStream_t s) {
 }
 
 }  // namespace
-
-// Chunks of a row that fit one block's registers.
-constexpr int kLongRow = 1024 * 16, kMiddleRow = 512 * 16;
 
 int64_t distill_part_floats(int64_t rows, int vocab, int top, int dtype) {
   const int k = splits_of(rows, vocab, dtype);

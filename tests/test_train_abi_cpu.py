@@ -93,6 +93,24 @@ def test_distill_problem_is_checked(pmx):
     assert pmx.lib.pmx_distill_workspace_size(None, None) == pmx.ERR_INVALID_VALUE
 
 
+def test_distill_rows_cut_over_blocks(pmx):
+    """Only few long rows are: their partial sums, the listed logits; one counter for long rows otherwise."""
+    def size(rows, vocab, dtype, top=20):
+        q = pmx.DistillProblem(1, dtype, rows, vocab, top, 4096, vocab, 8192, top, 16384, top, None, None, pmx.I32, 0, pmx.F32,
+                               1.0, 1.0, 0)
+        sz = ctypes.c_size_t()
+        assert pmx.lib.pmx_distill_workspace_size(ctypes.byref(q), ctypes.byref(sz)) == pmx.OK
+        return sz.value
+
+    for rows in (1, 8, 32):
+        for vocab, dtype in ((128000, pmx.BF16), (66000, pmx.BF16), (50000, pmx.F32), (262144, pmx.F32)):
+            n = size(rows, vocab, dtype)
+            assert n >= rows * (2 * 3 + 21) * 4 and n % (rows * 4) == 0, (rows, vocab, dtype)
+        assert size(rows, 32000, pmx.BF16) == size(rows, 65536, pmx.BF16) == size(rows, 32000, pmx.F32) == 0
+    assert size(64, 32000, pmx.BF16) == size(128, 17000, pmx.BF16) == size(64, 200000, pmx.BF16) == 0
+    assert size(64, 128000, pmx.BF16) == size(33, 50000, pmx.F32) == 4
+
+
 def test_no_handle_no_call(pmx):
     L, i = pmx.lib, pmx.ERR_INVALID_VALUE
     assert L.pmx_grouped_product(None, 256, pmx.F32, 8, 8, 8, 512, 8, 8, 64, 0, 256, pmx.I32, 1, 4096, pmx.F32, 8, None, 0, None) == i
