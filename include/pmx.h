@@ -476,7 +476,9 @@ enum { PMX_I32 = 0, PMX_I64 = 1 };
  * operands with a bf16 C: PMX_ERR_NOT_SUPPORTED).  Accumulation is fp32 with
  * one rounding.  No alignment beyond the element's is asked for; row distances
  * of A and B above 2^22 elements are PMX_ERR_NOT_SUPPORTED.  rows may be
- * 0 (nothing is enqueued); 1 <= k, n <= 2^20, 1 <= groups <= PMX_MAX_GROUPS.
+ * 0 (nothing is enqueued); 1 <= k, n <= 2^20, 1 <= groups <= PMX_MAX_GROUPS;
+ * (rows / 32 + groups) ceil(n / 128) above 2^25 tiles (in the outer form
+ * (groups m / 32 + groups) ceil(n / 128)) are PMX_ERR_NOT_SUPPORTED.
  * The workspace may be NULL when the query says 0.
  */
 pmx_status pmx_grouped_product_workspace_size(int64_t rows, int k, int n, int groups,
@@ -503,7 +505,8 @@ pmx_status pmx_grouped_outer(pmx_handle handle, const void* A, pmx_dtype dtype, 
 
 /*
  * Token embedding: Y[t] = scale W[ids[t]] for the vocab x dim table W; an id
- * outside [0, vocab) gives a row of zeros.  Y has the table's type.
+ * outside [0, vocab) gives a row of zeros.  Y has the table's type.  tokens
+ * may be 0, at most 2^31 - 1.
  */
 pmx_status pmx_embedding(pmx_handle handle, const void* table, pmx_dtype dtype, int vocab, int dim,
                          int64_t ldt, const void* ids, pmx_itype itype, int64_t tokens,

@@ -15,16 +15,21 @@
 // up to 1024 threads: 128 Ki bf16 or 64 Ki fp32 logits), packed as it was
 // loaded.  Blocks are persistent: as soon as a chunk's gradient is computed,
 // its registers take the load of the block's next row, so the loads run under
-// the exponentials and the stores.  Longer rows are read twice (the second time
-// mostly from the last-level cache).  When there are few rows, a row is cut
+// the exponentials and the stores.  Longer rows are read three times, for the
+// maximum, the sums and the gradient.  When there are few long rows, a row is cut
 // over several blocks: one launch for partial sums, one for the rest.
 // exp(z - m) is the tau-th power of exp((z - m) / tau): for tau = 2, 4 or 8 it
 // is squared up instead of a second exponential (a quarter-rate instruction).
 //
 // Measured, 8192 rows of 128000 bf16 with the gradient, tau = 2, a tenth of the
-// rows ignored: 915 us for 4.0 GB, 4.4 TB/s where a copy reaches 5.1.  1023 rows of
-// 32003 bf16, the loss 19 us, the later gradient 26.  7 rows of 128000 fp32: 5 us
-// for the partial sums, 8 for the rest.
+// rows ignored: 927 us for 4.0 GB, 4.3 TB/s where a copy reaches 5.1 (936 to 1038 one
+// call at a time under a profiler).  4096 rows of 50000 fp32: 405 us, 4.0 TB/s.
+// 1023 rows of 32003 bf16, the loss 19 us, the later gradient 25.  7 rows of 128000
+// fp32: 5 us for the partial sums, 8 for the rest.  Rows past the registers, 4096 of
+// 151936 bf16: 873 us, all three reads and the write beyond the L2s (5.0 GB, 5.7
+// TB/s); 490 would be one read and the write.  A list of many entries costs a
+// block entries^2 / threads steps where it corrects the gradient: 1024 rows of 32000
+// bf16, 20 entries 37 us, 1023 entries 312.
 #include <algorithm>
 
 #include "pmx_train.h"
@@ -504,7 +509,7 @@ __global__ __launch_bounds__(NT, waves_for(NC)) void distill_row_kernel(DistillP
   }
 }
 
-// Rows too long for the registers: read twice.
+// Rows too long for the registers: read three times.
 template <typename T, int EX, bool GRAD>
 __global__ __launch_bounds__(1024) void distill_long_kernel(DistillParams p) {
   constexpr int VEC = Elem<T>::VEC, NT = 1024;

@@ -29,12 +29,14 @@
 //    the card the contraction is cut into splits whose fp32 partial results are
 //    joined in order by a second launch.
 //
-// Measured, 32768 bf16 rows, 32 experts of 4096 x 1024 (275 GFLOP): forward 281 us,
-// 0.98 PFLOP/s; input gradient 291; weight gradient, which also writes 537 MB of
-// fp32, 365.  In the large tile's blocks the matrix cores are busy 58 to 66% of
-// the time.  16 rows through 13 of the experts: 22 us for 107 MB of weights,
-// 4.9 TB/s.  2011 fp32 rows, 7 experts of 1001 x 500 (2 GFLOP): 34 to 39 us each
-// way, matrix cores busy 61 to 67%.
+// Measured, 32768 bf16 rows, 32 experts of 4096 x 1024 (275 GFLOP): forward 293 us,
+// 0.94 PFLOP/s; input gradient 295; weight gradient, which also writes 537 MB of
+// fp32, 352 to 362 (393 to 409 one call at a time under a profiler), added to what is there 487, into bf16 322.  In the large
+// tile's blocks the matrix cores are busy 58 to 66% of the time, 36 in the weight
+// gradient.  Short groups, weight gradient: 16 rows an expert 136 us, 60 168, 200
+// 182 (537 MB of results at a copy's rate: 106).  16 rows through 13 of the experts:
+// 22 us for 107 MB of weights, 4.9 TB/s.  2011 fp32 rows, 7 experts of 1001 x 500
+// (2 GFLOP): 33 to 38 us each way, matrix cores busy 62 to 64%.
 #include <algorithm>
 
 #include "pmx_train.h"
@@ -1319,6 +1321,20 @@ using FSmall = Cfg<float, 32, 128, 32, 32, 32, 3>;
 // 52 such tiles, 24 us instead of 31; 5075 rows, 17 of 1075 x 289, input
 // gradient, 171, 32 instead of 45; but 23489 rows, 13 of 165 x 432, forward, 392,
 // 29 instead of 25.
+//
+// The host knows the mean of the groups' rows only, so the rules go by it.
+// Small tile up to 48 rows, forward and input gradient, small and wider tiles:
+// bf16, 32 experts of 4096 x 1024, 12 rows 44, 41 and 48, 68 us; 40 rows 57, 54 and
+// 47, 71; 56 rows 68, 83 and 48, 73.  fp32, 64 of 768 x 2048, 12 rows 91, 85 and
+// 121, 117; 40 rows 130, 122 and 145, 134; 100 rows 227, 222 and 242, 232.
+// Large tile from 256 rows, large and 128 x 128: 32 of 4096 x 1024, forward, 200
+// rows 96 and 106, 300 rows 122 and 134; 64 of 768 x 2048, input gradient, 140 rows
+// 83 and 62, 250 rows 95 and 91, 300 rows 122 and 106.
+// In the outer form from 64 rows, large and 128 x 128, fp32 results: 32 of 4096 x
+// 1024, 72 rows 137 and 168, 140 rows 165 and 204; aligned operands gain below that
+// too (8 rows 114 and 126, 32 rows 125 and 150), others do not (8 rows 124 and
+// 128, 60 rows 183 and 178), nor do results of one tile (300 of 256 x 256, 32 rows,
+// 28 and 27).
 struct Choice {
   int cfg, bm, bn, bk;
 };
