@@ -547,7 +547,8 @@ pmx_status pmx_embedding_grad(pmx_handle handle, const void* dY, pmx_dtype dtype
  *     -inf: L_t = 0, zero gradient.
  *   - NaN, or +inf, in a row that counts: NaN.
  * labels may be NULL when mix = 1; top may be 0 when mix = 0 (plain cross
- * entropy; a list given all the same does not count).  tau > 0, 0 <= mix <= 1, top <= PMX_MAX_TOP, vocab <= PMX_MAX_VOCAB.
+ * entropy; a list given all the same does not count).  2^-100 <= tau < infinity,
+ * 0 <= mix <= 1, top <= PMX_MAX_TOP, vocab <= PMX_MAX_VOCAB.
  */
 typedef struct {
   int32_t struct_version;  /* 1 */

@@ -114,7 +114,8 @@ bool distill_shape_ok(const pmx_distill_problem* q) {
 bool distill_ok(const pmx_distill_problem* q) {
   if (!distill_shape_ok(q)) return false;
   if (!itype_ok(q->ids_type) || !itype_ok(q->labels_type)) return false;
-  if (!(q->tau > 0.f) || !isfinite(q->tau) || !(q->mix >= 0.f) || !(q->mix <= 1.f)) return false;
+  // below, a difference of logits over tau leaves fp32's range
+  if (!(q->tau >= 0x1p-100f) || !isfinite(q->tau) || !(q->mix >= 0.f) || !(q->mix <= 1.f)) return false;
   if (q->mix > 0.f && q->top < 1) return false;
   if (q->mix < 1.f && q->rows > 0 && !q->labels) return false;
   if (!layout_ok(q->z, q->rows, q->vocab, q->ldz, elem_size(q->dtype))) return false;

@@ -429,3 +429,16 @@ def test_no_teacher_part_whatever_it_holds(env, rows, vocab, dtype):
     total, r, stats, _ = pmx.distill_loss(z, ids, teacher, **kw)
     _compare(torch, total, r, None, ref, False)
     _compare(torch, None, None, pmx.distill_grad(z, ids, teacher, stats, **kw), ref, dtype == "bf16")
+
+
+def test_smallest_temperatures(env):
+    """Down to 2^-100 the softmax is the largest logit's alone, with finite results; below, tau is refused."""
+    torch, pmx, dev = env
+    z, ids, teacher, labels, weights = _inputs(torch, dev, 6, 500, 5, "f32", 47)
+    kw = dict(mix=0.5, labels=labels, weights=weights)
+    total, r, _, dz = pmx.distill_loss(z, ids, teacher, tau=2.0 ** -100, grad=True, **kw)
+    _compare(torch, total, r, dz, reference(_np(z), _np(ids), _np(teacher), 2.0 ** -100, 0.5, _np(labels), _np(weights)), False)
+    for tau in (2.0 ** -101, 1e-38, 1e-42, -1.0):
+        with pytest.raises(pmx.PmxError) as e:
+            pmx.distill_loss(z, ids, teacher, tau=tau, **kw)
+        assert e.value.code == pmx.ERR_INVALID_VALUE
