@@ -588,6 +588,163 @@ pmx_status pmx_distill_grad(pmx_handle handle, const pmx_distill_problem* proble
                             void* stream);
 
 /*
+ * The rest of an expert layer in a training step: the layer norm before it, the
+ * router with its balance loss, activations kept in 8 bits for the backward
+ * pass, and the products in 8 bits.  Conventions as for the operators above: on
+ * `stream`, nothing read on the host, capturable, a fixed order of every sum.
+ */
+#define PMX_MAX_NORM_COLS 16384
+#define PMX_MAX_ROUTE_TOP 16
+#define PMX_MAX_ROUTE_ROWS 268435456 /* 2^28 */
+
+/*
+ * Layer norm of the rows of X (rows x cols, cols <= PMX_MAX_NORM_COLS):
+ *   m = mean x, r = 1 / sqrt(mean (x - m)^2 + eps), Y = (x - m) r weight + bias
+ * weight and bias (cols values of param_dtype) may be NULL: ones, zeros.  stats
+ * (rows x 2 fp32: m, r) is what the gradient needs, or NULL.  Y has X's type.
+ * Statistics are fp32, of the deviations from the mean (no E x^2 - m^2).
+ * 0 <= eps < infinity; a row of equal values with eps = 0 gives NaN.
+ * rows may be 0.
+ */
+pmx_status pmx_layer_norm(pmx_handle handle, const void* X, pmx_dtype dtype, int64_t rows, int cols,
+                          int64_t ldx, const void* weight, const void* bias, pmx_dtype param_dtype,
+                          float eps, void* Y, int64_t ldy, float* stats, void* stream);
+/*
+ * Its gradients from the upstream dY, with h = (x - m) r and g = dY weight:
+ *   dX = r (g - mean g - h mean(g h)), dweight = sum_t dY h, dbias = sum_t dY
+ * dX, dweight, dbias: each may be NULL (not wanted).  dweight and dbias are fp32,
+ * overwritten, or added to with accumulate = 1.  dX has X's type and may be dY
+ * itself (same address and row distance).  rows may be 0.
+ */
+pmx_status pmx_layer_norm_grad_workspace_size(int64_t rows, int cols, pmx_dtype dtype, size_t* bytes);
+pmx_status pmx_layer_norm_grad(pmx_handle handle, const void* dY, pmx_dtype dtype, int64_t rows, int cols,
+                               int64_t lddy, const void* X, int64_t ldx, const float* stats,
+                               const void* weight, pmx_dtype param_dtype, void* dX, int64_t lddx,
+                               float* dweight, float* dbias, int accumulate, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Router.  Z holds rows x experts logits.  Per token t with p = softmax(z):
+ *   ids[t][0 .. top-1]  the experts of the largest logits, largest first, the
+ *                       lowest index among equals
+ *   gates[t][j]         p at ids[t][j]; normalize = 1: divided by their sum
+ * and over all tokens
+ *   counts[e]           tokens that chose e; counts[experts]: live tokens, n
+ *   offsets[e]          (experts + 1) sums of the counts before e
+ *   slots[t][j]         the row of pair (t, j) when the pairs are sorted by expert,
+ *                       then token: what the grouped products above take with
+ *                       these offsets
+ *   tokens[row]         the token of each such row; -1 from offsets[experts] on
+ *   loss = balance experts / (top n) sum_e counts[e] P_e + zloss / n sum_t lse_t^2,
+ *          P_e = sum_t p_te / n, lse = log sum exp z     (all sums over live tokens)
+ * The first term is `balance` when everything is even.  slots and tokens may
+ * both be NULL.
+ *   - live[t] = 0 (one byte a token; NULL: all live), or a row of nothing but
+ *     -inf: not routed, not counted, zero gradient; ids and slots -1, gates 0.
+ *   - logits of -inf: never chosen; where fewer than `top` others are left, the
+ *     remaining ids and slots are -1 and their gates 0.
+ *   - NaN or +inf in a live row: counted in n but routed nowhere (ids and slots
+ *     -1, gates NaN); the loss and the row's gradient are NaN.
+ * loss is 0 where n = 0.  rows may be 0, at most PMX_MAX_ROUTE_ROWS, rows top
+ * below 2^31; experts <= PMX_MAX_GROUPS, top <= min(experts, PMX_MAX_ROUTE_TOP).
+ */
+typedef struct {
+  int32_t struct_version;  /* 1 */
+  pmx_dtype dtype;         /* of z and dZ */
+  int64_t rows;
+  int32_t experts, top;
+  const void* z;
+  int64_t ldz;
+  const uint8_t* live;
+  float balance, zloss;    /* finite */
+  int32_t normalize;       /* 0 or 1 */
+  int32_t reserved;        /* 0 */
+} pmx_route_problem;
+
+pmx_status pmx_route_workspace_size(const pmx_route_problem* problem, size_t* bytes);
+pmx_status pmx_route(pmx_handle handle, const pmx_route_problem* problem, int32_t* ids, float* gates,
+                     int32_t* counts, int32_t* offsets, int32_t* slots, int32_t* tokens, float* loss,
+                     void* workspace, size_t workspace_bytes, void* stream);
+/*
+ * Gradient of the logits from that of the gates (dgates, rows x top fp32, or
+ * NULL) and of the loss (upstream, one device float, or NULL: 1):
+ *   dZ = p (a - sum_e p_e a_e) + u zloss 2 lse / n p + the gates' part,
+ *   a_e = u balance experts counts[e] / (top n^2)
+ * The choice itself and the counts are constants.  ids, gates and counts are
+ * those pmx_route wrote (counts may have been summed over several processes).
+ * dZ may be Z itself.
+ */
+pmx_status pmx_route_grad(pmx_handle handle, const pmx_route_problem* problem, const int32_t* ids,
+                          const float* gates, const int32_t* counts, const float* dgates,
+                          const float* upstream, void* dZ, int64_t lddz, void* stream);
+
+/*
+ * Values in 8 bits.  A row is cut into blocks of 128 values; a block has one
+ * power of two 2^k, the least with max |x| <= 448 2^k (k >= -126; k = 0 for a
+ * block of zeros), kept as the byte k + 127, and each value is the e4m3 (OCP,
+ * 448 at most) number nearest to x 2^-k, ties to even.  `cols` values take
+ * up(cols) = 128 ceil(cols / 128) bytes, the ones past cols zeros, and
+ * up(cols) / 128 scale bytes.  Infinities and NaN become NaN and are left out of
+ * the maximum.  `values` are 16-byte aligned and their row distance is a multiple
+ * of 16 and at least up(cols).  1 <= cols <= 2^20; rows may be 0.
+ * Reading back multiplies by 2^(byte - 127) (byte 255: NaN); the result has four
+ * significant bits, so bf16 and fp32 hold it exactly.
+ */
+pmx_status pmx_fp8_store(pmx_handle handle, const void* X, pmx_dtype dtype, int64_t rows, int cols,
+                         int64_t ldx, uint8_t* values, int64_t ldv, uint8_t* scales, int64_t lds,
+                         void* stream);
+pmx_status pmx_fp8_load(pmx_handle handle, const uint8_t* values, int64_t ldv, const uint8_t* scales,
+                        int64_t lds, int64_t rows, int cols, void* Y, pmx_dtype dtype, int64_t ldy,
+                        void* stream);
+/*
+ * Weights: `groups` matrices n x k (matrix e at W + e stride_w), one scale byte
+ * for each 128 x 128 tile.  transposed = 0: values n x up(k), scales
+ * ceil(n / 128) x up(k) / 128.  transposed = 1: the same values and scales
+ * transposed, k x up(n) and ceil(k / 128) x up(n) / 128 (what the input gradient's
+ * products take).
+ */
+pmx_status pmx_fp8_store_weight(pmx_handle handle, const void* W, pmx_dtype dtype, int groups, int n,
+                                int k, int64_t ldw, int64_t stride_w, int transposed, uint8_t* values,
+                                int64_t ldv, int64_t stride_v, uint8_t* scales, int64_t lds,
+                                int64_t stride_s, void* stream);
+/*
+ * silu with its checkpoint: A = h s(h), s(h) = 1 / (1 + exp(-h)), gated = 1:
+ * H is rows x 2 cols and A = h s(h) u for h its first and u its second half.  H
+ * goes to values and scales as above, gated in two halves of up(cols) bytes and
+ * up(cols) / 128 scale bytes each.  A (rows x cols, H's type) is computed from H
+ * itself.
+ */
+pmx_status pmx_silu_checkpoint(pmx_handle handle, const void* H, pmx_dtype dtype, int64_t rows, int cols,
+                               int64_t ldh, int gated, void* A, int64_t lda, uint8_t* values, int64_t ldv,
+                               uint8_t* scales, int64_t lds, void* stream);
+/*
+ * Backward from the stored values: dH = dA s (1 + h (1 - s)) (gated: first half
+ * times u, second half dA h s), and A once more from them (NULL: not wanted),
+ * which is what the next weight's gradient takes.  dH and A have dA's type.
+ */
+pmx_status pmx_silu_checkpoint_grad(pmx_handle handle, const void* dA, pmx_dtype dtype, int64_t rows,
+                                    int cols, int64_t ldda, const uint8_t* values, int64_t ldv,
+                                    const uint8_t* scales, int64_t lds, int gated, void* dH, int64_t lddh,
+                                    void* A, int64_t lda, void* stream);
+/*
+ * Products of 8-bit values, grouped by expert as in pmx_grouped_product:
+ *   C[t][j] = sum_k A[t][k] B_e[j][k]
+ * A: rows x up(k) values with rows x up(k) / 128 scales (pmx_fp8_store); B_e: n x
+ * up(k) values at B + e stride_b with ceil(n / 128) x up(k) / 128 scales at
+ * B_scales + e stride_bs (pmx_fp8_store_weight).  Values past column k take part:
+ * they are zeros as stored.  offsets NULL: one group of all rows (groups = 1).
+ * C is PMX_F32 or PMX_BF16; sums are fp32.  Values 16-byte aligned, row distances
+ * and stride_b multiples of 16.  Limits as in pmx_grouped_product.
+ */
+pmx_status pmx_fp8_product_workspace_size(int64_t rows, int k, int n, int groups, size_t* bytes);
+pmx_status pmx_fp8_product(pmx_handle handle, const uint8_t* A, int64_t rows, int k, int64_t lda,
+                           const uint8_t* A_scales, int64_t ldas, const uint8_t* B, int n, int64_t ldb,
+                           int64_t stride_b, const uint8_t* B_scales, int64_t ldbs, int64_t stride_bs,
+                           const void* offsets, pmx_itype itype, int groups, void* C,
+                           pmx_dtype out_dtype, int64_t ldc, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
  * Launch trace for benchmarking.  While enabled, every kernel that a call on
  * this handle enqueues is bracketed by a pair of HIP events recorded on the
  * call's stream (host-side event objects owned by the handle; no device

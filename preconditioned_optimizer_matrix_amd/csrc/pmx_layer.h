@@ -1,0 +1,217 @@
+// Parameter blocks and launchers of the expert layer's operators: layer norm
+// (pmx_norm.hip), the router with its balance loss (pmx_route.hip), values kept
+// in 8 bits (pmx_checkpoint.hip) and products of them (pmx_fp8.hip); reductions
+// and row pieces they share.
+#pragma once
+
+#include "pmx_train.h"
+
+namespace pmx {
+
+// ---------------------------------------------------------------------------
+// Reductions over 16 lanes (a DPP row) and over a wave; every lane gets the result.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int i = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // quad_perm, row_half_mirror, row_mirror
+
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kHalfMirror>(v);
+  return v + dpp<kMirror>(v);
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp<kXor1>(v));
+  v = fmaxf(v, dpp<kXor2>(v));
+  v = fmaxf(v, dpp<kHalfMirror>(v));
+  return fmaxf(v, dpp<kMirror>(v));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row_sum(v);
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = row_max(v);
+  return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
+}
+
+// ---------------------------------------------------------------------------
+// Pieces of 16 bytes of a row of n elements, at any element alignment.
+typedef u32x4_t piece_a2 __attribute__((aligned(2)));
+typedef u32x4_t piece_a4 __attribute__((aligned(4)));
+template <typename E>
+constexpr int kPiece = 16 / (int)sizeof(E);
+
+// Elements c .. of a row of n, zeros past its end.
+template <typename E>
+__device__ __forceinline__ u32x4_t load_piece(const E* row, int c, int n) {
+  constexpr int V = kPiece<E>;
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (c + V <= n) {
+    if constexpr (sizeof(E) == 2) v = *reinterpret_cast<const piece_a2*>(row + c);
+    else v = *reinterpret_cast<const piece_a4*>(row + c);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V - 1; ++j)
+      if (c + j < n) {
+        if constexpr (sizeof(E) == 2) v[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
+        else v[j] = __float_as_uint(row[c + j]);
+      }
+  }
+  return v;
+}
+template <typename E>
+__device__ __forceinline__ float element(const u32x4_t& v, int j) {
+  if constexpr (sizeof(E) == 2) return j & 1 ? bf16_hi(v[j >> 1]) : bf16_lo(v[j >> 1]);
+  else return __uint_as_float(v[j]);
+}
+// Rounds kPiece<E> values to elements c .. of a row of n.
+template <typename E>
+__device__ __forceinline__ void store_piece(E* row, int c, int n, const float (&f)[kPiece<E>]) {
+  constexpr int V = kPiece<E>;
+  u32x4_t v;
+  if constexpr (sizeof(E) == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __float_as_uint(f[j]);
+  }
+  if (c + V <= n) {
+    if constexpr (sizeof(E) == 2) *reinterpret_cast<piece_a2*>(row + c) = v;
+    else *reinterpret_cast<piece_a4*>(row + c) = v;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V - 1; ++j)
+      if (c + j < n) {
+        if constexpr (sizeof(E) == 2) row[c + j] = (E)(v[j >> 1] >> (16 * (j & 1)));
+        else row[c + j] = f[j];
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Layer norm.
+struct NormParams {
+  const void* x;
+  int64_t ldx;
+  const void* weight;  // null: ones
+  const void* bias;    // null: zeros
+  int param_dtype;
+  int dtype;
+  int64_t rows;
+  int cols;
+  float eps;
+  void* y;             // forward
+  int64_t ldy;
+  float* stats;        // [rows][2]: mean, 1 / sqrt(variance + eps)
+  const void* dy;      // gradient
+  int64_t lddy;
+  void* dx;
+  int64_t lddx;
+  float* dw;
+  float* db;
+  int accumulate;
+  float* part;         // [blocks][2][cols]
+  int blocks;
+  int num_cu;
+};
+size_t norm_grad_floats(int64_t rows, int cols, int dtype);
+hipError_t launch_norm(const NormParams& p, hipStream_t s);
+hipError_t launch_norm_grad(NormParams p, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Router.
+struct RouteParams {
+  const void* z;
+  int64_t ldz;
+  int dtype;
+  int64_t rows;
+  int experts, top;
+  const uint8_t* live;  // null: every token
+  int normalize;
+  float balance, zloss;
+  int32_t* ids;         // [rows][top]
+  float* gates;
+  int32_t* counts;      // [experts + 1]; the last: live tokens
+  int32_t* offsets;     // [experts + 1]
+  int32_t* slots;       // [rows][top]
+  int32_t* tokens;      // [rows * top]
+  float* loss;
+  void* ws;
+  // gradient
+  const float* dgates;
+  const float* upstream;
+  void* dz;
+  int64_t lddz;
+  int num_cu;
+};
+size_t route_workspace(int64_t rows, int experts);
+hipError_t launch_route(const RouteParams& p, hipStream_t s);
+hipError_t launch_route_grad(const RouteParams& p, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Values in 8 bits: e4m3, a power of two 2^(code - 127) for each 128 of a row.
+constexpr int kBlock8 = 128;
+struct Store8Params {
+  const void* x;       // rows x cols; gated: rows x 2 cols
+  int64_t ldx;
+  int dtype;
+  int64_t rows;
+  int cols;
+  uint8_t* values;     // rows x up128(cols); gated: twice that
+  int64_t ldv;
+  uint8_t* scales;
+  int64_t lds;
+  int gated;
+  void* act;           // silu of x (times the second half) in x's type
+  int64_t lda;
+  const void* dact;    // gradient of act
+  int64_t ldda;
+  void* dx;            // gradient of x
+  int64_t lddx;
+  // weights: `batch` matrices of rows x cols, one code for each 128 x 128
+  int batch;
+  int64_t stride_x, stride_v, stride_s;
+  int transposed;
+  int num_cu;
+};
+hipError_t launch_store8(const Store8Params& p, hipStream_t s);
+hipError_t launch_load8(const Store8Params& p, hipStream_t s);  // writes act
+hipError_t launch_store8_weight(const Store8Params& p, hipStream_t s);
+hipError_t launch_silu8(const Store8Params& p, hipStream_t s);
+hipError_t launch_silu8_grad(const Store8Params& p, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Products of 8-bit values, grouped by expert: C[t][j] = sum_k A[t][k] B_e[j][k].
+struct Fp8Params {
+  const uint8_t* a;    // rows x k
+  int64_t lda;
+  const uint8_t* sa;   // rows x k / 128
+  int64_t ldsa;
+  const uint8_t* b;    // per group n x k
+  int64_t ldb, stride_b;
+  const uint8_t* sb;   // per group ceil(n / 128) x k / 128
+  int64_t ldsb, stride_sb;
+  const void* offsets; // null: one group of all rows
+  int off64;
+  int groups;
+  int64_t rows;
+  int n, k;            // k a multiple of 128
+  void* c;
+  int64_t ldc;
+  int out_dtype;
+  float* part;
+  int splits;
+  int num_cu;
+};
+int fp8_splits(int64_t rows, int k, int n, int groups);
+hipError_t launch_fp8(const Fp8Params& p, hipStream_t s);
+
+}  // namespace pmx

@@ -1,0 +1,321 @@
+// Layer norm over the last dimension, forward and backward.
+//   m = mean x, r = 1 / sqrt(mean (x - m)^2 + eps), h = (x - m) r
+//   y = h w + b
+//   dx = r (g - mean g - h mean(g h)), g = dy w
+//   dw = sum_t dy h, db = sum_t dy
+//
+// Bound: HBM.  A row stays in registers, packed as it was read, from its load
+// to its result, so the variance is the two-pass one of the mean's deviations
+// and costs no second read.  One wave holds rows of up to 1024 elements, four
+// or sixteen waves longer ones.  Blocks are persistent: the next row's loads
+// are under way while this one is reduced, weights stay in registers, and in
+// the backward pass a thread's columns stay the same, so it sums dy and dy h of
+// its rows in registers.  The block's teams add those sums in a fixed order in
+// LDS, a second launch adds the blocks' in theirs: no atomics, the same bits on
+// every call.  Statistics and sums are fp32.
+#include <algorithm>
+
+#include "pmx_layer.h"
+
+namespace pmx {
+namespace {
+
+// W waves a row, NV pieces of 16 bytes a thread, TEAMS rows at a time a block.
+template <typename E_, int W_, int NV_, int TEAMS_>
+struct NCfg {
+  typedef E_ E;
+  static constexpr int W = W_, NV = NV_, TEAMS = TEAMS_, V = kPiece<E_>;
+  static constexpr int LANES = 64 * W, THREADS = LANES * TEAMS, COLS = LANES * NV * V;
+};
+
+// Sums over the team's lanes of N values; red: [2][TEAMS * W][N], alternating.
+template <class C, int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[C::TEAMS * C::W][N], int& flip) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (C::W > 1) {
+    const int wid = threadIdx.x >> 6, team = wid / C::W;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[flip][wid][i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = red[flip][team * C::W][i];
+#pragma unroll
+      for (int w = 1; w < C::W; ++w) s += red[flip][team * C::W + w][i];
+      v[i] = s;
+    }
+    flip ^= 1;  // the next sum writes the other half: one barrier a sum
+  }
+}
+
+// A thread's elements of a parameter vector, `other` where there is none.
+template <class C>
+__device__ __forceinline__ void load_param(float (&w)[C::NV][C::V], const void* p, int dtype, int cols, int lane,
+                                           float other) {
+#pragma unroll
+  for (int i = 0; i < C::NV; ++i)
+#pragma unroll
+    for (int j = 0; j < C::V; ++j) {
+      const int c = (i * C::LANES + lane) * C::V + j;
+      w[i][j] = other;
+      if (p && c < cols)
+        w[i][j] = dtype == PMX_BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[c] << 16)
+                                    : reinterpret_cast<const float*>(p)[c];
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void load_row(u32x4_t (&v)[C::NV], const void* p, int64_t ld, int64_t row, int cols,
+                                         int lane) {
+  const typename C::E* r = reinterpret_cast<const typename C::E*>(p) + row * ld;
+#pragma unroll
+  for (int i = 0; i < C::NV; ++i) v[i] = load_piece(r, (i * C::LANES + lane) * C::V, cols);
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void norm_kernel(NormParams p) {
+  typedef typename C::E E;
+  __shared__ float red[2][C::TEAMS * C::W][1];
+  const int team = threadIdx.x / C::LANES, lane = threadIdx.x % C::LANES;
+  const int64_t step = (int64_t)gridDim.x * C::TEAMS;
+  const float inv = 1.f / (float)p.cols;
+  int flip = 0;
+  int64_t base = (int64_t)blockIdx.x * C::TEAMS;
+  // the block's teams go round together (barriers); a team past the end repeats the last row
+  auto row_of = [&](int64_t b) { return min(b + team, p.rows - 1); };
+  u32x4_t x[C::NV];
+  load_row<C>(x, p.x, p.ldx, row_of(base), p.cols, lane);
+  float w[C::NV][C::V], b[C::NV][C::V];
+  load_param<C>(w, p.weight, p.param_dtype, p.cols, lane, 1.f);
+  load_param<C>(b, p.bias, p.param_dtype, p.cols, lane, 0.f);
+  for (; base < p.rows; base += step) {
+    u32x4_t next[C::NV];
+    const bool more = base + step < p.rows;
+    if (more) load_row<C>(next, p.x, p.ldx, row_of(base + step), p.cols, lane);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < C::NV; ++i)
+#pragma unroll
+      for (int j = 0; j < C::V; ++j) s[0] += element<E>(x[i], j);
+    team_sum<C, 1>(s, red, flip);
+    const float mean = s[0] * inv;
+    s[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < C::NV; ++i)
+#pragma unroll
+      for (int j = 0; j < C::V; ++j) {
+        const float d = element<E>(x[i], j) - mean;
+        if ((i * C::LANES + lane) * C::V + j < p.cols) s[0] += d * d;
+      }
+    team_sum<C, 1>(s, red, flip);
+    const float r = 1.f / sqrtf(s[0] * inv + p.eps);
+    const int64_t row = base + team;
+    if (row < p.rows) {
+      E* y = reinterpret_cast<E*>(p.y) + row * p.ldy;
+#pragma unroll
+      for (int i = 0; i < C::NV; ++i) {
+        float f[C::V];
+#pragma unroll
+        for (int j = 0; j < C::V; ++j) f[j] = (element<E>(x[i], j) - mean) * r * w[i][j] + b[i][j];
+        store_piece(y, (i * C::LANES + lane) * C::V, p.cols, f);
+      }
+      if (lane == 0 && p.stats) {
+        p.stats[2 * row] = mean;
+        p.stats[2 * row + 1] = r;
+      }
+    }
+    if (more)
+#pragma unroll
+      for (int i = 0; i < C::NV; ++i) x[i] = next[i];
+  }
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void norm_grad_kernel(NormParams p) {
+  typedef typename C::E E;
+  __shared__ float red[2][C::TEAMS * C::W][2];
+  __shared__ float sums[2][C::TEAMS > 1 ? C::COLS : 1];
+  const int team = threadIdx.x / C::LANES, lane = threadIdx.x % C::LANES;
+  const int64_t step = (int64_t)gridDim.x * C::TEAMS;
+  const float inv = 1.f / (float)p.cols;
+  int flip = 0;
+  int64_t base = (int64_t)blockIdx.x * C::TEAMS;
+  auto row_of = [&](int64_t b) { return min(b + team, p.rows - 1); };
+  u32x4_t x[C::NV], g[C::NV];
+  load_row<C>(x, p.x, p.ldx, row_of(base), p.cols, lane);
+  load_row<C>(g, p.dy, p.lddy, row_of(base), p.cols, lane);
+  float mean = p.stats[2 * row_of(base)], r = p.stats[2 * row_of(base) + 1];
+  float w[C::NV][C::V], dw[C::NV][C::V], db[C::NV][C::V];
+  load_param<C>(w, p.weight, p.param_dtype, p.cols, lane, 1.f);
+#pragma unroll
+  for (int i = 0; i < C::NV; ++i)
+#pragma unroll
+    for (int j = 0; j < C::V; ++j) dw[i][j] = db[i][j] = 0.f;
+  for (; base < p.rows; base += step) {
+    u32x4_t nx[C::NV], ng[C::NV];
+    float nmean = 0.f, nr = 0.f;
+    const bool more = base + step < p.rows;
+    if (more) {
+      load_row<C>(nx, p.x, p.ldx, row_of(base + step), p.cols, lane);
+      load_row<C>(ng, p.dy, p.lddy, row_of(base + step), p.cols, lane);
+      nmean = p.stats[2 * row_of(base + step)];
+      nr = p.stats[2 * row_of(base + step) + 1];
+    }
+    const int64_t row = base + team;
+    const bool own = row < p.rows;
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < C::NV; ++i)
+#pragma unroll
+      for (int j = 0; j < C::V; ++j) {
+        const float dy = element<E>(g[i], j), h = (element<E>(x[i], j) - mean) * r;
+        s[0] += dy * w[i][j];
+        s[1] += dy * w[i][j] * h;
+        if (own) {
+          dw[i][j] += dy * h;
+          db[i][j] += dy;
+        }
+      }
+    team_sum<C, 2>(s, red, flip);
+    if (own && p.dx) {
+      const float m0 = s[0] * inv, m1 = s[1] * inv;
+      E* dx = reinterpret_cast<E*>(p.dx) + row * p.lddx;
+#pragma unroll
+      for (int i = 0; i < C::NV; ++i) {
+        float f[C::V];
+#pragma unroll
+        for (int j = 0; j < C::V; ++j) {
+          const float h = (element<E>(x[i], j) - mean) * r;
+          f[j] = r * (element<E>(g[i], j) * w[i][j] - m0 - h * m1);
+        }
+        store_piece(dx, (i * C::LANES + lane) * C::V, p.cols, f);
+      }
+    }
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < C::NV; ++i) {
+        x[i] = nx[i];
+        g[i] = ng[i];
+      }
+      mean = nmean;
+      r = nr;
+    }
+  }
+  if (!p.part) return;
+  // the teams' sums in their order
+  float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
+  if constexpr (C::TEAMS > 1) {
+    for (int t = 0; t < C::TEAMS; ++t) {
+      if (team == t)
+#pragma unroll
+        for (int i = 0; i < C::NV; ++i)
+#pragma unroll
+          for (int j = 0; j < C::V; ++j) {
+            const int c = (i * C::V + j) * C::LANES + lane;
+            sums[0][c] = t ? sums[0][c] + dw[i][j] : dw[i][j];
+            sums[1][c] = t ? sums[1][c] + db[i][j] : db[i][j];
+          }
+      __syncthreads();
+    }
+  }
+  if (team == 0)
+#pragma unroll
+    for (int i = 0; i < C::NV; ++i)
+#pragma unroll
+      for (int j = 0; j < C::V; ++j) {
+        const int c = (i * C::LANES + lane) * C::V + j, k = (i * C::V + j) * C::LANES + lane;
+        if (c < p.cols) {
+          out[c] = C::TEAMS > 1 ? sums[0][k] : dw[i][j];
+          out[p.cols + c] = C::TEAMS > 1 ? sums[1][k] : db[i][j];
+        }
+      }
+}
+
+// dw and db: the blocks' sums in their order, eight segments of them at a time.
+__global__ __launch_bounds__(256) void norm_join_kernel(NormParams p) {
+  __shared__ float seg[8][32];
+  const int in = threadIdx.x & 31, s = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + in;  // of 2 cols
+  const int64_t wide = 2 * (int64_t)p.cols;
+  const int per = (p.blocks + 7) / 8, b0 = min(s * per, p.blocks), b1 = min(b0 + per, p.blocks);
+  float v = 0.f;
+  if (c < wide)
+    for (int b = b0; b < b1; ++b) v += p.part[b * wide + c];
+  seg[s][in] = v;
+  __syncthreads();
+  if (s == 0 && c < wide) {
+    float t = seg[0][in];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += seg[i][in];
+    float* out = c < p.cols ? p.dw : p.db;
+    if (out) {
+      out += c < p.cols ? c : c - p.cols;
+      *out = p.accumulate ? *out + t : t;
+    }
+  }
+}
+
+// The configuration of a row length: f(NCfg).
+template <typename E, typename F>
+hipError_t with_cfg(int cols, F&& f) {
+  constexpr int V = kPiece<E>;
+  if (cols <= 64 * V) return f(NCfg<E, 1, 1, 8>());
+  if (cols <= 128 * V) return f(NCfg<E, 1, 2, 8>());
+  if (cols <= 512 * V) return f(NCfg<E, 4, 2, 2>());
+  if (cols <= 1024 * V) return f(NCfg<E, 4, 4, 2>());
+  if (cols <= 2048 * V) return f(NCfg<E, 16, 2, 1>());
+  if constexpr (sizeof(E) == 4) return f(NCfg<E, 16, 4, 1>());
+  return hipErrorInvalidValue;
+}
+template <typename F>
+hipError_t with_cfg(int dtype, int cols, F&& f) {
+  return dtype == PMX_BF16 ? with_cfg<uint16_t>(cols, f) : with_cfg<float>(cols, f);
+}
+
+int grad_blocks(int64_t rows, int teams) {
+  return (int)std::min<int64_t>((rows + teams - 1) / teams, 512);
+}
+
+}  // namespace
+
+size_t norm_grad_floats(int64_t rows, int cols, int dtype) {
+  if (rows == 0) return 0;
+  size_t n = 0;
+  (void)with_cfg(dtype, cols, [&](auto c) {
+    n = (size_t)grad_blocks(rows, decltype(c)::TEAMS) * 2 * cols;
+    return hipSuccess;
+  });
+  return n;
+}
+
+hipError_t launch_norm(const NormParams& p, hipStream_t s) {
+  return with_cfg(p.dtype, p.cols, [&](auto c) {
+    typedef decltype(c) C;
+    const int64_t blocks = std::min<int64_t>((p.rows + C::TEAMS - 1) / C::TEAMS, p.num_cu * 4);
+    norm_kernel<C><<<dim3((unsigned)blocks), dim3(C::THREADS), 0, s>>>(p);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_norm_grad(NormParams p, hipStream_t s) {
+  p.blocks = 0;
+  const bool params = p.dw || p.db;
+  if (!params) p.part = nullptr;
+  if (p.rows > 0) {
+    const hipError_t e = with_cfg(p.dtype, p.cols, [&](auto c) {
+      typedef decltype(c) C;
+      p.blocks = grad_blocks(p.rows, C::TEAMS);
+      norm_grad_kernel<C><<<dim3(p.blocks), dim3(C::THREADS), 0, s>>>(p);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+  }
+  if (!params) return hipSuccess;
+  norm_join_kernel<<<dim3((2 * p.cols + 31) / 32), dim3(256), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace pmx

@@ -5,6 +5,7 @@ current HIP stream; every step of the computation runs in libpmx's kernels.
 Importing this module raises if the built library is missing, so no caller
 can silently fall back to another implementation.
 """
+import collections
 import ctypes
 import math
 import os
@@ -21,6 +22,7 @@ RUNNING, CONVERGED, MAXITER, STAGNATED, NONFINITE, DIVERGED = -1, 0, 1, 2, 3, 4
 F32, BF16 = 0, 1
 I32, I64 = 0, 1
 MAX_GROUPS, MAX_TOP, MAX_VOCAB, MAX_TOKENS = 1000, 1023, (1 << 22) - 1, 1 << 30
+MAX_NORM_COLS, MAX_ROUTE_TOP, MAX_ROUTE_ROWS = 16384, 16, 1 << 28
 OP_STATS, OP_INV_ROOT, OP_POLAR, OP_APPLY, OP_POLAR_VARBATCH = range(5)
 VARBATCH_MAX_DIM = 64
 VARBATCH_MAX_SIDE = 8192
@@ -47,6 +49,11 @@ EXPORTS = [
     "pmx_grouped_outer", "pmx_grouped_outer_workspace_size",
     "pmx_embedding", "pmx_embedding_grad", "pmx_embedding_grad_workspace_size",
     "pmx_distill_loss", "pmx_distill_grad", "pmx_distill_workspace_size",
+    "pmx_layer_norm", "pmx_layer_norm_grad", "pmx_layer_norm_grad_workspace_size",
+    "pmx_route", "pmx_route_grad", "pmx_route_workspace_size",
+    "pmx_fp8_store", "pmx_fp8_load", "pmx_fp8_store_weight",
+    "pmx_silu_checkpoint", "pmx_silu_checkpoint_grad",
+    "pmx_fp8_product", "pmx_fp8_product_workspace_size",
 ]
 
 # kernel classes of the launch trace (pmx_kernel_class)
@@ -91,6 +98,14 @@ class DistillProblem(ctypes.Structure):
                 ("ids_type", ctypes.c_int32), ("labels_type", ctypes.c_int32),
                 ("teacher_dtype", ctypes.c_int32), ("tau", ctypes.c_float),
                 ("mix", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class RouteProblem(ctypes.Structure):
+    _fields_ = [("struct_version", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("experts", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("live", ctypes.c_void_p),
+                ("balance", ctypes.c_float), ("zloss", ctypes.c_float),
+                ("normalize", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class Info(ctypes.Structure):
@@ -187,6 +202,28 @@ def _load():
                                     _vp, _sz, _vp]),
         "pmx_distill_grad": (_i32, [_vp, ctypes.POINTER(DistillProblem), _vp, _vp, _vp, _i64,
                                     _vp]),
+        "pmx_layer_norm": (_i32, [_vp, _vp, _i32, _i64, _i32, _i64, _vp, _vp, _i32, _f32, _vp,
+                                  _i64, _vp, _vp]),
+        "pmx_layer_norm_grad_workspace_size": (_i32, [_i64, _i32, _i32, ctypes.POINTER(_sz)]),
+        "pmx_layer_norm_grad": (_i32, [_vp, _vp, _i32, _i64, _i32, _i64, _vp, _i64, _vp, _vp,
+                                       _i32, _vp, _i64, _vp, _vp, _i32, _vp, _sz, _vp]),
+        "pmx_route_workspace_size": (_i32, [ctypes.POINTER(RouteProblem), ctypes.POINTER(_sz)]),
+        "pmx_route": (_i32, [_vp, ctypes.POINTER(RouteProblem), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                             _vp, _sz, _vp]),
+        "pmx_route_grad": (_i32, [_vp, ctypes.POINTER(RouteProblem), _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _i64, _vp]),
+        "pmx_fp8_store": (_i32, [_vp, _vp, _i32, _i64, _i32, _i64, _vp, _i64, _vp, _i64, _vp]),
+        "pmx_fp8_load": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _i32, _i64, _vp]),
+        "pmx_fp8_store_weight": (_i32, [_vp, _vp, _i32, _i32, _i32, _i32, _i64, _i64, _i32, _vp,
+                                        _i64, _i64, _vp, _i64, _i64, _vp]),
+        "pmx_silu_checkpoint": (_i32, [_vp, _vp, _i32, _i64, _i32, _i64, _i32, _vp, _i64, _vp,
+                                       _i64, _vp, _i64, _vp]),
+        "pmx_silu_checkpoint_grad": (_i32, [_vp, _vp, _i32, _i64, _i32, _i64, _vp, _i64, _vp,
+                                            _i64, _i32, _vp, _i64, _vp, _i64, _vp]),
+        "pmx_fp8_product_workspace_size": (_i32, [_i64, _i32, _i32, _i32, ctypes.POINTER(_sz)]),
+        "pmx_fp8_product": (_i32, [_vp, _vp, _i64, _i32, _i64, _vp, _i64, _vp, _i32, _i64, _i64,
+                                   _vp, _i64, _i64, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _sz,
+                                   _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -590,6 +627,8 @@ def _fill_codes():
     _codes["stream"] = torch._C._cuda_getCurrentRawStream
     _codes["empty"] = torch.empty
     _codes["f32"] = torch.float32
+    _codes["e4m3"], _codes["byte"], _codes["i32"] = torch.float8_e4m3fn, torch.uint8, torch.int32
+    _codes["bool"] = torch.bool
 
 
 def _elem_code(t):
@@ -898,3 +937,336 @@ def distill_grad(Z, teacher_ids, teacher, stats, upstream=None, tau=1.0, mix=1.0
         upstream.data_ptr() if upstream is not None else None, dz.data_ptr(), lddz,
         st), "distill_grad")
     return dz
+
+
+# ---------------------------------------------------------------- expert layer
+# Layer norm, the router with its balance loss, activations kept in 8 bits, and
+# products of 8-bit values.
+
+def _out_like(out, shape, dtype, device, what="out"):
+    """`out`, or a new tensor; its row distance."""
+    if out is None:
+        return _codes["empty"](shape, dtype=dtype, device=device), max(shape[-1], 1)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+        raise ValueError("%s has another shape or type" % what)
+    return out, _rows_of(out, what)[2]
+
+
+def _param(t, cols, what):
+    if t is None:
+        return None
+    if _vector(t, what) != cols:
+        raise ValueError("one value of %s per column" % what)
+    return t.data_ptr()
+
+
+def layer_norm(X, weight=None, bias=None, eps=1e-5, out=None, stats=None):
+    """Layer norm of the rows of X (rows x cols, bf16 or fp32): returns (Y,
+    stats), stats (rows x 2 fp32, mean and 1 / sqrt(variance + eps)) being what
+    layer_norm_grad needs.  weight and bias (cols; both of one type, X's or
+    fp32) default to ones and zeros."""
+    d = _on(X, weight, bias, out, stats)
+    rows, cols, ldx = _rows_of(X, "X")
+    wp, bp = _param(weight, cols, "weight"), _param(bias, cols, "bias")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias have different types")
+    param = weight if weight is not None else bias
+    dt = _elem_code(X)
+    out, ldy = _out_like(out, (rows, cols), X.dtype, X.device)
+    if stats is None:
+        stats = _codes["empty"]((rows, 2), dtype=_codes["f32"], device=X.device)
+    elif tuple(stats.shape) != (rows, 2) or stats.dtype != _codes["f32"] or not stats.is_contiguous():
+        raise ValueError("stats is rows x 2, fp32, contiguous")
+    h, st = _call(d)
+    check(lib.pmx_layer_norm(h, X.data_ptr(), dt, rows, cols, ldx, wp, bp,
+                             dt if param is None else _elem_code(param), eps, out.data_ptr(), ldy,
+                             stats.data_ptr(), st), "layer_norm")
+    return out, stats
+
+
+def layer_norm_grad(dY, X, stats, weight=None, params=True, out=None, dweight=None, dbias=None,
+                    accumulate=False, ws=None):
+    """Gradients of layer_norm: (dX, dweight, dbias), dX in X's type (out may
+    be dY itself), dweight and dbias fp32 (accumulate: added to those given).
+    params=False leaves the last two out (None)."""
+    d = _on(dY, X, stats, weight, out, dweight, dbias)
+    rows, cols, lddy = _rows_of(dY, "dY")
+    rx, cx, ldx = _rows_of(X, "X")
+    if (rx, cx) != (rows, cols):
+        raise ValueError("dY and X have different shapes")
+    if X.dtype != dY.dtype:
+        raise TypeError("dY and X have different types")
+    f32 = _codes["f32"]
+    if tuple(stats.shape) != (rows, 2) or stats.dtype != f32 or not stats.is_contiguous():
+        raise ValueError("stats are those layer_norm returned")
+    wp = _param(weight, cols, "weight")
+    dt = _elem_code(dY)
+    out, lddx = _out_like(out, (rows, cols), X.dtype, X.device)
+    need = 0
+    if params:
+        if accumulate and (dweight is None or dbias is None):
+            raise ValueError("accumulate needs dweight and dbias")
+        empty = _codes["empty"]
+        if dweight is None:
+            dweight = empty((cols,), dtype=f32, device=X.device)
+        if dbias is None:
+            dbias = empty((cols,), dtype=f32, device=X.device)
+        for t in (dweight, dbias):
+            if t.dtype != f32 or _vector(t, "dweight and dbias") != cols:
+                raise ValueError("dweight and dbias are fp32, one value per column")
+        need = _need("pmx_layer_norm_grad_workspace_size", rows, cols, dt)
+    elif accumulate or dweight is not None or dbias is not None:
+        raise ValueError("params=False has no dweight, dbias or accumulate")
+    wsp, wn = _ws_for(need, ws, X.device)
+    h, st = _call(d)
+    check(lib.pmx_layer_norm_grad(
+        h, dY.data_ptr(), dt, rows, cols, lddy, X.data_ptr(), ldx, stats.data_ptr(), wp,
+        dt if weight is None else _elem_code(weight), out.data_ptr(), lddx,
+        dweight.data_ptr() if params else None, dbias.data_ptr() if params else None,
+        1 if accumulate else 0, wsp, wn, st), "layer_norm_grad")
+    return out, dweight, dbias
+
+
+# ids, gates, slots: rows x top; counts: experts; offsets: experts + 1; tokens:
+# rows * top; loss: one value.  tally holds the counts and, last, the number of
+# live tokens: what processes that balance together sum before route_grad.
+Routes = collections.namedtuple("Routes", "ids gates counts offsets slots tokens loss tally")
+
+
+def _route_problem(Z, top, live, balance, zloss, normalize):
+    rows, experts, ldz = _rows_of(Z, "Z")
+    lp = None
+    if live is not None:
+        if _vector(live, "live") != rows:
+            raise ValueError("one live flag per row")
+        if live.dtype not in (_codes["bool"], _codes["byte"]):
+            raise TypeError("live is bool or uint8")
+        lp = live.data_ptr()
+    return RouteProblem(1, _elem_code(Z), rows, experts, top, Z.data_ptr(), ldz, lp, balance, zloss,
+                        1 if normalize else 0, 0)
+
+
+def route(Z, top, live=None, balance=0.0, zloss=0.0, normalize=True, order=True, ws=None):
+    """Routes each row of the logits Z (rows x experts, bf16 or fp32) to its
+    `top` experts: returns Routes.  ids (largest logit first, the lowest index
+    among equals) and gates (softmax there, with normalize divided by their
+    sum); counts and offsets of the experts; slots, the row of each pair among
+    the pairs sorted by expert, and tokens, the token of each such row (-1
+    behind the last): embedding(X, tokens) and offsets are what grouped_product
+    takes (order=False leaves both out); loss, the balance loss plus the
+    z-loss.  Rows whose live flag is 0 are not routed: ids and slots -1."""
+    d = _on(Z, live)
+    top = int(top)
+    q = _route_problem(Z, top, live, balance, zloss, normalize)
+    empty, dev, i32 = _codes["empty"], Z.device, _codes["i32"]
+    rows, experts = q.rows, q.experts
+    ids = empty((rows, top), dtype=i32, device=dev)
+    gates = empty((rows, top), dtype=_codes["f32"], device=dev)
+    tally = empty((experts + 1,), dtype=i32, device=dev)
+    offsets = empty((experts + 1,), dtype=i32, device=dev)
+    slots = empty((rows, top), dtype=i32, device=dev) if order else None
+    tokens = empty((rows * top,), dtype=i32, device=dev) if order else None
+    loss = empty((), dtype=_codes["f32"], device=dev)
+    ref = ctypes.byref(q)
+    key = ("route", rows, experts, top)
+    need = _sizes.get(key)
+    if need is None:
+        sz = _sz()
+        check(lib.pmx_route_workspace_size(ref, ctypes.byref(sz)), "route_workspace_size")
+        need = _keep_size(key, sz.value)
+    wp, wn = _ws_for(need, ws, dev)
+    h, st = _call(d)
+    check(lib.pmx_route(h, ref, ids.data_ptr(), gates.data_ptr(), tally.data_ptr(), offsets.data_ptr(),
+                        slots.data_ptr() if order else None, tokens.data_ptr() if order else None,
+                        loss.data_ptr(), wp, wn, st), "route")
+    return Routes(ids, gates, tally[:experts], offsets, slots, tokens, loss, tally)
+
+
+def route_grad(Z, routes, dgates=None, upstream=None, live=None, balance=0.0, zloss=0.0, normalize=True,
+               out=None):
+    """Gradient of the logits from that of the gates (dgates, rows x top fp32)
+    and of the loss (upstream, a device fp32 scalar, default 1), with the
+    arguments of the route call.  out may be Z itself."""
+    ids, gates, tally = routes.ids, routes.gates, routes.tally
+    d = _on(Z, live, ids, gates, tally, dgates, upstream, out)
+    shape = tuple(ids.shape)
+    if len(shape) != 2 or tuple(gates.shape) != shape or shape[0] != Z.shape[0] or tally.numel() != Z.shape[1] + 1:
+        raise ValueError("routes are those of a route call of the same logits")
+    q = _route_problem(Z, shape[1], live, balance, zloss, normalize)
+    i32, f32 = _codes["i32"], _codes["f32"]
+    for t, want in ((ids, i32), (gates, f32), (tally, i32)):
+        if t.dtype != want or not t.is_contiguous():
+            raise ValueError("routes are those of a route call")
+    if dgates is not None and (tuple(dgates.shape) != shape or dgates.dtype != f32 or not dgates.is_contiguous()):
+        raise ValueError("dgates is rows x top, fp32, contiguous")
+    if upstream is not None and (upstream.numel() != 1 or upstream.dtype != f32):
+        raise ValueError("upstream is one fp32 value")
+    dz, lddz = _dz_of(Z, out)
+    h, st = _call(d)
+    check(lib.pmx_route_grad(h, ctypes.byref(q), ids.data_ptr(), gates.data_ptr(), tally.data_ptr(),
+                             dgates.data_ptr() if dgates is not None else None,
+                             upstream.data_ptr() if upstream is not None else None, dz.data_ptr(), lddz, st),
+          "route_grad")
+    return dz
+
+
+def _up128(n):
+    return (n + 127) // 128 * 128
+
+
+def _fp8_of(values, scales, halves=1):
+    """(rows, padded columns, row distances) of stored rows."""
+    if values.dtype != _codes["e4m3"] or scales.dtype != _codes["byte"]:
+        raise TypeError("values are float8_e4m3fn and scales uint8")
+    rows, wide, ldv = _rows_of(values, "values")
+    rs, blocks, lds = _rows_of(scales, "scales")
+    if wide % (128 * halves) or rs != rows or blocks * 128 != wide:
+        raise ValueError("values are rows x a multiple of 128, scales one for each 128 of them")
+    return rows, wide, ldv, lds
+
+
+def _fp8_out(values, scales, rows, wide, device):
+    values, ldv = _out_like(values, (rows, wide), _codes["e4m3"], device, "values")
+    scales, lds = _out_like(scales, (rows, wide // 128), _codes["byte"], device, "scales")
+    return values, ldv, scales, lds
+
+
+def fp8_store(X, values=None, scales=None):
+    """The rows of X (bf16 or fp32) in 8 bits: (values, scales), float8_e4m3fn
+    of rows x cols padded with zeros to a multiple of 128, and one power of two
+    for each 128 of a row as uint8, exponent + 127."""
+    d = _on(X, values, scales)
+    rows, cols, ldx = _rows_of(X, "X")
+    dt = _elem_code(X)
+    values, ldv, scales, lds = _fp8_out(values, scales, rows, _up128(cols), X.device)
+    h, st = _call(d)
+    check(lib.pmx_fp8_store(h, X.data_ptr(), dt, rows, cols, ldx, values.data_ptr(), ldv, scales.data_ptr(),
+                            lds, st), "fp8_store")
+    return values, scales
+
+
+def fp8_load(values, scales, cols=None, dtype=None, out=None):
+    """What fp8_store's values stand for, exactly, in bf16 (the default) or
+    fp32; cols: of the stored rows (default: the padded ones)."""
+    d = _on(values, scales, out)
+    rows, wide, ldv, lds = _fp8_of(values, scales)
+    cols = wide if cols is None else int(cols)
+    if _up128(cols) != wide:
+        raise ValueError("values hold another number of columns")
+    if dtype is None:
+        dtype = out.dtype if out is not None else _torch().bfloat16
+    out, ldy = _out_like(out, (rows, cols), dtype, values.device)
+    h, st = _call(d)
+    check(lib.pmx_fp8_load(h, values.data_ptr(), ldv, scales.data_ptr(), lds, rows, cols, out.data_ptr(),
+                           _elem_code(out), ldy, st), "fp8_load")
+    return out
+
+
+def _blocks_out(t, shape, dtype, device, what):
+    if t is None:
+        t = _codes["empty"](shape, dtype=dtype, device=device)
+    elif tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError("%s has another shape or type" % what)
+    return (t,) + _matrices_of(t, what)[3:]
+
+
+def fp8_store_weight(W, transposed=False, values=None, scales=None):
+    """Weights W (groups x n x k, or one n x k) in 8 bits with one power of two
+    for each 128 x 128 tile: values groups x n x k (k padded to a multiple of
+    128) and scales, or transposed, groups x k x n (n padded): the same values
+    and powers, what the input gradient's fp8_product takes."""
+    d = _on(W, values, scales)
+    if W.dim() == 2:
+        W = W.unsqueeze(0)
+    groups, n, k, ldw, sw = _matrices_of(W, "W")
+    dt = _elem_code(W)
+    r, c = (k, n) if transposed else (n, k)
+    wide = _up128(c)
+    values, ldv, sv = _blocks_out(values, (groups, r, wide), _codes["e4m3"], W.device, "values")
+    scales, lds, ss = _blocks_out(scales, (groups, _up128(r) // 128, wide // 128), _codes["byte"], W.device,
+                                  "scales")
+    h, st = _call(d)
+    check(lib.pmx_fp8_store_weight(h, W.data_ptr(), dt, groups, n, k, ldw, sw, 1 if transposed else 0,
+                                   values.data_ptr(), ldv, sv, scales.data_ptr(), lds, ss, st),
+          "fp8_store_weight")
+    return values, scales
+
+
+def silu_checkpoint(H, gated=False, out=None, values=None, scales=None):
+    """A = silu(H), or with gated silu of H's first half times its second, and H
+    in 8 bits for the backward pass, in one go: (A, values, scales).  gated:
+    each half padded to a multiple of 128 by itself."""
+    d = _on(H, out, values, scales)
+    rows, cols, ldh = _rows_of(H, "H")
+    dt = _elem_code(H)
+    halves = 2 if gated else 1
+    if cols % halves:
+        raise ValueError("gated needs an even number of columns")
+    cols //= halves
+    out, lda = _out_like(out, (rows, cols), H.dtype, H.device)
+    values, ldv, scales, lds = _fp8_out(values, scales, rows, halves * _up128(cols), H.device)
+    h, st = _call(d)
+    check(lib.pmx_silu_checkpoint(h, H.data_ptr(), dt, rows, cols, ldh, halves - 1, out.data_ptr(), lda,
+                                  values.data_ptr(), ldv, scales.data_ptr(), lds, st), "silu_checkpoint")
+    return out, values, scales
+
+
+def silu_checkpoint_grad(dA, values, scales, gated=False, again=True, out=None, act=None):
+    """(dH, A) from the upstream dA (rows x cols) and the stored H: the gradient
+    of silu_checkpoint there, and the activation once more, which is what the
+    next weight's gradient takes (again=False: None)."""
+    d = _on(dA, values, scales, out, act)
+    rows, cols, ldda = _rows_of(dA, "dA")
+    dt = _elem_code(dA)
+    halves = 2 if gated else 1
+    rv, wide, ldv, lds = _fp8_of(values, scales, halves)
+    if rv != rows or wide != halves * _up128(cols):
+        raise ValueError("values are those of another shape")
+    out, lddh = _out_like(out, (rows, halves * cols), dA.dtype, dA.device)
+    ap, lda = None, 0
+    if again:
+        act, lda = _out_like(act, (rows, cols), dA.dtype, dA.device, "act")
+        ap = act.data_ptr()
+    elif act is not None:
+        raise ValueError("again=False has no act")
+    h, st = _call(d)
+    check(lib.pmx_silu_checkpoint_grad(h, dA.data_ptr(), dt, rows, cols, ldda, values.data_ptr(), ldv,
+                                       scales.data_ptr(), lds, halves - 1, out.data_ptr(), lddh, ap, lda, st),
+          "silu_checkpoint_grad")
+    return out, act
+
+
+def fp8_product(A, A_scales, B, B_scales, offsets=None, out=None, out_dtype=None, ws=None):
+    """C[t] = A[t] B[e]^T for the rows offsets[e] <= t < offsets[e + 1] of group
+    e, rows in no group zeros: A and its scales from fp8_store (rows x k), B and
+    its scales from fp8_store_weight (groups x n x k; transposed for the input
+    gradient).  One group needs no offsets.  C in bf16 (the default) or fp32."""
+    d = _on(A, A_scales, B, B_scales, offsets, out)
+    rows, k, lda, ldas = _fp8_of(A, A_scales)
+    if B.dtype != _codes["e4m3"] or B_scales.dtype != _codes["byte"]:
+        raise TypeError("values are float8_e4m3fn and scales uint8")
+    groups, n, kb, ldb, sb = _matrices_of(B, "B")
+    gs, ns, ks, ldbs, sbs = _matrices_of(B_scales, "B_scales")
+    if kb != k:
+        raise ValueError("A and B disagree about k")
+    if gs != groups or ns * 128 != _up128(n) or ks * 128 != k:
+        raise ValueError("B_scales has one value for each 128 x 128 of B")
+    op, ot = None, 0
+    if offsets is None:
+        if groups != 1:
+            raise ValueError("several groups need offsets")
+    else:
+        if _vector(offsets, "offsets") != groups + 1:
+            raise ValueError("one offset per group and one more")
+        op, ot = offsets.data_ptr(), _index_code(offsets)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else _torch().bfloat16
+    out, ldc = _out_like(out, (rows, n), out_dtype, A.device)
+    need = _need("pmx_fp8_product_workspace_size", rows, k, n, groups)
+    wp, wn = _ws_for(need, ws, A.device)
+    h, st = _call(d)
+    check(lib.pmx_fp8_product(
+        h, A.data_ptr(), rows, k, lda, A_scales.data_ptr(), ldas, B.data_ptr(), n, ldb, sb,
+        B_scales.data_ptr(), ldbs, sbs, op, ot, groups, out.data_ptr(), _elem_code(out), ldc, wp, wn, st),
+        "fp8_product")
+    return out
