@@ -688,7 +688,9 @@ pmx_status pmx_route_grad(pmx_handle handle, const pmx_route_problem* problem, c
  * the maximum.  `values` are 16-byte aligned and their row distance is a multiple
  * of 16 and at least up(cols).  1 <= cols <= 2^20; rows may be 0.
  * Reading back multiplies by 2^(byte - 127) (byte 255: NaN); the result has four
- * significant bits, so bf16 and fp32 hold it exactly.
+ * significant bits, so bf16 and fp32 hold it exactly (magnitudes from 0.97 2^128
+ * on were rounded to 2^128, infinity in either type; bf16 rounds results below
+ * 2^-130).
  */
 pmx_status pmx_fp8_store(pmx_handle handle, const void* X, pmx_dtype dtype, int64_t rows, int cols,
                          int64_t ldx, uint8_t* values, int64_t ldv, uint8_t* scales, int64_t lds,

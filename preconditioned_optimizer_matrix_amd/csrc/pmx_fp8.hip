@@ -1,6 +1,25 @@
 // Products of 8-bit values grouped by expert: C[t][j] = sum_k A[t][k] B_e[j][k]
 // over e4m3 values with a power of two for each 128 of k, a row's own for A, a
 // 128 x 128 tile's for B.
+//
+// Design (CDNA4):
+//  * bf16 results: the scaled 8-bit matrix instructions, which take the powers of
+//    two as the bytes they are stored as, so scaling costs nothing.  A lane's four
+//    scale bytes of four k tiles are one register, and each instruction names the
+//    byte it takes.  These instructions add the products of a group with about 20
+//    bits below its largest (K = 1024: 1.5e-5 of the result, whatever C holds and
+//    however short the chain): a hundredth of bf16's own rounding.
+//  * fp32 results: that would be what limits them, so the values are widened to
+//    bf16, exactly, and multiplied at half the rate; the sum over each 128 of k is
+//    scaled (ldexp, exact) and added in fp32.
+//  * Tiles by rule (choose): up to kStreamRows rows a group, weights go from memory
+//    to the matrix cores without LDS, a block's waves sharing the contraction;
+//    64 x 64 and 128 x 128 through LDS, two k tiles; 256 x 256 (bf16) loaded
+//    straight into LDS, two groups of waves taking turns at the matrix cores.
+//  * The matrix instruction's operands are swapped (B first), so a lane ends with
+//    four neighbouring columns of one row of C.
+//  * Rows past a group's end read the group's last row; their results are not
+//    stored.
 #include <algorithm>
 
 #include "pmx_groups.h"
@@ -11,69 +30,573 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// 64 x 64 tiles, four waves of 32 x 32, k tiles of 128 through LDS.
-constexpr int kPitch = 144;
+__device__ __forceinline__ i32x8 join8(i32x4 a, i32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
+// Eight e4m3 values as bf16, exactly.
+__device__ __forceinline__ bf16x8 widen(int lo, int hi) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false),
+               b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true),
+               c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false),
+               d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Rows of C in no group, [0, lo) and [hi, rows): zeros.
 template <typename O>
-__global__ __launch_bounds__(256) void fp8_kernel(Fp8Params p) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * 64 * kPitch];
-  __shared__ Table T;
-  const int tiles_n = (p.n + 63) / 64, kb = p.k / 128;
-  build_table(T, p, 64, tiles_n, 0);
-  const int wid = threadIdx.x >> 6, lane = threadIdx.x & 63, wm = (wid >> 1) * 32, wn = (wid & 1) * 32;
-  uint8_t *sa = smem, *sb = smem + 64 * kPitch;
-  for (int q = blockIdx.x; q < T.tile[p.groups]; q += gridDim.x) {
-    const int e = group_of(T, p.groups, q), r0 = T.begin[e], M = T.begin[e + 1] - r0;
-    int tm, tn;
-    tile_of(q - T.tile[e], (M + 63) / 64, tiles_n, tm, tn);
-    const int m0 = tm * 64, n0 = tn * 64;
-    const uint8_t *A = p.a + (int64_t)r0 * p.lda, *B = p.b + e * p.stride_b;
-    const uint8_t *SA = p.sa + (int64_t)r0 * p.ldsa, *SB = p.sb + e * p.stride_sb;
-    f32x16 acc;
-#pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = 0.f;
-    const int ra = min(m0 + wm + (lane & 31), M - 1), rb = min(n0 + wn + (lane & 31), p.n - 1);
-    for (int kt = 0; kt < kb; ++kt) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int idx = threadIdx.x + 256 * i, r = idx >> 3, c = (idx & 7) * 16;
-        *reinterpret_cast<u32x4_t*>(sa + r * kPitch + c) =
-            *reinterpret_cast<const u32x4_t*>(A + (int64_t)min(m0 + r, M - 1) * p.lda + kt * 128 + c);
-        *reinterpret_cast<u32x4_t*>(sb + r * kPitch + c) =
-            *reinterpret_cast<const u32x4_t*>(B + (int64_t)min(n0 + r, p.n - 1) * p.ldb + kt * 128 + c);
-      }
-      const int ca = SA[(int64_t)ra * p.ldsa + kt], cb = SB[(int64_t)(rb >> 7) * p.ldsb + kt];
-      __syncthreads();
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int o = (lane & 31) * kPitch + 64 * s + 32 * (lane >> 5);
-        const i32x4 a0 = *reinterpret_cast<const i32x4*>(sa + wm * kPitch + o), a1 = *reinterpret_cast<const i32x4*>(sa + wm * kPitch + o + 16);
-        const i32x4 b0 = *reinterpret_cast<const i32x4*>(sb + wn * kPitch + o), b1 = *reinterpret_cast<const i32x4*>(sb + wn * kPitch + o + 16);
-        const i32x8 a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7), b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, 0, 0, 0, cb, 0, ca);
-      }
-    }
-    const int row = m0 + wm + (lane & 31);
-    if (row < M)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int col = n0 + wn + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-        if (col < p.n) {
-          O* c = reinterpret_cast<O*>(p.c) + (int64_t)(r0 + row) * p.ldc + col;
-          if constexpr (sizeof(O) == 4) *c = acc[v];
-          else *c = (O)pack_bf16(acc[v], 0.f);
-        }
-      }
-  }
-  // rows in no group
-  const int lo = T.begin[0], hi = T.begin[p.groups];
+__device__ __forceinline__ void zero_outside(const Fp8Params& p, int lo, int hi) {
   const int64_t outside = lo + (p.rows - hi);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < outside * p.n; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < outside * p.n; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t r = i / p.n;
     reinterpret_cast<O*>(p.c)[(r < lo ? r : hi + r - lo) * p.ldc + (i - r * p.n)] = 0;
   }
+}
+
+// ------------------------------------------------------------ few rows a group
+// A block has 64 columns of a group and RT x 16 of its rows at a time; its four
+// waves take k tiles of 128 in turn and add their results in LDS.  A lane loads
+// 32 bytes of a row of B: 16 rows of whole 128-byte lines an instruction pair.
+template <typename O, int RT>
+__global__ __launch_bounds__(256) void fp8_stream_kernel(Fp8Params p, int slabs) {
+  __shared__ float sum[4][16 * RT][68];
+  const int wid = threadIdx.x >> 6, lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int e = blockIdx.x / slabs, n0 = (blockIdx.x - e * slabs) * 64, kb = p.k / 128;
+  // this group's rows: offsets clamped, and none below an earlier one
+  int first = 0, last = (int)p.rows, lo = 0, hi = (int)p.rows;
+  if (p.offsets) {
+    int a = 0, b = 0;
+    auto offset = [&](int i) {
+      const int64_t o = load_index(p.offsets, i, p.off64);
+      return (int)(o < 0 ? 0 : o > p.rows ? p.rows : o);
+    };
+    const int begin = offset(0);
+    for (int i = lane; i <= p.groups; i += 64) {
+      const int o = offset(i);
+      if (i <= e) a = max(a, o);
+      if (i <= e + 1) b = max(b, o);
+      hi = i == lane ? o : max(hi, o);
+    }
+    if (lane > p.groups) hi = 0;
+    for (int d = 32; d > 0; d >>= 1) {
+      a = max(a, __shfl_xor(a, d));
+      b = max(b, __shfl_xor(b, d));
+      hi = max(hi, __shfl_xor(hi, d));
+    }
+    first = a;
+    last = b;
+    lo = begin;
+  }
+  zero_outside<O>(p, lo, hi);
+  const uint8_t* B[4];
+  const uint8_t* SB = p.sb + e * p.stride_sb + (int64_t)min(n0 >> 7, (p.n - 1) >> 7) * p.ldsb;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) B[c] = p.b + e * p.stride_b + (int64_t)min(n0 + 16 * c + l16, p.n - 1) * p.ldb + 32 * g;
+  for (int r0 = first; r0 < last; r0 += 16 * RT) {
+    f32x4_t acc[4][RT];
+    bool bad[RT];
+    const uint8_t *A[RT], *SA[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int64_t row = min(r0 + 16 * r + l16, last - 1);
+      A[r] = p.a + row * p.lda + 32 * g;
+      SA[r] = p.sa + row * p.ldsa;
+      bad[r] = false;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    i32x8 b[4], a[RT];
+    int cb = 0, ca[RT];
+    auto load = [&](int kt) {
+      const int o = kt * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        b[c] = join8(*reinterpret_cast<const i32x4*>(B[c] + o), *reinterpret_cast<const i32x4*>(B[c] + o + 16));
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        a[r] = join8(*reinterpret_cast<const i32x4*>(A[r] + o), *reinterpret_cast<const i32x4*>(A[r] + o + 16));
+        ca[r] = SA[r][kt];
+      }
+      cb = SB[kt];
+    };
+    if (wid < kb) load(wid);
+    for (int kt = wid; kt < kb; kt += 4) {
+      i32x8 xb[4], xa[RT];
+      int sa[RT];
+      const int sb = cb;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) xb[c] = b[c];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        xa[r] = a[r];
+        sa[r] = ca[r];
+      }
+      if (kt + 4 < kb) load(kt + 4);
+      if constexpr (sizeof(O) == 2) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            acc[c][r] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xb[c], xa[r], acc[c][r], 0, 0, 0, sb, 0, sa[r]);
+      } else {
+        bf16x8 wa[RT][4];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) wa[r][t] = widen(xa[r][2 * t], xa[r][2 * t + 1]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          f32x4_t part[RT];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) part[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const bf16x8 wb = widen(xb[c][2 * t], xb[c][2 * t + 1]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) part[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, wa[r][t], part[r], 0, 0, 0);
+          }
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[c][r][v] += __builtin_ldexpf(part[r][v], sa[r] + sb - 254);
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) bad[r] |= sa[r] == 255 || sb == 255;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f32x4_t v = acc[c][r];
+        if (bad[r])
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = __builtin_nanf("");
+        *reinterpret_cast<f32x4_t*>(&sum[wid][16 * r + l16][16 * c + 4 * g]) = v;
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * RT * 32; i += 256) {
+      const int r = i >> 5, c = (i & 31) * 2, row = r0 + r;
+      if (row >= last || n0 + c >= p.n) continue;
+      float v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) v[j] = (sum[0][r][c + j] + sum[1][r][c + j]) + (sum[2][r][c + j] + sum[3][r][c + j]);
+      O* out = reinterpret_cast<O*>(p.c) + (int64_t)row * p.ldc + n0 + c;
+      if constexpr (sizeof(O) == 2) {
+        const uint32_t u = pack_bf16(v[0], v[1]);
+        out[0] = (O)u;
+        if (n0 + c + 1 < p.n) out[1] = (O)(u >> 16);
+      } else {
+        out[0] = v[0];
+        if (n0 + c + 1 < p.n) out[1] = v[1];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------ tiles through registers and LDS
+// S x S tiles, four waves of S/2 x S/2, k tiles of 128 bytes a row at a pitch of
+// 144 (16 rows' pieces fall on distinct banks), two of them; the next one's loads
+// are under way while one is multiplied.
+constexpr int kPitch = 144;
+
+template <typename O, int S>
+__global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Params p) {
+  constexpr int W = S / 2, F = W / 32, N = S * 8 / 256, STAGE = 2 * S * kPitch;
+  constexpr int OUT = 32 * (W + 16 / (int)sizeof(O)) * (int)sizeof(O);  // a wave's rows of C on their way out
+  static_assert(4 * OUT <= 2 * STAGE, "the waves' rows fit the k tiles' place");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE];
+  __shared__ Table T;
+  const int tiles_n = (p.n + S - 1) / S, kb = p.k / 128;
+  build_table(T, p, S, tiles_n, 0);
+  zero_outside<O>(p, T.begin[0], T.begin[p.groups]);
+  const int wid = threadIdx.x >> 6, lane = threadIdx.x & 63, wm = (wid >> 1) * W, wn = (wid & 1) * W;
+  const int items = T.tile[p.groups];
+  // neighbouring tiles to one XCD: blocks are dealt to the 8 of them in turn
+  const int per = gridDim.x >> 3;
+  for (int q = gridDim.x & 7 ? (int)blockIdx.x : ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3); q < items; q += gridDim.x) {
+    const int e = group_of(T, p.groups, q), r0 = T.begin[e], M = T.begin[e + 1] - r0;
+    int tm, tn;
+    tile_of(q - T.tile[e], (M + S - 1) / S, tiles_n, tm, tn);
+    const int m0 = tm * S, n0 = tn * S;
+    const uint8_t *pa[N], *pb[N], *SA[F], *SB[F];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = threadIdx.x + 256 * i, r = idx >> 3, c = (idx & 7) * 16;
+      pa[i] = p.a + (int64_t)(r0 + min(m0 + r, M - 1)) * p.lda + c;
+      pb[i] = p.b + e * p.stride_b + (int64_t)min(n0 + r, p.n - 1) * p.ldb + c;
+    }
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      SA[i] = p.sa + (int64_t)(r0 + min(m0 + wm + 32 * i + (lane & 31), M - 1)) * p.ldsa;
+      SB[i] = p.sb + e * p.stride_sb + (int64_t)(min(n0 + wn + 32 * i, p.n - 1) >> 7) * p.ldsb;
+    }
+    u32x4_t va[N], vb[N];
+    int ca[F], cb[F];
+    auto load = [&](int kt) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        va[i] = *reinterpret_cast<const u32x4_t*>(pa[i] + kt * 128);
+        vb[i] = *reinterpret_cast<const u32x4_t*>(pb[i] + kt * 128);
+      }
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        ca[i] = SA[i][kt];
+        cb[i] = SB[i][kt];
+      }
+    };
+    auto store = [&](uint8_t* st) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int idx = threadIdx.x + 256 * i, o = (idx >> 3) * kPitch + (idx & 7) * 16;
+        *reinterpret_cast<u32x4_t*>(st + o) = va[i];
+        *reinterpret_cast<u32x4_t*>(st + S * kPitch + o) = vb[i];
+      }
+    };
+    f32x16 acc[F][F];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    bool bad[F][F] = {};
+    load(0);
+    store(smem);
+    __syncthreads();
+    for (int kt = 0; kt < kb; ++kt) {
+      int sa[F], sb[F];
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        sa[i] = ca[i];
+        sb[i] = cb[i];
+      }
+      if (kt + 1 < kb) load(kt + 1);
+      const uint8_t* st = smem + (kt & 1) * STAGE;
+      const uint8_t* la = st + (wm + (lane & 31)) * kPitch + 32 * (lane >> 5);
+      const uint8_t* lb = st + (S + wn + (lane & 31)) * kPitch + 32 * (lane >> 5);
+      auto frag = [&](const uint8_t* q, int i, int s) {
+        const i32x4* f = reinterpret_cast<const i32x4*>(q + i * 32 * kPitch + 64 * s);
+        return join8(f[0], f[1]);
+      };
+      if constexpr (sizeof(O) == 2) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          i32x8 fa[F], fb[F];
+#pragma unroll
+          for (int i = 0; i < F; ++i) {
+            fa[i] = frag(la, i, s);
+            fb[i] = frag(lb, i, s);
+          }
+#pragma unroll
+          for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], acc[i][j], 0, 0, 0, sb[j], 0, sa[i]);
+        }
+      } else {
+        // lane l widens the 8 values from 32 (l / 32) + 8 t on: the same places of k in both operands
+        f32x16 part[F][F];
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < F; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) part[i][j][v] = 0.f;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          i32x8 fa[F], fb[F];
+#pragma unroll
+          for (int i = 0; i < F; ++i) {
+            fa[i] = frag(la, i, s);
+            fb[i] = frag(lb, i, s);
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            bf16x8 xa[F], xb[F];
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+              xa[i] = widen(fa[i][2 * t], fa[i][2 * t + 1]);
+              xb[i] = widen(fb[i][2 * t], fb[i][2 * t + 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+              for (int j = 0; j < F; ++j)
+                part[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xb[j], xa[i], part[i][j], 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < F; ++j) {
+            const int ex = sa[i] + sb[j] - 254;
+            bad[i][j] |= sa[i] == 255 || sb[j] == 255;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] += __builtin_ldexpf(part[i][j][v], ex);
+          }
+      }
+      if (kt + 1 < kb) store(smem + (~kt & 1) * STAGE);
+      __syncthreads();
+    }
+    if constexpr (sizeof(O) == 4)
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+          if (bad[i][j])
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = __builtin_nanf("");
+    O* c = reinterpret_cast<O*>(p.c) + (int64_t)r0 * p.ldc;
+    O* stage = reinterpret_cast<O*>(smem + wid * OUT);
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+      store_rows<W, O>(acc[i], stage, c, p.ldc, m0 + wm + 32 * i, M, n0 + wn, p.n);
+    __syncthreads();  // the k tiles' place is free
+  }
+}
+
+// ------------------------------------------------------------ 256 x 256 tiles
+// Eight waves of 128 x 64, one block a unit.  Operands go from memory straight to
+// LDS, two k tiles of 128 (64 KB each); a load instruction writes its wave's 64 x
+// 16 bytes in lane order, eight rows of 128 bytes, and the 16-byte piece c of row
+// r lies at c ^ swizzle(r), so 16 rows' pieces fall on distinct banks.  Waves 0-3
+// and 4-7 take turns: one group multiplies from registers while the other reads
+// its operands of the k tile from LDS.
+constexpr int kSide = 256, kHalf = 32 * 1024, kStage = 2 * kHalf;  // bytes of an operand's part, of a k tile
+typedef __attribute__((address_space(3))) void* lds_ptr;
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
+
+struct Dma8 {
+  const uint8_t* base;
+  uint32_t off[4];  // of this lane's piece, for the wave's four instructions
+  // rows r0 .. of `limit`, read past the end from the last one
+  __device__ __forceinline__ void init(const uint8_t* b, int64_t ld, int r0, int limit, int wid) {
+    const int lane = threadIdx.x & 63;
+    base = b + (int64_t)r0 * ld;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 32 * wid + 8 * j + (lane >> 3);
+      off[j] = (uint32_t)(min(row, limit - 1 - r0) * (int)ld + (((lane & 7) ^ swizzle(row)) * 16));
+    }
+  }
+  __device__ __forceinline__ void issue(uint8_t* part, int kt, int wid) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_global_load_lds((const void*)(base + kt * 128 + off[j]), (lds_ptr)(part + (4 * wid + j) * 1024), 16, 0, 0);
+  }
+};
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
+}
+
+// Two row tiles of 32 (4096 bytes apart), both halves of the k tile: at[s][q] is the
+// lane's address of piece q of half s.  The reads are written out, with their wait
+// in the same block: the compiler takes any LDS read it sees to depend on the loads
+// to LDS under way and would wait for all of them.
+template <int OFF>
+__device__ __forceinline__ void read_two(i32x8 (&f)[2][2], const uint32_t (&at)[2][2]) {
+  i32x4 x[8];
+  asm volatile(
+      "ds_read_b128 %0, %8 offset:%c12\n\t"
+      "ds_read_b128 %1, %9 offset:%c12\n\t"
+      "ds_read_b128 %2, %8 offset:%c13\n\t"
+      "ds_read_b128 %3, %9 offset:%c13\n\t"
+      "ds_read_b128 %4, %10 offset:%c12\n\t"
+      "ds_read_b128 %5, %11 offset:%c12\n\t"
+      "ds_read_b128 %6, %10 offset:%c13\n\t"
+      "ds_read_b128 %7, %11 offset:%c13\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+      : "v"(at[0][0]), "v"(at[0][1]), "v"(at[1][0]), "v"(at[1][1]), "n"(OFF), "n"(OFF + 4096)
+      : "memory");
+  f[0][0] = join8(x[0], x[1]);
+  f[0][1] = join8(x[2], x[3]);
+  f[1][0] = join8(x[4], x[5]);
+  f[1][1] = join8(x[6], x[7]);
+}
+
+// Four scale bytes, k tiles kt .. kt + 3 of a row of kb >= 4 (zeros past its end).
+__device__ __forceinline__ int load_scales(const uint8_t* s, int kt, int kb) {
+  typedef uint32_t u32_a1 __attribute__((aligned(1)));
+  const int o = min(kt, kb - 4);
+  return (int)(*reinterpret_cast<const u32_a1*>(s + o) >> (8 * (kt - o)));
+}
+
+__global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
+  __shared__ Table T;
+  const int tiles_n = (p.n + kSide - 1) / kSide, kb = p.k / 128;
+  build_table(T, p, kSide, tiles_n, 0);
+  zero_outside<uint16_t>(p, T.begin[0], T.begin[p.groups]);
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = wid >> 2, lane = threadIdx.x & 63;
+  const int wm = group * 128, wn = (wid & 3) * 64;
+  const int items = T.tile[p.groups];
+  int q0 = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);  // the grid is a multiple of 8
+  struct Item {
+    int e, r0, m0, n0, M;
+  };
+  auto next = [&](Item& it) -> bool {
+    if (q0 >= items) return false;
+    it.e = __builtin_amdgcn_readfirstlane(group_of(T, p.groups, q0));
+    it.r0 = __builtin_amdgcn_readfirstlane(T.begin[it.e]);
+    it.M = __builtin_amdgcn_readfirstlane(T.begin[it.e + 1]) - it.r0;
+    int tm, tn;
+    tile_of(q0 - __builtin_amdgcn_readfirstlane(T.tile[it.e]), (it.M + kSide - 1) / kSide, tiles_n, tm, tn);
+    it.m0 = tm * kSide;
+    it.n0 = tn * kSide;
+    q0 += gridDim.x;
+    return true;
+  };
+  Dma8 A, B;
+  // this lane's pieces of its wave's rows in a k tile
+  uint32_t at[2][2];
+  const int r = lane & 31;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      at[s][q] = lds_address(smem) + r * 128 + ((4 * s + 2 * (lane >> 5) + q) ^ swizzle(r)) * 16;
+  const uint8_t *SA, *SB;
+  uint32_t so[4];
+  int ca[4], cb, na[4], nb;  // scale bytes of this chunk of four k tiles, and of the next
+  auto issue = [&](int kt) {
+    uint8_t* st = smem + (kt & 1) * kStage;
+    A.issue(st, kt, wid);
+    B.issue(st + kHalf, kt, wid);
+  };
+  auto start = [&](const Item& it) {
+    A.init(p.a + (int64_t)it.r0 * p.lda, p.lda, it.m0, it.M, wid);
+    B.init(p.b + it.e * p.stride_b, p.ldb, it.n0, p.n, wid);
+    SA = p.sa + (int64_t)(it.r0 + it.m0) * p.ldsa;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      so[i] = (uint32_t)(min(wm + 32 * i + r, it.M - 1 - it.m0) * (int)p.ldsa);
+      na[i] = load_scales(SA + so[i], 0, kb);
+    }
+    SB = p.sb + it.e * p.stride_sb + (int64_t)(min(it.n0 + wn, p.n - 1) >> 7) * p.ldsb;
+    nb = load_scales(SB, 0, kb);
+    issue(0);
+  };
+  Item it;
+  if (!next(it)) return;
+  start(it);
+  for (;;) {
+    f32x16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    // k tile 0 has landed for this wave, then for every wave
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (group) {  // the second group is one turn behind
+      if (1 < kb) issue(1);
+      __builtin_amdgcn_s_barrier();
+    }
+    // k tile kt's turns.  Its place is refilled with kt + 2, and kt + 1's with kt + 1,
+    // once the second group has read what was there: the first group issues at the
+    // start of its reading turn, the second, at the same time, before it multiplies.
+    // Both see their loads landed at the end of the next turn, before kt + 1 is read.
+    auto turn = [&](int kt, auto byte) {
+      constexpr int J = decltype(byte)::value;
+      if (!group && kt + 1 < kb) issue(kt + 1);
+      const uint32_t sa = (kt & 1) * kStage + wm * 128, sb = (kt & 1) * kStage + kHalf + wn * 128;
+      uint32_t a[2][2], b[2][2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          a[s][q] = at[s][q] + sa;
+          b[s][q] = at[s][q] + sb;
+        }
+      i32x8 fb[2][2], f0[2][2], f1[2][2];
+      read_two<0>(fb, b);
+      read_two<0>(f0, a);
+      read_two<8192>(f1, a);
+      if (group) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      if (group && kt + 2 < kb) issue(kt + 2);
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[s][j], i < 2 ? f0[s][i] : f1[s][i - 2], acc[i][j],
+                                                                       0, 0, J, cb, J, ca[i]);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (!group) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    for (int kt = 0; kt < kb; kt += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ca[i] = na[i];
+      cb = nb;
+      if (kt + 4 < kb) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) na[i] = load_scales(SA + so[i], kt + 4, kb);
+        nb = load_scales(SB, kt + 4, kb);
+      }
+      turn(kt, std::integral_constant<int, 0>());
+      if (kt + 1 < kb) turn(kt + 1, std::integral_constant<int, 1>());
+      if (kt + 2 < kb) turn(kt + 2, std::integral_constant<int, 2>());
+      if (kt + 3 < kb) turn(kt + 3, std::integral_constant<int, 3>());
+    }
+    if (!group) __builtin_amdgcn_s_barrier();
+    const Item done = it;
+    const bool more = next(it);
+    if (more) start(it);  // the first k tile's place; the results leave through the second's
+    uint16_t* c = reinterpret_cast<uint16_t*>(p.c) + (int64_t)done.r0 * p.ldc;
+    uint16_t* stage = reinterpret_cast<uint16_t*>(smem + kStage + wid * 32 * (64 + 8) * 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      store_rows<64, uint16_t>(acc[i], stage, c, p.ldc, done.m0 + wm + 32 * i, done.M, done.n0 + wn, p.n);
+    if (!more) return;
+    __syncthreads();  // the second k tile's place is free
+  }
+}
+
+// ------------------------------------------------------------ launchers
+constexpr int kStreamRows = 32;
+enum { STREAM = 0, SMALL = 1, MIDDLE = 2, LARGE = 3 };
+
+int choose(int64_t rows, int k, int n, int groups, int out_dtype, int num_cu) {
+  const int64_t avg = rows / groups;
+  if (avg <= kStreamRows) return STREAM;
+  if (out_dtype == PMX_BF16 && avg >= 256 && n >= 256 && k >= 512 && (rows / 256) * ((n + 255) / 256) >= num_cu) return LARGE;
+  if ((rows / 128 + groups) * ((n + 127) / 128) >= num_cu) return MIDDLE;
+  return SMALL;
+}
+
+template <typename O>
+hipError_t launch(const Fp8Params& p, hipStream_t s) {
+  const int cfg = choose(p.rows, p.k, p.n, p.groups, p.out_dtype, p.num_cu);
+  if (cfg == STREAM) {
+    const int slabs = (p.n + 63) / 64;
+    const dim3 grid((unsigned)(slabs * p.groups));
+    if (p.rows <= 8 * (int64_t)p.groups) fp8_stream_kernel<O, 1><<<grid, 256, 0, s>>>(p, slabs);
+    else fp8_stream_kernel<O, 2><<<grid, 256, 0, s>>>(p, slabs);
+  } else if (cfg == LARGE) {
+    if constexpr (sizeof(O) == 2) fp8_large_kernel<<<dim3((unsigned)(p.num_cu / 8 * 8)), 512, 0, s>>>(p);
+  } else {
+    const int side = cfg == SMALL ? 64 : 128;
+    const int64_t tiles = (p.rows / side + std::min<int64_t>(p.groups, p.rows)) * ((p.n + side - 1) / side);
+    const dim3 grid((unsigned)std::min<int64_t>(tiles, p.num_cu * (cfg == SMALL ? 3 : 2)));
+    if (cfg == SMALL) fp8_tile_kernel<O, 64><<<grid, 256, 0, s>>>(p);
+    else fp8_tile_kernel<O, 128><<<grid, 256, 0, s>>>(p);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -81,11 +604,7 @@ __global__ __launch_bounds__(256) void fp8_kernel(Fp8Params p) {
 int fp8_splits(int64_t rows, int k, int n, int groups) { return 1; }
 
 hipError_t launch_fp8(const Fp8Params& p, hipStream_t s) {
-  const int64_t tiles = (p.rows / 64 + std::min<int64_t>(p.groups, p.rows)) * ((p.n + 63) / 64);
-  const dim3 grid((unsigned)std::min<int64_t>(tiles, p.num_cu * 8));
-  if (p.out_dtype == PMX_BF16) fp8_kernel<uint16_t><<<grid, 256, 0, s>>>(p);
-  else fp8_kernel<float><<<grid, 256, 0, s>>>(p);
-  return hipGetLastError();
+  return p.out_dtype == PMX_BF16 ? launch<uint16_t>(p, s) : launch<float>(p, s);
 }
 
 }  // namespace pmx

@@ -56,15 +56,24 @@ template <class C>
 __device__ __forceinline__ void load_param(float (&w)[C::NV][C::V], const void* p, int dtype, int cols, int lane,
                                            float other) {
 #pragma unroll
-  for (int i = 0; i < C::NV; ++i)
+  for (int i = 0; i < C::NV; ++i) {
+    const int c = (i * C::LANES + lane) * C::V;
+    if (!p) {
 #pragma unroll
-    for (int j = 0; j < C::V; ++j) {
-      const int c = (i * C::LANES + lane) * C::V + j;
-      w[i][j] = other;
-      if (p && c < cols)
-        w[i][j] = dtype == PMX_BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[c] << 16)
-                                    : reinterpret_cast<const float*>(p)[c];
+      for (int j = 0; j < C::V; ++j) w[i][j] = other;
+    } else if (dtype == PMX_F32) {
+#pragma unroll
+      for (int k = 0; k < C::V; k += 4) {
+        const u32x4_t v = load_piece(reinterpret_cast<const float*>(p), c + k, cols);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i][k + j] = element<float>(v, j);
+      }
+    } else {
+      const u32x4_t v = load_piece(reinterpret_cast<const uint16_t*>(p), c, cols);
+#pragma unroll
+      for (int j = 0; j < C::V; ++j) w[i][j] = element<uint16_t>(v, j);
     }
+  }
 }
 
 template <class C>
@@ -81,7 +90,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormParams p) {
   __shared__ float red[2][C::TEAMS * C::W][1];
   const int team = threadIdx.x / C::LANES, lane = threadIdx.x % C::LANES;
   const int64_t step = (int64_t)gridDim.x * C::TEAMS;
-  const float inv = 1.f / (float)p.cols;
+  const float cols = (float)p.cols;
   int flip = 0;
   int64_t base = (int64_t)blockIdx.x * C::TEAMS;
   // the block's teams go round together (barriers); a team past the end repeats the last row
@@ -101,7 +110,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormParams p) {
 #pragma unroll
       for (int j = 0; j < C::V; ++j) s[0] += element<E>(x[i], j);
     team_sum<C, 1>(s, red, flip);
-    const float mean = s[0] * inv;
+    const float mean = s[0] / cols;  // a row of equal values has their mean
     s[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < C::NV; ++i)
@@ -111,7 +120,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormParams p) {
         if ((i * C::LANES + lane) * C::V + j < p.cols) s[0] += d * d;
       }
     team_sum<C, 1>(s, red, flip);
-    const float r = 1.f / sqrtf(s[0] * inv + p.eps);
+    const float r = 1.f / sqrtf(s[0] / cols + p.eps);
     const int64_t row = base + team;
     if (row < p.rows) {
       E* y = reinterpret_cast<E*>(p.y) + row * p.ldy;
@@ -234,22 +243,31 @@ __global__ __launch_bounds__(C::THREADS) void norm_grad_kernel(NormParams p) {
       }
 }
 
-// dw and db: the blocks' sums in their order, eight segments of them at a time.
-__global__ __launch_bounds__(256) void norm_join_kernel(NormParams p) {
-  __shared__ float seg[8][32];
+// dw and db: the blocks' sums in their order, 32 segments of them at a time.
+__global__ __launch_bounds__(1024) void norm_join_kernel(NormParams p) {
+  __shared__ float seg[32][33];
   const int in = threadIdx.x & 31, s = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + in;  // of 2 cols
   const int64_t wide = 2 * (int64_t)p.cols;
-  const int per = (p.blocks + 7) / 8, b0 = min(s * per, p.blocks), b1 = min(b0 + per, p.blocks);
+  const int per = (p.blocks + 31) / 32, b0 = min(s * per, p.blocks), b1 = min(b0 + per, p.blocks);
   float v = 0.f;
-  if (c < wide)
-    for (int b = b0; b < b1; ++b) v += p.part[b * wide + c];
+  if (c < wide) {
+    int b = b0;
+    for (; b + 8 <= b1; b += 8) {  // eight loads on their way
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = p.part[(b + i) * wide + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += x[i];
+    }
+    for (; b < b1; ++b) v += p.part[b * wide + c];
+  }
   seg[s][in] = v;
   __syncthreads();
   if (s == 0 && c < wide) {
     float t = seg[0][in];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += seg[i][in];
+    for (int i = 1; i < 32; ++i) t += seg[i][in];
     float* out = c < p.cols ? p.dw : p.db;
     if (out) {
       out += c < p.cols ? c : c - p.cols;
@@ -264,6 +282,11 @@ hipError_t with_cfg(int cols, F&& f) {
   constexpr int V = kPiece<E>;
   if (cols <= 64 * V) return f(NCfg<E, 1, 1, 8>());
   if (cols <= 128 * V) return f(NCfg<E, 1, 2, 8>());
+  if constexpr (sizeof(E) == 4) {
+    if (cols <= 256 * V) return f(NCfg<E, 1, 4, 8>());
+  } else {
+    if (cols <= 256 * V) return f(NCfg<E, 4, 1, 2>());
+  }
   if (cols <= 512 * V) return f(NCfg<E, 4, 2, 2>());
   if (cols <= 1024 * V) return f(NCfg<E, 4, 4, 2>());
   if (cols <= 2048 * V) return f(NCfg<E, 16, 2, 1>());
@@ -314,7 +337,7 @@ hipError_t launch_norm_grad(NormParams p, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (!params) return hipSuccess;
-  norm_join_kernel<<<dim3((2 * p.cols + 31) / 32), dim3(256), 0, s>>>(p);
+  norm_join_kernel<<<dim3((2 * p.cols + 31) / 32), dim3(1024), 0, s>>>(p);
   return hipGetLastError();
 }
 
