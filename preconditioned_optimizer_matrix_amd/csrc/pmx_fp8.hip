@@ -367,25 +367,27 @@ __global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Param
 // its operands of the k tile from LDS.
 constexpr int kSide = 256, kHalf = 32 * 1024, kStage = 2 * kHalf;  // bytes of an operand's part, of a k tile
 typedef __attribute__((address_space(3))) void* lds_ptr;
-__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int swizzle(int row) { return row & 7; }
 
+// One operand's tile of 256 rows as a buffer resource: rows past the end read as
+// zeros.  The offset within the wave's eight rows is the lane's, the rest uniform.
 struct Dma8 {
-  const uint8_t* base;
-  uint32_t off[4];  // of this lane's piece, for the wave's four instructions
-  // rows r0 .. of `limit`, read past the end from the last one
-  __device__ __forceinline__ void init(const uint8_t* b, int64_t ld, int r0, int limit, int wid) {
-    const int lane = threadIdx.x & 63;
-    base = b + (int64_t)r0 * ld;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = 32 * wid + 8 * j + (lane >> 3);
-      off[j] = (uint32_t)(min(row, limit - 1 - r0) * (int)ld + (((lane & 7) ^ swizzle(row)) * 16));
-    }
+  __amdgpu_buffer_rsrc_t rsrc;
+  int ld;
+  __device__ __forceinline__ void init(const uint8_t* b, int64_t ld_, int r0, int limit, int k) {
+    ld = (int)ld_;
+    const int rows = min(kSide, limit - r0);
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(b) + (int64_t)r0 * ld_, 0, (rows - 1) * ld + k, 0x00020000);
   }
-  __device__ __forceinline__ void issue(uint8_t* part, int kt, int wid) const {
+  __device__ __forceinline__ uint32_t lane_offset() const {
+    const int lane = threadIdx.x & 63;
+    return (uint32_t)((lane >> 3) * ld + (((lane & 7) ^ swizzle(lane >> 3)) * 16));
+  }
+  __device__ __forceinline__ void issue(uint8_t* part, uint32_t off, int kt, int wid) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      __builtin_amdgcn_global_load_lds((const void*)(base + kt * 128 + off[j]), (lds_ptr)(part + (4 * wid + j) * 1024), 16, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(part + (4 * wid + j) * 1024), 16, off,
+                                               kt * 128 + (32 * wid + 8 * j) * ld, 0, 0);
   }
 };
 __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
@@ -418,21 +420,107 @@ __device__ __forceinline__ void read_two(i32x8 (&f)[2][2], const uint32_t (&at)[
   f[1][1] = join8(x[6], x[7]);
 }
 
-// Four scale bytes, k tiles kt .. kt + 3 of a row of kb >= 4 (zeros past its end).
-__device__ __forceinline__ int load_scales(const uint8_t* s, int kt, int kb) {
-  typedef uint32_t u32_a1 __attribute__((aligned(1)));
-  const int o = min(kt, kb - 4);
-  return (int)(*reinterpret_cast<const u32_a1*>(s + o) >> (8 * (kt - o)));
+struct Large {
+  Dma8 A, B;
+  uint32_t oa, ob;     // this lane's offsets in their eight rows
+  uint32_t at[2][2];   // of its pieces of row lane % 32 of a part, in LDS
+  const uint8_t *SA, *SB;
+  uint32_t so[4];      // its rows' scales from SA on
+  uint8_t* smem;
+  int kb, wid, wm, wn;
+  __device__ __forceinline__ void issue(int kt) const {  // past the last k tile: the last one again
+    uint8_t* st = smem + (kt & 1) * kStage;
+    const int k = min(kt, kb - 1);
+    A.issue(st, oa, k, wid);
+    B.issue(st + kHalf, ob, k, wid);
+  }
+};
+
+// The k tiles of one item for one of the two groups; the first has landed.  k tile
+// kt's place takes kt + 2 once the second group has read it: the first group issues
+// its share at the start of its next reading turn, the second at the same time, before
+// it multiplies.  Both see their loads landed at the end of the turn after that,
+// before the first group reads.  So a load has two turns' time.
+template <int GROUP>
+__device__ __forceinline__ void large_loop(f32x16 (&acc)[4][2], const Large& L) {
+  if constexpr (GROUP == 1) {  // one turn behind
+    L.issue(1);
+    __builtin_amdgcn_s_barrier();
+  }
+  int ca[4], cb;
+#pragma unroll 1
+  for (int kt = 0; kt < L.kb; ++kt) {
+    // the lowest bytes are this k tile's: four bytes of a row at a time, its last four at its end
+    int shift = 8;
+    if ((kt & 3) == 0) {
+      typedef int int_a1 __attribute__((aligned(1)));
+      const int o = min(kt, L.kb - 4);
+      shift = 8 * (kt - o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ca[i] = *reinterpret_cast<const int_a1*>(L.SA + L.so[i] + o);
+      cb = *reinterpret_cast<const int_a1*>(L.SB + o);
+    }
+    if constexpr (GROUP == 0) L.issue(kt + 1);
+    uint32_t a[2][2], b[2][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        a[s][q] = L.at[s][q] + ((kt & 1) * kStage + L.wm * 128);
+        b[s][q] = L.at[s][q] + ((kt & 1) * kStage + kHalf + L.wn * 128);
+      }
+    i32x8 fb[2][2], f0[2][2], f1[2][2];
+    read_two<0>(fb, b);
+    read_two<0>(f0, a);
+    read_two<8192>(f1, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ca[i] = (int)((uint32_t)ca[i] >> shift);
+    cb = (int)((uint32_t)cb >> shift);
+    if constexpr (GROUP == 1) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (GROUP == 1) L.issue(kt + 2);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[s][j], i < 2 ? f0[s][i] : f1[s][i - 2], acc[i][j],
+                                                                     0, 0, 0, cb, 0, ca[i]);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (GROUP == 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if constexpr (GROUP == 0) __builtin_amdgcn_s_barrier();
+  // what was issued past the last k tile has landed before the places are used again
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
 }
 
 __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
   __shared__ Table T;
-  const int tiles_n = (p.n + kSide - 1) / kSide, kb = p.k / 128;
+  const int tiles_n = (p.n + kSide - 1) / kSide;
   build_table(T, p, kSide, tiles_n, 0);
   zero_outside<uint16_t>(p, T.begin[0], T.begin[p.groups]);
-  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = wid >> 2, lane = threadIdx.x & 63;
-  const int wm = group * 128, wn = (wid & 3) * 64;
+  const int lane = threadIdx.x & 63, r = lane & 31;
+  Large L;
+  L.smem = smem;
+  L.kb = p.k / 128;
+  L.wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  L.wm = (L.wid >> 2) * 128;
+  L.wn = (L.wid & 3) * 64;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      L.at[s][q] = lds_address(smem) + r * 128 + ((4 * s + 2 * (lane >> 5) + q) ^ swizzle(r)) * 16;
   const int items = T.tile[p.groups];
   int q0 = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);  // the grid is a multiple of 8
   struct Item {
@@ -445,40 +533,21 @@ __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
     it.M = __builtin_amdgcn_readfirstlane(T.begin[it.e + 1]) - it.r0;
     int tm, tn;
     tile_of(q0 - __builtin_amdgcn_readfirstlane(T.tile[it.e]), (it.M + kSide - 1) / kSide, tiles_n, tm, tn);
-    it.m0 = tm * kSide;
-    it.n0 = tn * kSide;
+    it.m0 = __builtin_amdgcn_readfirstlane(tm * kSide);
+    it.n0 = __builtin_amdgcn_readfirstlane(tn * kSide);
     q0 += gridDim.x;
     return true;
   };
-  Dma8 A, B;
-  // this lane's pieces of its wave's rows in a k tile
-  uint32_t at[2][2];
-  const int r = lane & 31;
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      at[s][q] = lds_address(smem) + r * 128 + ((4 * s + 2 * (lane >> 5) + q) ^ swizzle(r)) * 16;
-  const uint8_t *SA, *SB;
-  uint32_t so[4];
-  int ca[4], cb, na[4], nb;  // scale bytes of this chunk of four k tiles, and of the next
-  auto issue = [&](int kt) {
-    uint8_t* st = smem + (kt & 1) * kStage;
-    A.issue(st, kt, wid);
-    B.issue(st + kHalf, kt, wid);
-  };
   auto start = [&](const Item& it) {
-    A.init(p.a + (int64_t)it.r0 * p.lda, p.lda, it.m0, it.M, wid);
-    B.init(p.b + it.e * p.stride_b, p.ldb, it.n0, p.n, wid);
-    SA = p.sa + (int64_t)(it.r0 + it.m0) * p.ldsa;
+    L.A.init(p.a + (int64_t)it.r0 * p.lda, p.lda, it.m0, it.M, p.k);
+    L.B.init(p.b + it.e * p.stride_b, p.ldb, it.n0, p.n, p.k);
+    L.oa = L.A.lane_offset();
+    L.ob = L.B.lane_offset();
+    L.SA = p.sa + (int64_t)(it.r0 + it.m0) * p.ldsa;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      so[i] = (uint32_t)(min(wm + 32 * i + r, it.M - 1 - it.m0) * (int)p.ldsa);
-      na[i] = load_scales(SA + so[i], 0, kb);
-    }
-    SB = p.sb + it.e * p.stride_sb + (int64_t)(min(it.n0 + wn, p.n - 1) >> 7) * p.ldsb;
-    nb = load_scales(SB, 0, kb);
-    issue(0);
+    for (int i = 0; i < 4; ++i) L.so[i] = (uint32_t)(min(L.wm + 32 * i + r, it.M - 1 - it.m0) * (int)p.ldsa);
+    L.SB = p.sb + it.e * p.stride_sb + (int64_t)(min(it.n0 + L.wn, p.n - 1) >> 7) * p.ldsb;
+    L.issue(0);
   };
   Item it;
   if (!next(it)) return;
@@ -494,74 +563,16 @@ __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
     // k tile 0 has landed for this wave, then for every wave
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
-    if (group) {  // the second group is one turn behind
-      if (1 < kb) issue(1);
-      __builtin_amdgcn_s_barrier();
-    }
-    // k tile kt's turns.  Its place is refilled with kt + 2, and kt + 1's with kt + 1,
-    // once the second group has read what was there: the first group issues at the
-    // start of its reading turn, the second, at the same time, before it multiplies.
-    // Both see their loads landed at the end of the next turn, before kt + 1 is read.
-    auto turn = [&](int kt, auto byte) {
-      constexpr int J = decltype(byte)::value;
-      if (!group && kt + 1 < kb) issue(kt + 1);
-      const uint32_t sa = (kt & 1) * kStage + wm * 128, sb = (kt & 1) * kStage + kHalf + wn * 128;
-      uint32_t a[2][2], b[2][2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          a[s][q] = at[s][q] + sa;
-          b[s][q] = at[s][q] + sb;
-        }
-      i32x8 fb[2][2], f0[2][2], f1[2][2];
-      read_two<0>(fb, b);
-      read_two<0>(f0, a);
-      read_two<8192>(f1, a);
-      if (group) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      if (group && kt + 2 < kb) issue(kt + 2);
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[s][j], i < 2 ? f0[s][i] : f1[s][i - 2], acc[i][j],
-                                                                       0, 0, J, cb, J, ca[i]);
-      __builtin_amdgcn_s_setprio(0);
-      __builtin_amdgcn_sched_barrier(0);
-      if (!group) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    for (int kt = 0; kt < kb; kt += 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ca[i] = na[i];
-      cb = nb;
-      if (kt + 4 < kb) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) na[i] = load_scales(SA + so[i], kt + 4, kb);
-        nb = load_scales(SB, kt + 4, kb);
-      }
-      turn(kt, std::integral_constant<int, 0>());
-      if (kt + 1 < kb) turn(kt + 1, std::integral_constant<int, 1>());
-      if (kt + 2 < kb) turn(kt + 2, std::integral_constant<int, 2>());
-      if (kt + 3 < kb) turn(kt + 3, std::integral_constant<int, 3>());
-    }
-    if (!group) __builtin_amdgcn_s_barrier();
+    if (L.wid >> 2) large_loop<1>(acc, L);
+    else large_loop<0>(acc, L);
     const Item done = it;
     const bool more = next(it);
     if (more) start(it);  // the first k tile's place; the results leave through the second's
     uint16_t* c = reinterpret_cast<uint16_t*>(p.c) + (int64_t)done.r0 * p.ldc;
-    uint16_t* stage = reinterpret_cast<uint16_t*>(smem + kStage + wid * 32 * (64 + 8) * 2);
+    uint16_t* stage = reinterpret_cast<uint16_t*>(smem + kStage + L.wid * 32 * (64 + 8) * 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      store_rows<64, uint16_t>(acc[i], stage, c, p.ldc, done.m0 + wm + 32 * i, done.M, done.n0 + wn, p.n);
+      store_rows<64, uint16_t>(acc[i], stage, c, p.ldc, done.m0 + L.wm + 32 * i, done.M, done.n0 + L.wn, p.n);
     if (!more) return;
     __syncthreads();  // the second k tile's place is free
   }
