@@ -367,7 +367,7 @@ __global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Param
 // its operands of the k tile from LDS.
 constexpr int kSide = 256, kHalf = 32 * 1024, kStage = 2 * kHalf;  // bytes of an operand's part, of a k tile
 typedef __attribute__((address_space(3))) void* lds_ptr;
-__device__ __forceinline__ int swizzle(int row) { return row & 7; }
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }  // row & 7: every second access waits for its bank
 
 // One operand's tile of 256 rows as a buffer resource: rows past the end read as
 // zeros.  The offset within the wave's eight rows is the lane's, the rest uniform.
@@ -379,15 +379,15 @@ struct Dma8 {
     const int rows = min(kSide, limit - r0);
     rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(b) + (int64_t)r0 * ld_, 0, (rows - 1) * ld + k, 0x00020000);
   }
-  __device__ __forceinline__ uint32_t lane_offset() const {
+  // even and odd groups of eight rows
+  __device__ __forceinline__ void lane_offsets(uint32_t (&off)[2]) const {
     const int lane = threadIdx.x & 63;
-    return (uint32_t)((lane >> 3) * ld + (((lane & 7) ^ swizzle(lane >> 3)) * 16));
-  }
-  __device__ __forceinline__ void issue(uint8_t* part, uint32_t off, int kt, int wid) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(part + (4 * wid + j) * 1024), 16, off,
-                                               kt * 128 + (32 * wid + 8 * j) * ld, 0, 0);
+    for (int j = 0; j < 2; ++j) off[j] = (uint32_t)((lane >> 3) * ld + ((lane & 7) ^ swizzle(8 * j + (lane >> 3))) * 16);
+  }
+  // the q-th eight rows of k tile kt
+  __device__ __forceinline__ void load(uint8_t* part, const uint32_t (&off)[2], int kt, int q) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(part + q * 1024), 16, off[q & 1], kt * 128 + 8 * q * ld, 0, 0);
   }
 };
 __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
@@ -422,30 +422,36 @@ __device__ __forceinline__ void read_two(i32x8 (&f)[2][2], const uint32_t (&at)[
 
 struct Large {
   Dma8 A, B;
-  uint32_t oa, ob;     // this lane's offsets in their eight rows
+  uint32_t oa[2], ob[2];  // this lane's offsets in their eight rows
   uint32_t at[2][2];   // of its pieces of row lane % 32 of a part, in LDS
   const uint8_t *SA, *SB;
   uint32_t so[4];      // its rows' scales from SA on
   uint8_t* smem;
   int kb, wid, wm, wn;
-  __device__ __forceinline__ void issue(int kt) const {  // past the last k tile: the last one again
-    uint8_t* st = smem + (kt & 1) * kStage;
-    const int k = min(kt, kb - 1);
-    A.issue(st, oa, k, wid);
-    B.issue(st + kHalf, ob, k, wid);
+  // past the last k tile: the last one again, into a place that nobody reads any more
+  __device__ __forceinline__ void load_a(int kt, int q) const { A.load(smem + (kt & 1) * kStage, oa, min(kt, kb - 1), q); }
+  __device__ __forceinline__ void load_b(int kt, int q) const {
+    B.load(smem + (kt & 1) * kStage + kHalf, ob, min(kt, kb - 1), q);
   }
 };
 
-// The k tiles of one item for one of the two groups; the first has landed.  k tile
-// kt's place takes kt + 2 once the second group has read it: the first group issues
-// its share at the start of its next reading turn, the second at the same time, before
-// it multiplies.  Both see their loads landed at the end of the turn after that,
-// before the first group reads.  So a load has two turns' time.
+// The k tiles of one item for one of the two groups; the first has landed.  In turn
+// 2 kt the first group reads k tile kt and the second multiplies kt - 1, in turn
+// 2 kt + 1 they change.  Loads are issued between the matrix instructions, where
+// they cost no time: the second group's turn loads B's k tile kt + 1, whose place
+// both have read; the first group's loads its own half of A's k tile kt + 2, and
+// the second's half of kt + 1.  Each has a turn and a half to land, by the end of
+// the turn before it is read.
 template <int GROUP>
 __device__ __forceinline__ void large_loop(f32x16 (&acc)[4][2], const Large& L) {
+  const int w = L.wid & 3;
   if constexpr (GROUP == 1) {  // one turn behind
-    L.issue(1);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) L.load_b(1, 8 * w + j);
     __builtin_amdgcn_s_barrier();
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) L.load_a(1, 4 * w + j);
   }
   int ca[4], cb;
 #pragma unroll 1
@@ -460,7 +466,6 @@ __device__ __forceinline__ void large_loop(f32x16 (&acc)[4][2], const Large& L) 
       for (int i = 0; i < 4; ++i) ca[i] = *reinterpret_cast<const int_a1*>(L.SA + L.so[i] + o);
       cb = *reinterpret_cast<const int_a1*>(L.SB + o);
     }
-    if constexpr (GROUP == 0) L.issue(kt + 1);
     uint32_t a[2][2], b[2][2];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -476,23 +481,31 @@ __device__ __forceinline__ void large_loop(f32x16 (&acc)[4][2], const Large& L) 
 #pragma unroll
     for (int i = 0; i < 4; ++i) ca[i] = (int)((uint32_t)ca[i] >> shift);
     cb = (int)((uint32_t)cb >> shift);
+    // B's kt + 1 has landed; the second group's half of A's kt (its own half of kt + 1 may be under way)
     if constexpr (GROUP == 1) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (GROUP == 1) L.issue(kt + 2);
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[s][j], i < 2 ? f0[s][i] : f1[s][i - 2], acc[i][j],
                                                                      0, 0, 0, cb, 0, ca[i]);
+        const int t = 4 * s + i;  // a load after every two of the first matrix instructions
+        if constexpr (GROUP == 1) L.load_b(kt + 2, 8 * w + t);
+        else if (t < 4) L.load_a(kt + 1, 16 + 4 * w + t);
+        else L.load_a(kt + 2, 4 * w + t - 4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (GROUP == 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // the first group's half of A's kt + 1, which the loads of this turn follow
+    if constexpr (GROUP == 0) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
@@ -541,13 +554,17 @@ __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
   auto start = [&](const Item& it) {
     L.A.init(p.a + (int64_t)it.r0 * p.lda, p.lda, it.m0, it.M, p.k);
     L.B.init(p.b + it.e * p.stride_b, p.ldb, it.n0, p.n, p.k);
-    L.oa = L.A.lane_offset();
-    L.ob = L.B.lane_offset();
+    L.A.lane_offsets(L.oa);
+    L.B.lane_offsets(L.ob);
     L.SA = p.sa + (int64_t)(it.r0 + it.m0) * p.ldsa;
 #pragma unroll
     for (int i = 0; i < 4; ++i) L.so[i] = (uint32_t)(min(L.wm + 32 * i + r, it.M - 1 - it.m0) * (int)p.ldsa);
     L.SB = p.sb + it.e * p.stride_sb + (int64_t)(min(it.n0 + L.wn, p.n - 1) >> 7) * p.ldsb;
-    L.issue(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      L.load_a(0, 4 * L.wid + j);
+      L.load_b(0, 4 * L.wid + j);
+    }
   };
   Item it;
   if (!next(it)) return;
