@@ -359,45 +359,43 @@ __global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Param
 }
 
 // ------------------------------------------------------------ 256 x 256 tiles
-// Eight waves of 128 x 64, one block a unit.  Operands go from memory straight to
-// LDS, two k tiles of 128 (64 KB each); a load instruction writes its wave's 64 x
-// 16 bytes in lane order, eight rows of 128 bytes, and the 16-byte piece c of row
-// r lies at c ^ swizzle(r), so 16 rows' pieces fall on distinct banks.  Waves 0-3
-// and 4-7 take turns: one group multiplies from registers while the other reads
-// its operands of the k tile from LDS.
+// Eight waves of 128 x 64, one persistent block a unit.  Operands go from memory
+// straight to LDS, two k tiles of 128 (64 KB each); a load instruction writes its
+// wave's 64 x 16 bytes in lane order, eight rows of 128 bytes, and the 16-byte piece
+// c of row r lies at c ^ swizzle(r), so 16 rows' pieces fall on distinct banks (r & 7
+// instead: half of LDS's time goes into bank conflicts).
+//
+// Waves 0-3 and 4-7 take turns: in one the first group reads its operands of k tile
+// kt from LDS while the second multiplies kt - 1 from registers, in the next they
+// change.  A group's results leave in a turn of their own, in which the other
+// multiplies or reads; the k tiles of a block's items follow each other without a
+// gap.  Loads are issued between the matrix instructions, where they cost no time:
+//   second group, multiplying kt: all of B's kt + 2, whose place both have read
+//   first group, multiplying kt:  the second's half of A's kt + 1, then its own of kt + 2
+// and have at least a turn to land.  Loads and stores of a wave are counted together,
+// in order: N stores under way between them let a wait leave N more.
+// (Loads before the matrix instructions: 8192 x 8192 x 8192 440 us, between them 389.
+// 32768 rows, 32 experts of 4096 x 1024, 268 MB of results: 182 us with all waiting
+// for the stores, 155 with stores that pass the caches by.)
 constexpr int kSide = 256, kHalf = 32 * 1024, kStage = 2 * kHalf;  // bytes of an operand's part, of a k tile
+constexpr int kLargeK = 4;                                         // k tiles it takes at least
+constexpr int kOutPitch = 144, kOutWave = 16 * kOutPitch;          // 16 rows of 64 results on their way out
 typedef __attribute__((address_space(3))) void* lds_ptr;
-__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }  // row & 7: every second access waits for its bank
-
-// One operand's tile of 256 rows as a buffer resource: rows past the end read as
-// zeros.  The offset within the wave's eight rows is the lane's, the rest uniform.
-struct Dma8 {
-  __amdgpu_buffer_rsrc_t rsrc;
-  int ld;
-  __device__ __forceinline__ void init(const uint8_t* b, int64_t ld_, int r0, int limit, int k) {
-    ld = (int)ld_;
-    const int rows = min(kSide, limit - r0);
-    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(b) + (int64_t)r0 * ld_, 0, (rows - 1) * ld + k, 0x00020000);
-  }
-  // even and odd groups of eight rows
-  __device__ __forceinline__ void lane_offsets(uint32_t (&off)[2]) const {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) off[j] = (uint32_t)((lane >> 3) * ld + ((lane & 7) ^ swizzle(8 * j + (lane >> 3))) * 16);
-  }
-  // the q-th eight rows of k tile kt
-  __device__ __forceinline__ void load(uint8_t* part, const uint32_t (&off)[2], int kt, int q) const {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(part + q * 1024), 16, off[q & 1], kt * 128 + 8 * q * ld, 0, 0);
-  }
-};
-__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
 }
 
+// LDS accesses are written out, reads with their wait in the same block: the compiler
+// takes any it sees to depend on the loads to LDS under way and would wait for them.
+__device__ __forceinline__ int lds_int(const int* p) {
+  int v;
+  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(lds_address(p)) : "memory");
+  return v;
+}
+
 // Two row tiles of 32 (4096 bytes apart), both halves of the k tile: at[s][q] is the
-// lane's address of piece q of half s.  The reads are written out, with their wait
-// in the same block: the compiler takes any LDS read it sees to depend on the loads
-// to LDS under way and would wait for all of them.
+// lane's address of piece q of half s.
 template <int OFF>
 __device__ __forceinline__ void read_two(i32x8 (&f)[2][2], const uint32_t (&at)[2][2]) {
   i32x4 x[8];
@@ -420,155 +418,253 @@ __device__ __forceinline__ void read_two(i32x8 (&f)[2][2], const uint32_t (&at)[
   f[1][1] = join8(x[6], x[7]);
 }
 
+// What hangs on it is computed where it is used, not kept in registers over the loop
+// (which has none left).
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// The kernel's arguments, read again where they are used between items: kept in
+// scalar registers over the loop they would push its own out.
+typedef const __attribute__((address_space(4))) Fp8Params* Args;
+__device__ __forceinline__ Args args() {
+  Args a = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(a));
+  return a;
+}
+
+// A tile of C, and its operands as buffers: rows past the end read as zeros.
+struct LItem {
+  int e, row0, rows, n0;  // rows: of the group from row0 on
+  const uint8_t *a, *b;
+  int na, nb;  // bytes
+};
+
 struct Large {
-  Dma8 A, B;
-  uint32_t oa[2], ob[2];  // this lane's offsets in their eight rows
-  uint32_t at[2][2];   // of its pieces of row lane % 32 of a part, in LDS
-  const uint8_t *SA, *SB;
-  uint32_t so[4];      // its rows' scales from SA on
+  const Table& T;
   uint8_t* smem;
-  int kb, wid, wm, wn;
-  // past the last k tile: the last one again, into a place that nobody reads any more
-  __device__ __forceinline__ void load_a(int kt, int q) const { A.load(smem + (kt & 1) * kStage, oa, min(kt, kb - 1), q); }
-  __device__ __forceinline__ void load_b(int kt, int q) const {
-    B.load(smem + (kt & 1) * kStage + kHalf, ob, min(kt, kb - 1), q);
+  int kb, wid, wm, wn, lda, ldb, q;
+  uint32_t oa[2], ob[2];  // this lane's offsets in even and odd groups of eight rows
+  uint32_t at[2][2];      // of its pieces of row lane % 32 of a part, in LDS
+
+  __device__ __forceinline__ Large(const Fp8Params& p, const Table& T_, uint8_t* s) : T(T_), smem(s) {
+    const int lane = threadIdx.x & 63, r = lane & 31;
+    kb = p.k / 128;
+    lda = (int)p.lda;
+    ldb = (int)p.ldb;
+    q = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);  // the grid is a multiple of 8
+    wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    wm = (wid >> 2) * 128;
+    wn = (wid & 3) * 64;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int piece = ((lane & 7) ^ swizzle(8 * j + (lane >> 3))) * 16;
+      oa[j] = (uint32_t)((lane >> 3) * lda + piece);
+      ob[j] = (uint32_t)((lane >> 3) * ldb + piece);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        at[s][j] = lds_address(smem) + r * 128 + ((4 * s + 2 * (lane >> 5) + j) ^ swizzle(r)) * 16;
+  }
+  // The block's next item; false: there is none, and `it` stays.
+  __device__ __forceinline__ bool next(LItem& it) {
+    const Args p = args();
+    const int groups = p->groups, tiles_n = (p->n + kSide - 1) / kSide;
+    if (q >= __builtin_amdgcn_readfirstlane(lds_int(&T.tile[groups]))) return false;
+    // the last group whose first tile is not behind q: of every `step`-th one, then of those after it
+    const int lane = threadIdx.x & 63, step = (groups + 63) >> 6;
+    int e = 0;
+    for (int s = step, base = 0;; s = 1) {
+      const int i = base + lane * s;
+      const int first = lds_int(&T.tile[min(i, groups)]);
+      const uint64_t le = __ballot(i < groups && first <= q);
+      e = base + (63 - __builtin_clzll(le)) * s;
+      if (s == 1) break;
+      base = e;
+    }
+    it.e = __builtin_amdgcn_readfirstlane(e);
+    const int r0 = __builtin_amdgcn_readfirstlane(lds_int(&T.begin[it.e]));
+    const int M = __builtin_amdgcn_readfirstlane(lds_int(&T.begin[it.e + 1])) - r0;
+    int tm, tn;
+    tile_of(q - __builtin_amdgcn_readfirstlane(lds_int(&T.tile[it.e])), (M + kSide - 1) / kSide, tiles_n, tm, tn);
+    it.row0 = __builtin_amdgcn_readfirstlane(r0 + tm * kSide);
+    it.rows = min(kSide, r0 + M - it.row0);
+    it.n0 = __builtin_amdgcn_readfirstlane(tn * kSide);
+    it.a = p->a + (int64_t)it.row0 * p->lda;
+    it.b = p->b + it.e * p->stride_b + (int64_t)it.n0 * p->ldb;
+    it.na = (it.rows - 1) * (int)p->lda + p->k;
+    it.nb = (min(kSide, p->n - it.n0) - 1) * (int)p->ldb + p->k;
+    q += gridDim.x;
+    return true;
+  }
+  // eight rows of k tile kt of `it`, or past its last one of `nx`, to place `g`
+  __device__ __forceinline__ void load_a(const LItem& it, const LItem& nx, int kt, int g, int j) const {
+    const bool over = kt >= kb;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(over ? nx.a : it.a), 0, over ? nx.na : it.na, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(smem + (g & 1) * kStage + j * 1024), 16, oa[j & 1],
+                                             (over ? kt - kb : kt) * 128 + 8 * j * lda, 0, 0);
+  }
+  __device__ __forceinline__ void load_b(const LItem& it, const LItem& nx, int kt, int g, int j) const {
+    const bool over = kt >= kb;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(over ? nx.b : it.b), 0, over ? nx.nb : it.nb, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(smem + (g & 1) * kStage + kHalf + j * 1024), 16, ob[j & 1],
+                                             (over ? kt - kb : kt) * 128 + 8 * j * ldb, 0, 0);
   }
 };
 
-// The k tiles of one item for one of the two groups; the first has landed.  In turn
-// 2 kt the first group reads k tile kt and the second multiplies kt - 1, in turn
-// 2 kt + 1 they change.  Loads are issued between the matrix instructions, where
-// they cost no time: the second group's turn loads B's k tile kt + 1, whose place
-// both have read; the first group's loads its own half of A's k tile kt + 2, and
-// the second's half of kt + 1.  Each has a turn and a half to land, by the end of
-// the turn before it is read.
-template <int GROUP>
-__device__ __forceinline__ void large_loop(f32x16 (&acc)[4][2], const Large& L) {
-  const int w = L.wid & 3;
-  if constexpr (GROUP == 1) {  // one turn behind
+// Scale bytes of four k tiles, of this lane's rows and its columns' tile.
+struct Scales {
+  int a[4], b;
+  // from k tile kt on (at a row's end its last four: skip(kt) bits too early)
+  __device__ __forceinline__ void load(const Large& L, const LItem& it, int kt) {
+    typedef int int_a1 __attribute__((aligned(1)));
+    const Args p = args();
+    const int o = min(kt, L.kb - 4), r = here(threadIdx.x & 31), ldsa = (int)p->ldsa;
+    const uint8_t* s = p->sa + (int64_t)it.row0 * ldsa + o;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) L.load_b(1, 8 * w + j);
-    __builtin_amdgcn_s_barrier();
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) L.load_a(1, 4 * w + j);
+    for (int i = 0; i < 4; ++i)
+      a[i] = *reinterpret_cast<const int_a1*>(s + (uint32_t)(min(L.wm + 32 * i + r, it.rows - 1) * ldsa));
+    b = *reinterpret_cast<const int_a1*>(p->sb + it.e * p->stride_sb + (int64_t)(min(it.n0 + L.wn, p->n - 1) >> 7) * p->ldsb + o);
   }
-  int ca[4], cb;
-#pragma unroll 1
-  for (int kt = 0; kt < L.kb; ++kt) {
-    // the lowest bytes are this k tile's: four bytes of a row at a time, its last four at its end
-    int shift = 8;
-    if ((kt & 3) == 0) {
-      typedef int int_a1 __attribute__((aligned(1)));
-      const int o = min(kt, L.kb - 4);
-      shift = 8 * (kt - o);
+  static __device__ __forceinline__ int skip(const Large& L, int kt) { return 8 * (kt - min(kt, L.kb - 4)); }
+  __device__ __forceinline__ void shift(int bits) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ca[i] = *reinterpret_cast<const int_a1*>(L.SA + L.so[i] + o);
-      cb = *reinterpret_cast<const int_a1*>(L.SB + o);
-    }
-    uint32_t a[2][2], b[2][2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        a[s][q] = L.at[s][q] + ((kt & 1) * kStage + L.wm * 128);
-        b[s][q] = L.at[s][q] + ((kt & 1) * kStage + kHalf + L.wn * 128);
-      }
-    i32x8 fb[2][2], f0[2][2], f1[2][2];
-    read_two<0>(fb, b);
-    read_two<0>(f0, a);
-    read_two<8192>(f1, a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ca[i] = (int)((uint32_t)ca[i] >> shift);
-    cb = (int)((uint32_t)cb >> shift);
-    // B's kt + 1 has landed; the second group's half of A's kt (its own half of kt + 1 may be under way)
-    if constexpr (GROUP == 1) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[s][j], i < 2 ? f0[s][i] : f1[s][i - 2], acc[i][j],
-                                                                     0, 0, 0, cb, 0, ca[i]);
-        const int t = 4 * s + i;  // a load after every two of the first matrix instructions
-        if constexpr (GROUP == 1) L.load_b(kt + 2, 8 * w + t);
-        else if (t < 4) L.load_a(kt + 1, 16 + 4 * w + t);
-        else L.load_a(kt + 2, 4 * w + t - 4);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    __builtin_amdgcn_s_setprio(0);
-    __builtin_amdgcn_sched_barrier(0);
-    // the first group's half of A's kt + 1, which the loads of this turn follow
-    if constexpr (GROUP == 0) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < 4; ++i) a[i] = (int)((uint32_t)a[i] >> bits);
+    b = (int)((uint32_t)b >> bits);
   }
-  if constexpr (GROUP == 0) __builtin_amdgcn_s_barrier();
-  // what was issued past the last k tile has landed before the places are used again
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-}
+  __device__ __forceinline__ void wait() {  // here, not behind what is issued next
+    asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]), "+v"(b));
+  }
+};
 
-__global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
-  __shared__ Table T;
-  const int tiles_n = (p.n + kSide - 1) / kSide;
-  build_table(T, p, kSide, tiles_n, 0);
-  zero_outside<uint16_t>(p, T.begin[0], T.begin[p.groups]);
-  const int lane = threadIdx.x & 63, r = lane & 31;
-  Large L;
-  L.smem = smem;
-  L.kb = p.k / 128;
-  L.wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  L.wm = (L.wid >> 2) * 128;
-  L.wn = (L.wid & 3) * 64;
+// The two turns of k tile kt, the block's g-th.  FIRST: the item's first, before which
+// up to 16 stores were issued after its loads.  cur: its lowest bytes are k tile
+// kt - 1's; next: of the following four, or of the next item.
+template <int GROUP, bool FIRST>
+__device__ __forceinline__ void large_turns(f32x16 (&acc)[4][2], const Large& L, const LItem& it, const LItem& nx, int kt,
+                                            int g, Scales& cur, Scales& next) {
+  const int w = L.wid & 3;
+  if (FIRST || (kt & 3) == 0) {
+    cur = next;
+    cur.shift(Scales::skip(L, kt));
+  } else {
+    cur.shift(8);
+  }
+  uint32_t a[2][2], b[2][2];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      L.at[s][q] = lds_address(smem) + r * 128 + ((4 * s + 2 * (lane >> 5) + q) ^ swizzle(r)) * 16;
-  const int items = T.tile[p.groups];
-  int q0 = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);  // the grid is a multiple of 8
-  struct Item {
-    int e, r0, m0, n0, M;
-  };
-  auto next = [&](Item& it) -> bool {
-    if (q0 >= items) return false;
-    it.e = __builtin_amdgcn_readfirstlane(group_of(T, p.groups, q0));
-    it.r0 = __builtin_amdgcn_readfirstlane(T.begin[it.e]);
-    it.M = __builtin_amdgcn_readfirstlane(T.begin[it.e + 1]) - it.r0;
-    int tm, tn;
-    tile_of(q0 - __builtin_amdgcn_readfirstlane(T.tile[it.e]), (it.M + kSide - 1) / kSide, tiles_n, tm, tn);
-    it.m0 = __builtin_amdgcn_readfirstlane(tm * kSide);
-    it.n0 = __builtin_amdgcn_readfirstlane(tn * kSide);
-    q0 += gridDim.x;
-    return true;
-  };
-  auto start = [&](const Item& it) {
-    L.A.init(p.a + (int64_t)it.r0 * p.lda, p.lda, it.m0, it.M, p.k);
-    L.B.init(p.b + it.e * p.stride_b, p.ldb, it.n0, p.n, p.k);
-    L.A.lane_offsets(L.oa);
-    L.B.lane_offsets(L.ob);
-    L.SA = p.sa + (int64_t)(it.r0 + it.m0) * p.ldsa;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) L.so[i] = (uint32_t)(min(L.wm + 32 * i + r, it.M - 1 - it.m0) * (int)p.ldsa);
-    L.SB = p.sb + it.e * p.stride_sb + (int64_t)(min(it.n0 + L.wn, p.n - 1) >> 7) * p.ldsb;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      L.load_a(0, 4 * L.wid + j);
-      L.load_b(0, 4 * L.wid + j);
+    for (int j = 0; j < 2; ++j) {
+      a[s][j] = L.at[s][j] + ((g & 1) * kStage + L.wm * 128);
+      b[s][j] = L.at[s][j] + ((g & 1) * kStage + kHalf + L.wn * 128);
     }
-  };
-  Item it;
-  if (!next(it)) return;
-  start(it);
+  i32x8 fb[2][2], f0[2][2], f1[2][2];
+  read_two<0>(fb, b);
+  read_two<0>(f0, a);
+  read_two<8192>(f1, a);
+  // B's kt + 1 has landed; the second group's half of A's kt (the first's of kt + 1 may be under way)
+  if constexpr (GROUP == 1 && FIRST) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+  else if constexpr (GROUP == 1) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  else if constexpr (FIRST) asm volatile("s_waitcnt vmcnt(20)" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  if (kt + 1 == L.kb) next.load(L, nx, 0);
+  else if ((kt & 3) == 3) next.load(L, it, kt + 1);
+  __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[s][j], i < 2 ? f0[s][i] : f1[s][i - 2], acc[i][j],
+                                                                   0, 0, 0, cur.b, 0, cur.a[i]);
+      const int t = 4 * s + i;
+      if constexpr (GROUP == 1) L.load_b(it, nx, kt + 2, g, 8 * w + t);
+      else if (t < 4) L.load_a(it, nx, kt + 1, g + 1, 16 + 4 * w + t);
+      else L.load_a(it, nx, kt + 2, g, 4 * w + t - 4);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  __builtin_amdgcn_s_setprio(0);
+  __builtin_amdgcn_sched_barrier(0);
+  // the first group's half of A's kt + 1, which the loads of this turn follow
+  if constexpr (GROUP == 0 && FIRST) asm volatile("s_waitcnt vmcnt(24)" ::: "memory");
+  else if constexpr (GROUP == 0) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// A wave's 128 x 64 results, 16 rows at a time through its place in LDS: 16 stores of
+// whole 128-byte lines where C is aligned and the tile's columns are whole.  They pass
+// the caches by: a launch has 32 MB of them at least, the L2s' size.
+__device__ __forceinline__ void large_store(f32x16 (&acc)[4][2], const Large& L, const LItem& it, uint8_t* stage) {
+  const Args p = args();
+  const int lane = here(threadIdx.x & 63), ldc = (int)p->ldc;
+  uint16_t* c = reinterpret_cast<uint16_t*>(p->c) + (int64_t)it.row0 * p->ldc + it.n0;
+  const bool whole = it.n0 + kSide <= p->n && p->ldc % 8 == 0 && p->ldc <= (1 << 21) && ((uintptr_t)p->c & 15) == 0;
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(c, 0, whole ? ((it.rows - 1) * ldc + kSide) * 2 : 0, 0x00020000);
+  const uint32_t w = lds_address(stage) + (lane & 15) * kOutPitch + 8 * (lane >> 5);
+  const uint32_t rd = lds_address(stage) + (lane >> 3) * kOutPitch + (lane & 7) * 16;
+  const int row0 = L.wm + (lane >> 3), col = L.wn + (lane & 7) * 8, left = p->n - it.n0 - col;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if ((lane >> 4 & 1) == h) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const u32x2_t x = {pack_bf16(acc[i][j][4 * v], acc[i][j][4 * v + 1]), pack_bf16(acc[i][j][4 * v + 2], acc[i][j][4 * v + 3])};
+            asm volatile("ds_write_b64 %0, %1 offset:%c2" ::"v"(w), "v"(x), "n"(64 * j + 16 * v) : "memory");
+          }
+      }
+      u32x4_t x[2];  // a wave's accesses to LDS keep their order
+      asm volatile(
+          "ds_read_b128 %0, %2\n\t"
+          "ds_read_b128 %1, %2 offset:%c3\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1])
+          : "v"(rd), "n"(8 * kOutPitch)
+          : "memory");
+      if (whole) {  // rows past the group's end are past the buffer's
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          __builtin_amdgcn_raw_buffer_store_b128(x[k], rsrc, (row0 * ldc + col) * 2, (32 * i + 16 * h + 8 * k) * ldc * 2, 2);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int row = row0 + 32 * i + 16 * h + 8 * k;
+          uint16_t* d = c + (int64_t)row * p->ldc + col;
+          if (row < it.rows && left >= 8) *reinterpret_cast<u32x4_a2*>(d) = x[k];
+          if (row < it.rows && left < 8)
+#pragma unroll 1
+            for (int t = 0; t < left; ++t) {
+              uint32_t u;
+              asm volatile("ds_read_u16 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(u) : "v"(rd + 8 * k * kOutPitch + 2 * t) : "memory");
+              d[t] = (uint16_t)u;
+            }
+        }
+      }
+    }
+  if (!whole) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // of another number
+}
+
+template <int GROUP>
+__device__ __forceinline__ void large_group(Large& L, LItem it, uint8_t* stage) {
+  LItem nx = it;
+  bool more = L.next(nx);
+  int g = 0;
+  Scales cur, next;
+  next.load(L, it, 0);
+  next.wait();
+  if constexpr (GROUP == 1) __builtin_amdgcn_s_barrier();  // one turn behind
   for (;;) {
     f32x16 acc[4][2];
 #pragma unroll
@@ -577,22 +673,43 @@ __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    // k tile 0 has landed for this wave, then for every wave
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    large_turns<GROUP, true>(acc, L, it, nx, 0, g, cur, next);
+#pragma unroll 1
+    for (int kt = 1; kt < L.kb; ++kt) large_turns<GROUP, false>(acc, L, it, nx, kt, g + kt, cur, next);
+    g += L.kb;
+    next.wait();
+    large_store(acc, L, it, stage);
     __builtin_amdgcn_s_barrier();
-    if (L.wid >> 2) large_loop<1>(acc, L);
-    else large_loop<0>(acc, L);
-    const Item done = it;
-    const bool more = next(it);
-    if (more) start(it);  // the first k tile's place; the results leave through the second's
-    uint16_t* c = reinterpret_cast<uint16_t*>(p.c) + (int64_t)done.r0 * p.ldc;
-    uint16_t* stage = reinterpret_cast<uint16_t*>(smem + kStage + L.wid * 32 * (64 + 8) * 2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      store_rows<64, uint16_t>(acc[i], stage, c, p.ldc, done.m0 + L.wm + 32 * i, done.M, done.n0 + L.wn, p.n);
-    if (!more) return;
-    __syncthreads();  // the second k tile's place is free
+    if (!more) break;
+    it = nx;
+    more = L.next(nx);
   }
+  if constexpr (GROUP == 0) __builtin_amdgcn_s_barrier();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads past the last item
+}
+
+__global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t out[8 * kOutWave];
+  __shared__ Table T;
+  build_table(T, p, kSide, (p.n + kSide - 1) / kSide, 0);
+  zero_outside<uint16_t>(p, T.begin[0], T.begin[p.groups]);
+  Large L(p, T, smem);
+  LItem it = {};
+  if (!L.next(it)) return;
+  // the first k tile, and of the second what the turns before it do not load
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    L.load_a(it, it, 0, 0, 4 * L.wid + j);
+    L.load_b(it, it, 0, 0, 4 * L.wid + j);
+    L.load_b(it, it, 1, 1, 4 * L.wid + j);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) L.load_a(it, it, 1, 1, 2 * L.wid + j);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  if (L.wid >> 2) large_group<1>(L, it, out + L.wid * kOutWave);
+  else large_group<0>(L, it, out + L.wid * kOutWave);
 }
 
 // ------------------------------------------------------------ launchers
@@ -602,7 +719,7 @@ enum { STREAM = 0, SMALL = 1, MIDDLE = 2, LARGE = 3 };
 int choose(int64_t rows, int k, int n, int groups, int out_dtype, int num_cu) {
   const int64_t avg = rows / groups;
   if (avg <= kStreamRows) return STREAM;
-  if (out_dtype == PMX_BF16 && avg >= 256 && n >= 256 && k >= 512 && (rows / 256) * ((n + 255) / 256) >= num_cu) return LARGE;
+  if (out_dtype == PMX_BF16 && avg >= 256 && n >= 256 && k >= 128 * kLargeK && (rows / 256) * ((n + 255) / 256) >= num_cu) return LARGE;
   if ((rows / 128 + groups) * ((n + 127) / 128) >= num_cu) return MIDDLE;
   return SMALL;
 }
