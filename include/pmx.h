@@ -595,7 +595,7 @@ pmx_status pmx_distill_grad(pmx_handle handle, const pmx_distill_problem* proble
  */
 #define PMX_MAX_NORM_COLS 16384
 #define PMX_MAX_ROUTE_TOP 16
-#define PMX_MAX_ROUTE_ROWS 268435456 /* 2^28 */
+#define PMX_MAX_ROUTE_ROWS 33554432 /* 2^25 */
 
 /*
  * Layer norm of the rows of X (rows x cols, cols <= PMX_MAX_NORM_COLS):

@@ -2,17 +2,18 @@
 // gates, counts, the order of the pairs by expert, and the balance loss with
 // its gradient.  Formulas and edge cases: include/pmx.h.
 //
-// Design: the tokens are cut into chunks of up to 64, a block each.  A team of 16
-// lanes (up to 128 experts) or a wave holds a token's row in registers, a lane
-// neighbouring experts, so among equal logits the lowest lane with a match and
-// its first match are the lowest index.  A chunk's choice of an expert is one
-// 64-bit mask in LDS: its count is the mask's bits, a pair's rank the bits below
-// its token, whatever order they were set in.  So the pairs are sorted by
-// (expert, token) without a sort:
+// Design: a block takes a chunk of tokens, 1024 threads. A team of 16 lanes (up to 128
+// experts) or a wave holds a token's row in registers, a lane neighbouring experts,
+// so among equal logits the lowest lane with a match and its first match are the
+// lowest index.  A chunk's choice of an expert is one 64-bit mask in LDS: its count is
+// the mask's bits, a pair's rank the bits below its token, whatever order they were
+// set in.  So the pairs are sorted by (expert, token) without a sort:
 //   1. rows:    ids, gates, masks -> counts a chunk; sums of p and lse^2 a chunk
-//   2. scan:    each expert's counts over the chunks, its total, its mean of p
-//   3. scatter: offsets from the totals, each pair's row from its rank, the loss
-// One chunk does everything in one launch.  Every sum has a fixed order.
+//   2. scatter: each block adds up the counts of the chunks before its own and of all
+//               (a byte each), so offsets and each pair's row; the first blocks sum p
+//               over the chunks, the last of them to finish writes the loss
+// With many chunks a launch between the two adds the counts up instead.  One chunk
+// does everything in one launch.  Every sum has a fixed order.
 //
 // Bound: launches and latency; the logits are read once forward and once in the
 // gradient (32768 x 64 fp32: 8 MB each).
@@ -23,7 +24,7 @@
 namespace pmx {
 namespace {
 
-constexpr int kMaxE = PMX_MAX_GROUPS;
+constexpr int kMaxE = PMX_MAX_GROUPS, kMaxTop = PMX_MAX_ROUTE_TOP;
 constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147180559945309f;
 
 // exp(x) for x <= 0: the product's rounding error goes back in as a factor.
@@ -34,26 +35,43 @@ __device__ __forceinline__ float exp_acc(float x) {
   return y > -200.f ? fmaf(e, r * kLn2, e) : 0.f;  // x = -inf: r is NaN
 }
 
-// Up to 64 tokens a chunk; shorter ones until there is one for every unit.
-int chunk_of(int64_t rows) { return rows <= 64 || rows >= 16384 ? 64 : 16; }
-int64_t chunks_of(int64_t rows) { return rows ? (rows + chunk_of(rows) - 1) / chunk_of(rows) : 1; }
+constexpr int kThreads = 1024, kOne = 64;  // tokens one launch takes
+constexpr int kScatter = 512;               // threads of the second launch: four blocks a unit
+int lanes_of(int experts) { return experts <= 128 ? 16 : 64; }
+int chunk_of(int experts) { return kThreads / lanes_of(experts); }
+int64_t chunks_of(int64_t rows, int experts) { return (rows + chunk_of(experts) - 1) / chunk_of(experts); }
+// Every block reads all counts while that is at most 32 MB in all (a launch less:
+// 32768 tokens, 64 experts, MEAS).
+bool counts_in_scatter(int64_t chunks, int experts) { return chunks * chunks * ((experts + 3) / 4 * 4) <= (32 << 20); }
 
 struct RouteWs {
-  int32_t* count;  // [chunks][experts]; after the scan: pairs of earlier chunks
-  float* share;    // [chunks][experts] sums of p
-  float* zsum;     // [chunks] sums of lse^2
-  int32_t* live;   // [chunks]
-  float* mean;     // [experts] sums of p over all chunks
-  float* total;    // [1] sum of lse^2
+  uint8_t* count;   // [chunks][experts, up to a multiple of 4]
+  float* share;     // [chunks][experts] sums of p
+  float* zsum;      // [chunks] sums of lse^2
+  int32_t* live;    // [chunks]
+  double* part;     // [experts / 16] of the loss
+  int32_t* done;    // blocks that have written theirs
+  int32_t* before;  // [chunks][experts] pairs of earlier chunks, from the launch between
+  size_t bytes;
 };
-__host__ __device__ __forceinline__ RouteWs route_ws(void* base, int64_t chunks, int experts) {
+__host__ __device__ __forceinline__ RouteWs route_ws(void* base, int64_t chunks, int experts, bool between) {
   RouteWs w;
-  w.count = reinterpret_cast<int32_t*>(base);
-  w.share = reinterpret_cast<float*>(w.count + chunks * experts);
-  w.zsum = w.share + chunks * experts;
-  w.live = reinterpret_cast<int32_t*>(w.zsum + chunks);
-  w.mean = reinterpret_cast<float*>(w.live + chunks);
-  w.total = w.mean + experts;
+  char* p = reinterpret_cast<char*>(base);
+  w.part = reinterpret_cast<double*>(p);
+  p += (experts + 15) / 16 * 8;
+  w.done = reinterpret_cast<int32_t*>(p);
+  p += 8;
+  w.share = reinterpret_cast<float*>(p);
+  p += chunks * experts * 4;
+  w.zsum = reinterpret_cast<float*>(p);
+  p += chunks * 4;
+  w.live = reinterpret_cast<int32_t*>(p);
+  p += chunks * 4;
+  w.before = reinterpret_cast<int32_t*>(p);
+  if (between) p += chunks * experts * 4;
+  w.count = reinterpret_cast<uint8_t*>(p);
+  p += chunks * ((experts + 3) / 4 * 4);
+  w.bytes = (size_t)(p - reinterpret_cast<char*>(base));
   return w;
 }
 
@@ -61,7 +79,7 @@ __host__ __device__ __forceinline__ RouteWs route_ws(void* base, int64_t chunks,
 template <typename E_, int T_, int V_>
 struct RCfg {
   typedef E_ E;
-  static constexpr int T = T_, V = V_, TEAMS = 256 / T_;
+  static constexpr int T = T_, V = V_, TEAMS = kThreads / T_;
 };
 
 template <int T>
@@ -96,6 +114,30 @@ __device__ __forceinline__ void load_logits(float (&z)[C::V], const RouteParams&
         else z[j] = r[e0 + j];
       }
     }
+  }
+}
+
+template <class C>
+__device__ __forceinline__ void store_logits(void* dz, int64_t ld, int64_t row, int experts, int lane, const float (&z)[C::V]) {
+  typedef typename C::E E;
+  E* r = reinterpret_cast<E*>(dz) + row * ld;
+  const int e0 = lane * C::V;
+  typedef uint32_t vec __attribute__((ext_vector_type(C::V * (int)sizeof(E) / 4), aligned(sizeof(E))));
+  vec v;
+#pragma unroll
+  for (int j = 0; j < C::V * (int)sizeof(E) / 4; ++j) {
+    if constexpr (sizeof(E) == 2) v[j] = pack_bf16(z[2 * j], z[2 * j + 1]);
+    else v[j] = __float_as_uint(z[j]);
+  }
+  if (e0 + C::V <= experts) {
+    *reinterpret_cast<vec*>(r + e0) = v;
+  } else {
+#pragma unroll
+    for (int j = 0; j < C::V; ++j)
+      if (e0 + j < experts) {
+        if constexpr (sizeof(E) == 2) r[e0 + j] = (E)(v[j >> 1] >> (16 * (j & 1)));
+        else r[e0 + j] = z[j];
+      }
   }
 }
 
@@ -136,12 +178,15 @@ __device__ __forceinline__ RowStat softmax_row(float (&e)[C::V], const float (&z
 struct Masks {
   uint64_t bits[kMaxE];
 };
+struct Chosen {
+  int16_t id[kThreads / 16][kMaxTop];
+};
 
 // Rows of one chunk: ids and gates to memory, the chosen to the masks, sums of p
 // to registers.
 template <class C>
-__device__ __forceinline__ void route_rows(const RouteParams& p, int64_t first, int count, Masks& M, float (&share)[C::V],
-                                           float& zsum, int& live_count) {
+__device__ __forceinline__ void route_rows(const RouteParams& p, int64_t first, int count, Masks& M, Chosen& S,
+                                           float (&share)[C::V], float& zsum, int& live_count) {
   const int team = threadIdx.x / C::T, lane = threadIdx.x % C::T, shift = (threadIdx.x & 63) & ~(C::T - 1);
   const int rounds = (count + C::TEAMS - 1) / C::TEAMS;
   for (int i = 0; i < rounds; ++i) {
@@ -162,78 +207,94 @@ __device__ __forceinline__ void route_rows(const RouteParams& p, int64_t first, 
         ++live_count;
       }
     }
-    // the chosen: `mine` keeps the choices of this lane's turn (choice j of lane j)
-    int my_id = -1;
-    float my_gate = 0.f, chosen_sum = 0.f;
+    // lane k keeps choice k: the logit; its index comes from the lane that has it
     const float none = -__builtin_inff();
+    const bool routed = !s.dead && !s.bad;
+    float mine = none, chosen_sum = 0.f;
     for (int k = 0; k < p.top; ++k) {
       float m = z[0];
 #pragma unroll
       for (int j = 1; j < C::V; ++j) m = fmaxf(m, z[j]);
       const float best = team_max<C::T>(m);
       const uint64_t votes = __ballot(m == best);
-      const uint64_t mine = C::T == 64 ? votes : (votes >> shift) & ((1ull << (C::T & 63)) - 1);
-      const bool ok = best != none && !s.dead && !s.bad && mine != 0;
-      const int win = ok ? __ffsll((unsigned long long)mine) - 1 : 0;
-      int v = 0;
-      float ev = 0.f;
-      bool found = false;
-#pragma unroll
-      for (int j = 0; j < C::V; ++j)
-        if (!found && z[j] == best) {
-          found = true;
-          v = j;
-          ev = e[j];
-        }
-      if (ok && lane == win) {
+      const uint64_t match = C::T == 64 ? votes : (votes >> shift) & ((1ull << (C::T & 63)) - 1);
+      const bool ok = routed && best != none;
+      if (ok) chosen_sum += exp_acc(best - s.high);
+      if (ok && lane == __ffsll((unsigned long long)match) - 1) {
+        bool found = false;
 #pragma unroll
         for (int j = 0; j < C::V; ++j)
-          if (j == v) z[j] = none;
+          if (!found && z[j] == best) {
+            found = true;
+            z[j] = none;
+            S.id[team][k] = (int16_t)(lane * C::V + j);
+          }
       }
-      const int id = __shfl(lane * C::V + v, shift + win);
-      const float ge = __shfl(ev, shift + win);
-      if (ok) chosen_sum += ge;
-      if (lane == k) {
-        my_id = ok ? id : -1;
-        my_gate = ok ? ge : 0.f;
-      }
+      if (lane == k && ok) mine = best;
     }
+    // the team's lanes exchange through LDS: nothing moves across this point
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
     if (inside && lane < p.top) {
-      const float gate = my_gate / (p.normalize ? chosen_sum : s.sum);
-      p.ids[row * p.top + lane] = my_id;
-      p.gates[row * p.top + lane] = s.dead ? 0.f : s.bad ? __builtin_nanf("") : my_id < 0 ? 0.f : gate;
-      if (my_id >= 0) atomicOr((unsigned long long*)&M.bits[my_id], 1ull << at);
+      const int id = mine != none ? S.id[team][lane] : -1;
+      p.ids[row * p.top + lane] = id;
+      const float gate = exp_acc(mine - s.high) / (p.normalize ? chosen_sum : s.sum);
+      p.gates[row * p.top + lane] = s.bad ? __builtin_nanf("") : id < 0 ? 0.f : gate;
+      if (id >= 0) atomicOr((unsigned long long*)&M.bits[id], 1ull << at);
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
-// Sums over the teams, in their order, of what each lane holds of its experts:
-// into LDS [experts].
+// Sums over the teams, in their order, of what each lane holds of its experts, and of
+// lse^2 and live tokens: all threads get the latter, sums[e] the former.
 template <class C>
-__device__ __forceinline__ void join_share(float* out, const float (&share)[C::V], int experts) {
-  const int team = threadIdx.x / C::T, lane = threadIdx.x % C::T;
-  for (int t = 0; t < C::TEAMS; ++t) {
-    if (team == t)
+__device__ __forceinline__ void join_teams(float* sums, float (*stage)[kMaxE], const float (&share)[C::V], float& z, int& n,
+                                           float* zs, int* ns, int experts) {
+  const int wid = threadIdx.x >> 6, lane = threadIdx.x % C::T;
+  float v[C::V];
+#pragma unroll
+  for (int j = 0; j < C::V; ++j) {
+    v[j] = share[j];
+    if constexpr (C::T == 16) {  // the wave's four teams
+      v[j] += __shfl_xor(v[j], 16);
+      v[j] += __shfl_xor(v[j], 32);
+    }
+  }
+  if constexpr (C::T == 16) {
+    z += __shfl_xor(z, 16);
+    z += __shfl_xor(z, 32);
+    n += __shfl_xor(n, 16);
+    n += __shfl_xor(n, 32);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    zs[wid] = z;
+    ns[wid] = n;
+  }
+  // sixteen waves through eight rows of LDS
+  for (int half = 0; half < 2; ++half) {
+    if (wid >> 3 == half && (C::T == 64 || (threadIdx.x & 63) < 16))
 #pragma unroll
       for (int j = 0; j < C::V; ++j) {
         const int e = lane * C::V + j;
-        if (e < experts) out[e] = t ? out[e] + share[j] : share[j];
+        if (e < experts) stage[wid & 7][e] = half ? stage[wid & 7][e] + v[j] : v[j];
       }
     __syncthreads();
   }
-}
-__device__ __forceinline__ void join_teams(float& z, int& n, float* zs, int* ns, int teams, int lanes) {
-  if (threadIdx.x % lanes == 0) {
-    zs[threadIdx.x / lanes] = z;
-    ns[threadIdx.x / lanes] = n;
+  for (int e = threadIdx.x; e < experts; e += kThreads) {
+    float t = stage[0][e];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) t += stage[w][e];
+    sums[e] = t;
   }
-  __syncthreads();
   z = 0.f;
   n = 0;
-  for (int t = 0; t < teams; ++t) {
-    z += zs[t];
-    n += ns[t];
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) {
+    z += zs[w];
+    n += ns[w];
   }
+  __syncthreads();
 }
 
 // Exclusive sums of `n` counts by the first wave, the total last.
@@ -255,218 +316,306 @@ __device__ __forceinline__ void scan_offsets(int* off, const int* counts, int n)
   __syncthreads();
 }
 
-// loss = balance E / (top n) sum_e c_e P_e / n + zloss / n sum lse^2, by the first wave.
-__device__ __forceinline__ void write_loss(const RouteParams& p, const int* counts, const float* sums, float zsum, int n) {
-  if (threadIdx.x < 64) {
-    double b = 0.0;
-    for (int e = threadIdx.x; e < p.experts; e += 64) b += (double)counts[e] * (double)sums[e];
-    for (int d = 32; d > 0; d >>= 1) b += __shfl_xor(b, d);
-    if (threadIdx.x == 0) {
-      const double nn = n;
-      *p.loss = n == 0 ? 0.f
-                       : (float)((p.balance != 0.f ? (double)p.balance * p.experts / (p.top * nn * nn) * b : 0.0) +
-                                 (p.zloss != 0.f ? (double)p.zloss / nn * (double)zsum : 0.0));
-    }
-  }
+// loss = balance E / (top n) sum_e c_e P_e / n + zloss / n sum lse^2, from the sum of c_e n P_e
+__device__ __forceinline__ void write_loss(const RouteParams& p, double dot, double zsum, int n) {
+  const double nn = n;
+  *p.loss = n == 0 ? 0.f
+                   : (float)((p.balance != 0.f ? (double)p.balance * p.experts / (p.top * nn * nn) * dot : 0.0) +
+                             (p.zloss != 0.f ? (double)p.zloss / nn * zsum : 0.0));
+}
+__device__ __forceinline__ double wave_sum_double(double v) {
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
 }
 
-// Rows of the pairs of a chunk: base[e] is the row of its first pair of expert e.
-template <typename Base>
-__device__ __forceinline__ void scatter_chunk(const RouteParams& p, int64_t first, int count, const Masks& M, Base&& base) {
-  for (int i = threadIdx.x; i < count * p.top; i += blockDim.x) {
-    const int at = i / p.top;
-    const int64_t pair = first * p.top + i;
-    const int e = p.ids[pair];
-    int slot = -1;
-    if (e >= 0) {
-      slot = base(e) + __popcll(M.bits[e] & ((1ull << at) - 1));
-      p.tokens[slot] = (int32_t)(first + at);
-    }
-    p.slots[pair] = slot;
-  }
-}
-
-// Everything, for up to one chunk of tokens (or none).
+// Everything, for up to kOne tokens (or none).
 template <class C>
-__global__ __launch_bounds__(256) void route_one_kernel(RouteParams p) {
+__global__ __launch_bounds__(kThreads, 4) void route_one_kernel(RouteParams p) {
   __shared__ Masks M;
-  __shared__ float sums[kMaxE];
-  __shared__ int counts[kMaxE], off[kMaxE + 1];
-  __shared__ float zs[C::TEAMS];
-  __shared__ int ns[C::TEAMS];
+  __shared__ Chosen S;
+  __shared__ float sums[kMaxE], stage[8][kMaxE], zs[kThreads / 64];
+  __shared__ int counts[kMaxE], off[kMaxE + 1], ns[kThreads / 64];
   const int count = (int)p.rows;
-  for (int e = threadIdx.x; e < p.experts; e += 256) M.bits[e] = 0;
+  for (int e = threadIdx.x; e < p.experts; e += kThreads) M.bits[e] = 0;
   __syncthreads();
   float share[C::V], z = 0.f;
   int n = 0;
 #pragma unroll
   for (int j = 0; j < C::V; ++j) share[j] = 0.f;
-  if (count) route_rows<C>(p, 0, count, M, share, z, n);
-  join_share<C>(sums, share, p.experts);  // its barriers: the masks are whole, ids written
-  join_teams(z, n, zs, ns, C::TEAMS, C::T);
-  for (int e = threadIdx.x; e < p.experts; e += 256) counts[e] = __popcll(M.bits[e]);
+  if (count) route_rows<C>(p, 0, count, M, S, share, z, n);
+  join_teams<C>(sums, stage, share, z, n, zs, ns, p.experts);  // its barriers: the masks are whole, ids written
+  for (int e = threadIdx.x; e < p.experts; e += kThreads) counts[e] = __popcll(M.bits[e]);
   __syncthreads();
   scan_offsets(off, counts, p.experts);
-  for (int e = threadIdx.x; e <= p.experts; e += 256) {
+  for (int e = threadIdx.x; e <= p.experts; e += kThreads) {
     p.counts[e] = e < p.experts ? counts[e] : n;
     p.offsets[e] = off[e];
   }
-  write_loss(p, counts, sums, z, n);
+  if (threadIdx.x < 64) {
+    double dot = 0.0;
+    for (int e = threadIdx.x; e < p.experts; e += 64) dot += (double)counts[e] * (double)sums[e];
+    dot = wave_sum_double(dot);
+    if (threadIdx.x == 0) write_loss(p, dot, z, n);
+  }
   if (p.slots) {
-    __threadfence_block();
-    scatter_chunk(p, 0, count, M, [&](int e) { return off[e]; });
-    for (int i = off[p.experts] + threadIdx.x; i < count * p.top; i += 256) p.tokens[i] = -1;
+    const int i0 = threadIdx.x;  // 1024 pairs at most
+    if (i0 < count * p.top) {
+      const int e = p.ids[i0];
+      int slot = -1;
+      if (e >= 0) {
+        slot = off[e] + __popcll(M.bits[e] & ((1ull << (i0 / p.top)) - 1));
+        p.tokens[slot] = i0 / p.top;
+      }
+      p.slots[i0] = slot;
+    }
+    for (int i = off[p.experts] + threadIdx.x; i < count * p.top; i += kThreads) p.tokens[i] = -1;
   }
 }
 
 template <class C>
-__global__ __launch_bounds__(256) void route_rows_kernel(RouteParams p, int chunk, int64_t chunks) {
+__global__ __launch_bounds__(kThreads, 4) void route_rows_kernel(RouteParams p, int64_t chunks, bool between) {
   __shared__ Masks M;
-  __shared__ float sums[kMaxE];
-  __shared__ float zs[C::TEAMS];
-  __shared__ int ns[C::TEAMS];
-  const RouteWs w = route_ws(p.ws, chunks, p.experts);
-  const int64_t b = blockIdx.x, first = b * chunk;
-  const int count = (int)min((int64_t)chunk, p.rows - first);
-  for (int e = threadIdx.x; e < p.experts; e += 256) M.bits[e] = 0;
+  __shared__ Chosen S;
+  __shared__ float sums[kMaxE], stage[8][kMaxE], zs[kThreads / 64];
+  __shared__ int ns[kThreads / 64];
+  const RouteWs w = route_ws(p.ws, chunks, p.experts, between);
+  const int64_t b = blockIdx.x, first = b * C::TEAMS;
+  const int count = (int)min((int64_t)C::TEAMS, p.rows - first);
+  for (int e = threadIdx.x; e < p.experts; e += kThreads) M.bits[e] = 0;
   __syncthreads();
   float share[C::V], z = 0.f;
   int n = 0;
 #pragma unroll
   for (int j = 0; j < C::V; ++j) share[j] = 0.f;
-  route_rows<C>(p, first, count, M, share, z, n);
-  join_share<C>(sums, share, p.experts);
-  join_teams(z, n, zs, ns, C::TEAMS, C::T);
-  for (int e = threadIdx.x; e < p.experts; e += 256) {
-    w.count[b * p.experts + e] = __popcll(M.bits[e]);
-    w.share[b * p.experts + e] = sums[e];
-  }
+  route_rows<C>(p, first, count, M, S, share, z, n);
+  join_teams<C>(sums, stage, share, z, n, zs, ns, p.experts);
+  const int wide = (p.experts + 3) / 4 * 4;
+  for (int e = threadIdx.x; e < wide; e += kThreads) w.count[b * wide + e] = e < p.experts ? (uint8_t)__popcll(M.bits[e]) : 0;
+  for (int e = threadIdx.x; e < p.experts; e += kThreads) w.share[b * p.experts + e] = sums[e];
   if (threadIdx.x == 0) {
     w.zsum[b] = z;
     w.live[b] = n;
+    if (b == 0) *w.done = 0;
   }
 }
 
-// 16 experts a block, 64 segments of the chunks each.
+// Between: 16 experts a block, 64 segments of the chunks each.
 __global__ __launch_bounds__(1024) void route_scan_kernel(RouteParams p, int64_t chunks) {
   __shared__ int part[64][17];
-  __shared__ float fpart[64][17];
-  const RouteWs w = route_ws(p.ws, chunks, p.experts);
-  const int in = threadIdx.x & 15, seg = threadIdx.x >> 4, e = blockIdx.x * 16 + in;
+  const RouteWs w = route_ws(p.ws, chunks, p.experts, true);
+  const int in = threadIdx.x & 15, seg = threadIdx.x >> 4, e = blockIdx.x * 16 + in, wide = (p.experts + 3) / 4 * 4;
   const int64_t per = (chunks + 63) / 64, c0 = min(seg * per, chunks), c1 = min(c0 + per, chunks);
   int n = 0;
-  float f = 0.f;
   if (e < p.experts)
-    for (int64_t c = c0; c < c1; ++c) {
-      n += w.count[c * p.experts + e];
-      f += w.share[c * p.experts + e];
-    }
+#pragma unroll 8
+    for (int64_t c = c0; c < c1; ++c) n += w.count[c * wide + e];
   part[seg][in] = n;
-  fpart[seg][in] = f;
   __syncthreads();
   int before = 0;
   for (int s = 0; s < seg; ++s) before += part[s][in];
-  if (e < p.experts) {
+  if (e >= p.experts) return;
+#pragma unroll 8
+  for (int64_t c = c0; c < c1; ++c) {
+    w.before[c * p.experts + e] = before;
+    before += w.count[c * wide + e];
+  }
+  if (seg == 63) p.counts[e] = before;
+}
+
+// The loss from the chunks' sums: 16 experts a block, the chunks in 32 segments; the
+// last block to finish adds the parts up.
+__device__ __forceinline__ void route_loss(const RouteParams& p, const RouteWs& w, int q, int64_t chunks) {
+  __shared__ float seg[32][17];
+  __shared__ int part[32][17];
+  __shared__ double zs[8];
+  __shared__ int ns[8], last;
+  const int parts = (p.experts + 15) / 16, wide = (p.experts + 3) / 4 * 4;
+  const int in = threadIdx.x & 15, s = threadIdx.x >> 4, e = q * 16 + in;
+  const int64_t per = (chunks + 31) / 32, c0 = min(s * per, chunks), c1 = min(c0 + per, chunks);
+  float t = 0.f;
+  int c_e = 0;
+  if (e < p.experts)
+#pragma unroll 8
     for (int64_t c = c0; c < c1; ++c) {
-      const int64_t i = c * p.experts + e;
-      const int v = w.count[i];
-      w.count[i] = before;
-      before += v;
+      t += w.share[c * p.experts + e];
+      c_e += w.count[c * wide + e];
     }
-    if (seg == 63) p.counts[e] = before;
-    if (seg == 0) {
-      float t = 0.f;
-      for (int s = 0; s < 64; ++s) t += fpart[s][in];
-      w.mean[e] = t;
+  seg[s][in] = t;
+  part[s][in] = c_e;
+  __syncthreads();
+  if (threadIdx.x < 64) {  // four quarters of the segments
+    double d = 0.0;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      d += (double)seg[8 * s + i][in];
+      c += part[8 * s + i][in];
+    }
+    d += __shfl_xor(d, 16);
+    d += __shfl_xor(d, 32);
+    c += __shfl_xor(c, 16);
+    c += __shfl_xor(c, 32);
+    d *= (double)c;
+    for (int k = 8; k > 0; k >>= 1) d += __shfl_xor(d, k);
+    if (threadIdx.x == 0) {
+      w.part[q] = d;
+      __threadfence();
+      last = atomicAdd(w.done, 1) == parts - 1;
+      __threadfence();
     }
   }
-  if (blockIdx.x) return;
-  // the chunks' sums of lse^2 and live tokens
   __syncthreads();
-  const int64_t per1 = (chunks + 1023) / 1024, k0 = min((int64_t)threadIdx.x * per1, chunks), k1 = min(k0 + per1, chunks);
-  f = 0.f;
-  n = 0;
-  for (int64_t c = k0; c < k1; ++c) {
-    f += w.zsum[c];
+  if (!last) return;
+  double z = 0.0;
+  int n = 0;
+  for (int64_t c = threadIdx.x; c < chunks; c += kScatter) {
+    z += (double)w.zsum[c];
     n += w.live[c];
   }
-  f = wave_sum(f);
+  z = wave_sum_double(z);
   for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
   if ((threadIdx.x & 63) == 0) {
-    fpart[threadIdx.x >> 6][0] = f;
-    part[threadIdx.x >> 6][0] = n;
+    zs[threadIdx.x >> 6] = z;
+    ns[threadIdx.x >> 6] = n;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    f = 0.f;
-    n = 0;
-    for (int s = 0; s < 16; ++s) {
-      f += fpart[s][0];
-      n += part[s][0];
+  if (threadIdx.x < 64) {
+    double dot = 0.0;
+    if ((int)threadIdx.x < parts) dot = __hip_atomic_load(&w.part[threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    dot = wave_sum_double(dot);
+    if (threadIdx.x == 0) {
+      z = 0.0;
+      n = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        z += zs[i];
+        n += ns[i];
+      }
+      p.counts[p.experts] = n;
+      write_loss(p, dot, z, n);
     }
-    *w.total = f;
-    p.counts[p.experts] = n;
   }
 }
 
-__global__ __launch_bounds__(256) void route_scatter_kernel(RouteParams p, int chunk, int64_t chunks) {
+// Blocks past the chunks: the loss.
+__global__ __launch_bounds__(kScatter) void route_scatter_kernel(RouteParams p, int chunk, int64_t chunks, bool between) {
   __shared__ Masks M;
-  __shared__ int counts[kMaxE], off[kMaxE + 1];
-  const RouteWs w = route_ws(p.ws, chunks, p.experts);
-  const int64_t b = blockIdx.x, first = b * chunk;
+  __shared__ int counts[kMaxE], before[kMaxE], off[kMaxE + 1];
+  const RouteWs w = route_ws(p.ws, chunks, p.experts, between);
+  const int64_t b = blockIdx.x;
+  const int losses = (p.experts + 15) / 16;  // first: theirs is the longer way
+  if (b < losses) {
+    route_loss(p, w, (int)b, chunks);
+    return;
+  }
+  const int64_t at = b - losses, first = at * chunk;
   const int count = (int)min((int64_t)chunk, p.rows - first);
-  for (int e = threadIdx.x; e < p.experts; e += 256) {
+  const int pairs = p.slots ? count * p.top : 0;  // 1024 at most: two a thread
+  int chosen[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = threadIdx.x + k * kScatter;
+    chosen[k] = i < pairs ? p.ids[first * p.top + i] : -1;
+  }
+  for (int e = threadIdx.x; e < p.experts; e += kScatter) {
     M.bits[e] = 0;
-    counts[e] = p.counts[e];
+    counts[e] = between ? p.counts[e] : 0;
+    before[e] = between ? w.before[at * p.experts + e] : 0;
   }
   __syncthreads();
-  if (p.slots)
-    for (int i = threadIdx.x; i < count * p.top; i += 256) {
-      const int e = p.ids[first * p.top + i];
-      if (e >= 0) atomicOr((unsigned long long*)&M.bits[e], 1ull << (i / p.top));
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (chosen[k] >= 0) atomicOr((unsigned long long*)&M.bits[chosen[k]], 1ull << (((int)threadIdx.x + k * kScatter) / p.top));
+  if (!between) {  // four experts a thread, its share of the chunks
+    const int words = (p.experts + 3) / 4, segs = kScatter / words, s = (int)threadIdx.x / words;
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(w.count) + ((int)threadIdx.x - s * words);
+    int all[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
+    if (s < segs) {
+#pragma unroll 8
+      for (int i = s; i < (int)chunks; i += segs) {
+        const uint32_t v = c[(int64_t)i * words];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int x = v >> (8 * j) & 255;
+          all[j] += x;
+          low[j] += i < at ? x : 0;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = 4 * ((int)threadIdx.x - s * words) + j;
+        if (e < p.experts) {  // whole numbers: in any order
+          atomicAdd(&counts[e], all[j]);
+          atomicAdd(&before[e], low[j]);
+        }
+      }
     }
-  scan_offsets(off, counts, p.experts);
-  if (b == 0) {
-    for (int e = threadIdx.x; e <= p.experts; e += 256) p.offsets[e] = off[e];
-    write_loss(p, counts, w.mean, *w.total, p.counts[p.experts]);
   }
+  __syncthreads();
+  scan_offsets(off, counts, p.experts);
+  if (at == 0)
+    for (int e = threadIdx.x; e <= p.experts; e += kScatter) {
+      p.offsets[e] = off[e];
+      if (e < p.experts) p.counts[e] = counts[e];
+    }
   if (!p.slots) return;
-  const int32_t* base = w.count + b * p.experts;
-  scatter_chunk(p, first, count, M, [&](int e) { return off[e] + base[e]; });
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = threadIdx.x + k * kScatter, e = chosen[k], in = i / p.top;
+    if (i >= pairs) continue;
+    int slot = -1;
+    if (e >= 0) {
+      slot = off[e] + before[e] + __popcll(M.bits[e] & ((1ull << in) - 1));
+      p.tokens[slot] = (int32_t)(first + in);
+    }
+    p.slots[first * p.top + i] = slot;
+  }
   // rows behind the last pair
   const int64_t all = p.rows * p.top;
-  for (int64_t i = off[p.experts] + b * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) p.tokens[i] = -1;
+  for (int64_t i = off[p.experts] + at * kScatter + threadIdx.x; i < all; i += chunks * kScatter) p.tokens[i] = -1;
 }
 
 // dz = p (a - sum p a) + u zloss 2 lse / n p + the gates' part.
 template <class C>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
-  typedef typename C::E E;
+  constexpr int TEAMS = 256 / C::T;
   const int team = threadIdx.x / C::T, lane = threadIdx.x % C::T, shift = (threadIdx.x & 63) & ~(C::T - 1);
+  const int64_t step = (int64_t)gridDim.x * TEAMS;
+  int64_t base = (int64_t)blockIdx.x * TEAMS;
+  // a row's data, loaded ahead of what the row before it computes
+  float nz[C::V], ng = 0.f, nd = 0.f;
+  int nid = -1;
+  bool nlive = false;
+  auto fetch = [&](int64_t b) {
+    const int64_t row = min(b + team, p.rows - 1);
+    load_logits<C>(nz, p, row, lane);
+    if (p.dgates && lane < p.top) {
+      nid = p.ids[row * p.top + lane];
+      ng = p.gates[row * p.top + lane];
+      nd = p.dgates[row * p.top + lane];
+    }
+    nlive = !p.live || p.live[row] != 0;
+  };
+  fetch(base);
   const float n = (float)p.counts[p.experts], u = p.upstream ? *p.upstream : 1.f;
+  int c[C::V];
+#pragma unroll
+  for (int j = 0; j < C::V; ++j) c[j] = p.counts[min(lane * C::V + j, p.experts)];
   const float cb = n > 0.f ? u * p.balance * (float)p.experts / ((float)p.top * n) / n : 0.f;
   const float cz = n > 0.f ? u * p.zloss * 2.f / n : 0.f;
   float a[C::V];
 #pragma unroll
-  for (int j = 0; j < C::V; ++j) {
-    const int e = lane * C::V + j;
-    a[j] = e < p.experts ? cb * (float)p.counts[e] : 0.f;
-  }
-  const int64_t step = (int64_t)gridDim.x * C::TEAMS;
-  for (int64_t base = (int64_t)blockIdx.x * C::TEAMS; base < p.rows; base += step) {
-    const bool inside = base + team < p.rows;
-    const int64_t row = inside ? base + team : p.rows - 1;
+  for (int j = 0; j < C::V; ++j) a[j] = lane * C::V + j < p.experts ? cb * (float)c[j] : 0.f;
+  for (; base < p.rows; base += step) {
+    const bool inside = base + team < p.rows, live = nlive && inside;
+    const int64_t row = base + team;
     float z[C::V], e[C::V];
-    load_logits<C>(z, p, row, lane);
-    int my_id = -1;
-    float my_g = 0.f, my_d = 0.f;
-    if (p.dgates && lane < p.top) {
-      my_id = p.ids[row * p.top + lane];
-      my_g = p.gates[row * p.top + lane];
-      my_d = p.dgates[row * p.top + lane];
-      if (my_id < 0) my_g = my_d = 0.f;
-    }
-    const RowStat s = softmax_row<C>(e, z, inside && (!p.live || p.live[row] != 0));
+#pragma unroll
+    for (int j = 0; j < C::V; ++j) z[j] = nz[j];
+    const int my_id = nid;
+    const float my_g = nid < 0 ? 0.f : ng, my_d = nid < 0 ? 0.f : nd;
+    if (base + step < p.rows) fetch(base + step);
+    const RowStat s = softmax_row<C>(e, z, live);
     const float inv = 1.f / s.sum;
     float dot = 0.f;
 #pragma unroll
@@ -492,18 +641,9 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
           if (lane * C::V + j == id) z[j] += d;
       }
     }
-    if (inside) {
-      E* dz = reinterpret_cast<E*>(p.dz) + row * p.lddz;
 #pragma unroll
-      for (int j = 0; j < C::V; ++j) {
-        const int i = lane * C::V + j;
-        const float v = s.dead ? 0.f : s.bad ? __builtin_nanf("") : z[j];
-        if (i < p.experts) {
-          if constexpr (sizeof(E) == 2) dz[i] = (E)pack_bf16(v, 0.f);
-          else dz[i] = v;
-        }
-      }
-    }
+    for (int j = 0; j < C::V; ++j) z[j] = s.dead ? 0.f : s.bad ? __builtin_nanf("") : z[j];
+    if (inside) store_logits<C>(p.dz, p.lddz, row, p.experts, lane, z);
   }
 }
 
@@ -523,31 +663,34 @@ hipError_t with_cfg(const RouteParams& p, F&& f) {
 }  // namespace
 
 size_t route_workspace(int64_t rows, int experts) {
-  if (rows <= 64) return 0;
-  const int64_t c = chunks_of(rows);
-  return (size_t)(2 * c * experts + 2 * c + experts + 1) * 4;
+  if (rows <= kOne) return 0;
+  const int64_t c = chunks_of(rows, experts);
+  return route_ws(nullptr, c, experts, !counts_in_scatter(c, experts)).bytes;
 }
 
 hipError_t launch_route(const RouteParams& p, hipStream_t s) {
-  const hipError_t e = with_cfg(p, [&](auto c) {
+  const int64_t chunks = chunks_of(p.rows, p.experts);
+  const bool between = !counts_in_scatter(chunks, p.experts);
+  hipError_t e = with_cfg(p, [&](auto c) {
     typedef decltype(c) C;
-    if (p.rows <= 64) route_one_kernel<C><<<1, 256, 0, s>>>(p);
-    else route_rows_kernel<C><<<dim3((unsigned)chunks_of(p.rows)), 256, 0, s>>>(p, chunk_of(p.rows), chunks_of(p.rows));
+    if (p.rows <= kOne) route_one_kernel<C><<<1, kThreads, 0, s>>>(p);
+    else route_rows_kernel<C><<<dim3((unsigned)chunks), kThreads, 0, s>>>(p, chunks, between);
     return hipGetLastError();
   });
-  if (e != hipSuccess || p.rows <= 64) return e;
-  const int64_t chunks = chunks_of(p.rows);
-  route_scan_kernel<<<dim3((p.experts + 15) / 16), 1024, 0, s>>>(p, chunks);
-  const hipError_t e1 = hipGetLastError();
-  if (e1 != hipSuccess) return e1;
-  route_scatter_kernel<<<dim3((unsigned)chunks), 256, 0, s>>>(p, chunk_of(p.rows), chunks);
+  if (e != hipSuccess || p.rows <= kOne) return e;
+  if (between) {
+    route_scan_kernel<<<dim3((p.experts + 15) / 16), 1024, 0, s>>>(p, chunks);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  route_scatter_kernel<<<dim3((unsigned)(chunks + (p.experts + 15) / 16)), kScatter, 0, s>>>(p, chunk_of(p.experts), chunks, between);
   return hipGetLastError();
 }
 
 hipError_t launch_route_grad(const RouteParams& p, hipStream_t s) {
   return with_cfg(p, [&](auto c) {
     typedef decltype(c) C;
-    const int64_t blocks = std::min<int64_t>((p.rows + C::TEAMS - 1) / C::TEAMS, (int64_t)p.num_cu * 8);
+    const int64_t blocks = std::min<int64_t>((p.rows + 256 / C::T - 1) / (256 / C::T), (int64_t)p.num_cu * 8);
     route_grad_kernel<C><<<dim3((unsigned)blocks), 256, 0, s>>>(p);
     return hipGetLastError();
   });

@@ -22,7 +22,7 @@ RUNNING, CONVERGED, MAXITER, STAGNATED, NONFINITE, DIVERGED = -1, 0, 1, 2, 3, 4
 F32, BF16 = 0, 1
 I32, I64 = 0, 1
 MAX_GROUPS, MAX_TOP, MAX_VOCAB, MAX_TOKENS = 1000, 1023, (1 << 22) - 1, 1 << 30
-MAX_NORM_COLS, MAX_ROUTE_TOP, MAX_ROUTE_ROWS = 16384, 16, 1 << 28
+MAX_NORM_COLS, MAX_ROUTE_TOP, MAX_ROUTE_ROWS = 16384, 16, 1 << 25
 OP_STATS, OP_INV_ROOT, OP_POLAR, OP_APPLY, OP_POLAR_VARBATCH = range(5)
 VARBATCH_MAX_DIM = 64
 VARBATCH_MAX_SIDE = 8192
