@@ -55,156 +55,164 @@ __device__ __forceinline__ void zero_outside(const Fp8Params& p, int lo, int hi)
 }
 
 // ------------------------------------------------------------ few rows a group
-// A block has 64 columns of a group and RT x 16 of its rows at a time; its four
-// waves take k tiles of 128 in turn and add their results in LDS.  A lane loads
-// 32 bytes of a row of B: 16 rows of whole 128-byte lines an instruction pair.
-template <typename O, int RT>
-__global__ __launch_bounds__(256) void fp8_stream_kernel(Fp8Params p, int slabs) {
-  __shared__ float sum[4][16 * RT][68];
+// Weights go from memory to the matrix cores without LDS: a wave has 16 columns of a
+// group and 16 of its rows at a time, a lane loads 32 bytes of a row of B, 16 rows of
+// whole 128-byte lines an instruction pair, four k tiles on their way.  S = 1: every
+// wave its own columns; S = 4: a block's waves share the contraction and add their
+// results in LDS.
+template <typename O, int S>
+__global__ __launch_bounds__(256, S == 1 ? 4 : 3) void fp8_stream_kernel(Fp8Params p, int blocks) {
+  __shared__ float sum[S == 1 ? 1 : 4][16][17];
   const int wid = threadIdx.x >> 6, lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const int e = blockIdx.x / slabs, n0 = (blockIdx.x - e * slabs) * 64, kb = p.k / 128;
-  // this group's rows: offsets clamped, and none below an earlier one
-  int first = 0, last = (int)p.rows, lo = 0, hi = (int)p.rows;
+  const int slot = blockIdx.x / blocks, kb = p.k / 128;
+  const int n0 = ((blockIdx.x - slot * blocks) * (S == 1 ? 4 : 1) + (S == 1 ? wid : 0)) * 16;
+  // the slot-th group that has rows: offsets clamped, and none below an earlier one
+  int e = slot, first = 0, last = (int)p.rows, lo = 0, hi = (int)p.rows;
   if (p.offsets) {
-    int a = 0, b = 0;
-    auto offset = [&](int i) {
-      const int64_t o = load_index(p.offsets, i, p.off64);
-      return (int)(o < 0 ? 0 : o > p.rows ? p.rows : o);
-    };
-    const int begin = offset(0);
-    for (int i = lane; i <= p.groups; i += 64) {
-      const int o = offset(i);
-      if (i <= e) a = max(a, o);
-      if (i <= e + 1) b = max(b, o);
-      hi = i == lane ? o : max(hi, o);
+    e = -1;
+    hi = 0;
+    int seen = 0;
+    for (int base = 0; base < p.groups; base += 64) {
+      const int i = base + lane;
+      auto offset = [&](int j) {
+        const int64_t o = load_index(p.offsets, min(j, p.groups), p.off64);
+        return (int)(o < 0 ? 0 : o > p.rows ? p.rows : o);
+      };
+      int begin = offset(i);
+      const int after = offset(i + 1);
+      if (base == 0) lo = __builtin_amdgcn_readfirstlane(begin);
+      for (int d = 1; d < 64; d <<= 1) {
+        const int x = __shfl_up(begin, d);
+        if (lane >= d) begin = max(begin, x);
+      }
+      begin = max(begin, hi);
+      const int end = max(begin, after);
+      const uint64_t live = __ballot(i < p.groups && end > begin);
+      const uint64_t mine = __ballot((live >> lane & 1) && seen + __popcll(live & ((1ull << lane) - 1)) == slot);
+      if (mine) {
+        const int l = __builtin_ctzll(mine);
+        e = base + l;
+        first = __builtin_amdgcn_readlane(begin, l);
+        last = __builtin_amdgcn_readlane(end, l);
+      }
+      seen += __popcll(live);
+      hi = wave_max(end);
     }
-    if (lane > p.groups) hi = 0;
-    for (int d = 32; d > 0; d >>= 1) {
-      a = max(a, __shfl_xor(a, d));
-      b = max(b, __shfl_xor(b, d));
-      hi = max(hi, __shfl_xor(hi, d));
-    }
-    first = a;
-    last = b;
-    lo = begin;
   }
   zero_outside<O>(p, lo, hi);
-  const uint8_t* B[4];
-  const uint8_t* SB = p.sb + e * p.stride_sb + (int64_t)min(n0 >> 7, (p.n - 1) >> 7) * p.ldsb;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) B[c] = p.b + e * p.stride_b + (int64_t)min(n0 + 16 * c + l16, p.n - 1) * p.ldb + 32 * g;
-  for (int r0 = first; r0 < last; r0 += 16 * RT) {
-    f32x4_t acc[4][RT];
-    bool bad[RT];
-    const uint8_t *A[RT], *SA[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int64_t row = min(r0 + 16 * r + l16, last - 1);
-      A[r] = p.a + row * p.lda + 32 * g;
-      SA[r] = p.sa + row * p.ldsa;
-      bad[r] = false;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (e < 0 || (S == 1 && n0 >= p.n)) return;
+  const int k0 = S == 1 ? 0 : kb * wid / 4, k1 = S == 1 ? kb : kb * (wid + 1) / 4;
+  const uint8_t* B = p.b + e * p.stride_b + (int64_t)min(n0 + l16, p.n - 1) * p.ldb + 32 * g;
+  const uint8_t* SB = p.sb + e * p.stride_sb + (int64_t)(n0 >> 7) * p.ldsb;
+  // four scale bytes from k tile kt on
+  auto scales = [&](const uint8_t* q, int kt) {
+    typedef uint32_t u32_a1 __attribute__((aligned(1)));
+    if (kb >= 4) {
+      const int o = min(kt, kb - 4);
+      return (int)(*reinterpret_cast<const u32_a1*>(q + o) >> (8 * (kt - o)));
     }
-    i32x8 b[4], a[RT];
-    int cb = 0, ca[RT];
-    auto load = [&](int kt) {
-      const int o = kt * 128;
+    int v = 0;
+    for (int j = 0; kt + j < kb; ++j) v |= (int)q[kt + j] << (8 * j);
+    return v;
+  };
+  for (int r0 = first; r0 < last; r0 += 16) {
+    const int64_t row = min(r0 + l16, last - 1);
+    const uint8_t *A = p.a + row * p.lda + 32 * g, *SA = p.sa + row * p.ldsa;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    bool bad = false;
+    i32x4 b[4][2], a[4][2];
+    auto load = [&](int d, int kt) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        b[c] = join8(*reinterpret_cast<const i32x4*>(B[c] + o), *reinterpret_cast<const i32x4*>(B[c] + o + 16));
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        a[r] = join8(*reinterpret_cast<const i32x4*>(A[r] + o), *reinterpret_cast<const i32x4*>(A[r] + o + 16));
-        ca[r] = SA[r][kt];
+      for (int h = 0; h < 2; ++h) {
+        b[d][h] = *reinterpret_cast<const i32x4*>(B + kt * 128 + 16 * h);
+        a[d][h] = *reinterpret_cast<const i32x4*>(A + kt * 128 + 16 * h);
       }
-      cb = SB[kt];
     };
-    if (wid < kb) load(wid);
-    for (int kt = wid; kt < kb; kt += 4) {
-      i32x8 xb[4], xa[RT];
-      int sa[RT];
-      const int sb = cb;
+    int sa = 0, sb = 0;
+    if (k0 < k1) {
+      sa = scales(SA, k0);
+      sb = scales(SB, k0);
+    }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) xb[c] = b[c];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        xa[r] = a[r];
-        sa[r] = ca[r];
-      }
-      if (kt + 4 < kb) load(kt + 4);
+    for (int d = 0; d < 4; ++d)
+      if (k0 + d < k1) load(d, k0 + d);
+    auto step = [&](int kt, auto which) {
+      constexpr int D = decltype(which)::value;
+      if (kt >= k1) return;
+      const i32x8 xa = join8(a[D][0], a[D][1]), xb = join8(b[D][0], b[D][1]);
       if constexpr (sizeof(O) == 2) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            acc[c][r] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xb[c], xa[r], acc[c][r], 0, 0, 0, sb, 0, sa[r]);
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xb, xa, acc, 0, 0, D, sb, D, sa);
       } else {
-        bf16x8 wa[RT][4];
+        f32x4_t part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int t = 0; t < 4; ++t)
+          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(xb[2 * t], xb[2 * t + 1]), widen(xa[2 * t], xa[2 * t + 1]), part, 0, 0, 0);
+        const int ea = sa >> (8 * D) & 255, eb = sb >> (8 * D) & 255;
+        bad |= ea == 255 || eb == 255;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) wa[r][t] = widen(xa[r][2 * t], xa[r][2 * t + 1]);
+        for (int v = 0; v < 4; ++v) acc[v] += __builtin_ldexpf(part[v], ea + eb - 254);
+      }
+      if (kt + 4 < k1) load(D, kt + 4);
+    };
+    for (int kt = k0; kt < k1; kt += 4) {
+      int na = 0, nb = 0;
+      if (kt + 4 < k1) {
+        na = scales(SA, kt + 4);
+        nb = scales(SB, kt + 4);
+      }
+      step(kt, std::integral_constant<int, 0>());
+      step(kt + 1, std::integral_constant<int, 1>());
+      step(kt + 2, std::integral_constant<int, 2>());
+      step(kt + 3, std::integral_constant<int, 3>());
+      sa = na;
+      sb = nb;
+    }
+    if (bad)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          f32x4_t part[RT];
+      for (int v = 0; v < 4; ++v) acc[v] = __builtin_nanf("");
+    if constexpr (S == 1) {
+      const int col = n0 + 4 * g;
+      O* c = reinterpret_cast<O*>(p.c) + row * p.ldc + col;
+      if (r0 + l16 < last) {
+        if (col + 4 <= p.n) {
+          typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
+          typedef f32x4_t f32x4_a4 __attribute__((aligned(4)));
+          if constexpr (sizeof(O) == 2) *reinterpret_cast<u32x2_a2*>(c) = u32x2_t{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])};
+          else *reinterpret_cast<f32x4_a4*>(c) = acc;
+        } else {
 #pragma unroll
-          for (int r = 0; r < RT; ++r) part[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const bf16x8 wb = widen(xb[c][2 * t], xb[c][2 * t + 1]);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) part[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, wa[r][t], part[r], 0, 0, 0);
-          }
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[c][r][v] += __builtin_ldexpf(part[r][v], sa[r] + sb - 254);
+          for (int v = 0; v < 3; ++v)
+            if (col + v < p.n) {
+              if constexpr (sizeof(O) == 2) c[v] = (O)pack_bf16(acc[v], 0.f);
+              else c[v] = acc[v];
+            }
         }
-#pragma unroll
-        for (int r = 0; r < RT; ++r) bad[r] |= sa[r] == 255 || sb == 255;
       }
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) sum[wid][l16][4 * g + v] = acc[v];
+      __syncthreads();
+      const int r = threadIdx.x >> 4, col = threadIdx.x & 15;
+      if (r0 + r < last && n0 + col < p.n) {
+        const float t = (sum[0][r][col] + sum[1][r][col]) + (sum[2][r][col] + sum[3][r][col]);
+        O* c = reinterpret_cast<O*>(p.c) + (int64_t)(r0 + r) * p.ldc + n0 + col;
+        if constexpr (sizeof(O) == 2) *c = (O)pack_bf16(t, 0.f);
+        else *c = t;
+      }
+      __syncthreads();
     }
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        f32x4_t v = acc[c][r];
-        if (bad[r])
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = __builtin_nanf("");
-        *reinterpret_cast<f32x4_t*>(&sum[wid][16 * r + l16][16 * c + 4 * g]) = v;
-      }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * RT * 32; i += 256) {
-      const int r = i >> 5, c = (i & 31) * 2, row = r0 + r;
-      if (row >= last || n0 + c >= p.n) continue;
-      float v[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) v[j] = (sum[0][r][c + j] + sum[1][r][c + j]) + (sum[2][r][c + j] + sum[3][r][c + j]);
-      O* out = reinterpret_cast<O*>(p.c) + (int64_t)row * p.ldc + n0 + c;
-      if constexpr (sizeof(O) == 2) {
-        const uint32_t u = pack_bf16(v[0], v[1]);
-        out[0] = (O)u;
-        if (n0 + c + 1 < p.n) out[1] = (O)(u >> 16);
-      } else {
-        out[0] = v[0];
-        if (n0 + c + 1 < p.n) out[1] = v[1];
-      }
-    }
-    __syncthreads();
   }
 }
 
 // ------------------------------------------------------------ tiles through registers and LDS
 // S x S tiles, four waves of S/2 x S/2, k tiles of 128 bytes a row at a pitch of
-// 144 (16 rows' pieces fall on distinct banks), two of them; the next one's loads
-// are under way while one is multiplied.
+// 144 (16 rows' pieces fall on distinct banks), two of them; the next one's loads (64 x
+// 64: the next two's) are under way while one is multiplied.
 constexpr int kPitch = 144;
 
 template <typename O, int S>
 __global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Params p) {
-  constexpr int W = S / 2, F = W / 32, N = S * 8 / 256, STAGE = 2 * S * kPitch;
+  constexpr int W = S / 2, F = W / 32, N = S * 8 / 256, STAGE = 2 * S * kPitch, D = S == 64 ? 2 : 1;
   constexpr int OUT = 32 * (W + 16 / (int)sizeof(O)) * (int)sizeof(O);  // a wave's rows of C on their way out
   static_assert(4 * OUT <= 2 * STAGE, "the waves' rows fit the k tiles' place");
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE];
@@ -233,26 +241,31 @@ __global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Param
       SA[i] = p.sa + (int64_t)(r0 + min(m0 + wm + 32 * i + (lane & 31), M - 1)) * p.ldsa;
       SB[i] = p.sb + e * p.stride_sb + (int64_t)(min(n0 + wn + 32 * i, p.n - 1) >> 7) * p.ldsb;
     }
-    u32x4_t va[N], vb[N];
-    int ca[F], cb[F];
-    auto load = [&](int kt) {
+    u32x4_t va[D][N], vb[D][N];
+    int ca[D][F], cb[D][F], sa[F], sb[F];
+    auto load = [&](int d, int kt) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        va[i] = *reinterpret_cast<const u32x4_t*>(pa[i] + kt * 128);
-        vb[i] = *reinterpret_cast<const u32x4_t*>(pb[i] + kt * 128);
+        va[d][i] = *reinterpret_cast<const u32x4_t*>(pa[i] + kt * 128);
+        vb[d][i] = *reinterpret_cast<const u32x4_t*>(pb[i] + kt * 128);
       }
 #pragma unroll
       for (int i = 0; i < F; ++i) {
-        ca[i] = SA[i][kt];
-        cb[i] = SB[i][kt];
+        ca[d][i] = SA[i][kt];
+        cb[d][i] = SB[i][kt];
       }
     };
-    auto store = [&](uint8_t* st) {
+    auto store = [&](int d, uint8_t* st) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int idx = threadIdx.x + 256 * i, o = (idx >> 3) * kPitch + (idx & 7) * 16;
-        *reinterpret_cast<u32x4_t*>(st + o) = va[i];
-        *reinterpret_cast<u32x4_t*>(st + S * kPitch + o) = vb[i];
+        *reinterpret_cast<u32x4_t*>(st + o) = va[d][i];
+        *reinterpret_cast<u32x4_t*>(st + S * kPitch + o) = vb[d][i];
+      }
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        sa[i] = ca[d][i];
+        sb[i] = cb[d][i];
       }
     };
     f32x16 acc[F][F];
@@ -263,17 +276,21 @@ __global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Param
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     bool bad[F][F] = {};
-    load(0);
-    store(smem);
+    load(0, 0);
+    if (D == 2 && kb > 1) load(D - 1, 1);
+    store(0, smem);
+    if (D == 2 && kb > 2) load(0, 2);
     __syncthreads();
-    for (int kt = 0; kt < kb; ++kt) {
-      int sa[F], sb[F];
+    // k tile kt is in LDS, kt + 1 (and, two deep, kt + 2) under way
+    auto step = [&](int kt, auto parity) {
+      constexpr int P = decltype(parity)::value, NEXT = D == 2 ? 1 - P : 0;
+      int ta[F], tb[F];
 #pragma unroll
       for (int i = 0; i < F; ++i) {
-        sa[i] = ca[i];
-        sb[i] = cb[i];
+        ta[i] = sa[i];
+        tb[i] = sb[i];
       }
-      if (kt + 1 < kb) load(kt + 1);
+      if (D == 1 && kt + 1 < kb) load(0, kt + 1);
       const uint8_t* st = smem + (kt & 1) * STAGE;
       const uint8_t* la = st + (wm + (lane & 31)) * kPitch + 32 * (lane >> 5);
       const uint8_t* lb = st + (S + wn + (lane & 31)) * kPitch + 32 * (lane >> 5);
@@ -294,7 +311,7 @@ __global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Param
           for (int i = 0; i < F; ++i)
 #pragma unroll
             for (int j = 0; j < F; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], acc[i][j], 0, 0, 0, sb[j], 0, sa[i]);
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], acc[i][j], 0, 0, 0, tb[j], 0, ta[i]);
         }
       } else {
         // lane l widens the 8 values from 32 (l / 32) + 8 t on: the same places of k in both operands
@@ -332,14 +349,23 @@ __global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Param
         for (int i = 0; i < F; ++i)
 #pragma unroll
           for (int j = 0; j < F; ++j) {
-            const int ex = sa[i] + sb[j] - 254;
-            bad[i][j] |= sa[i] == 255 || sb[j] == 255;
+            const int ex = ta[i] + tb[j] - 254;
+            bad[i][j] |= ta[i] == 255 || tb[j] == 255;
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] += __builtin_ldexpf(part[i][j][v], ex);
           }
       }
-      if (kt + 1 < kb) store(smem + (~kt & 1) * STAGE);
+      if (kt + 1 < kb) store(NEXT, smem + (~kt & 1) * STAGE);
+      if (D == 2 && kt + 3 < kb) load(NEXT, kt + 3);
       __syncthreads();
+    };
+    if constexpr (D == 2) {
+      for (int kt = 0; kt < kb; kt += 2) {
+        step(kt, std::integral_constant<int, 0>());
+        if (kt + 1 < kb) step(kt + 1, std::integral_constant<int, 1>());
+      }
+    } else {
+      for (int kt = 0; kt < kb; ++kt) step(kt, std::integral_constant<int, 0>());
     }
     if constexpr (sizeof(O) == 4)
 #pragma unroll
@@ -713,7 +739,7 @@ __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
 }
 
 // ------------------------------------------------------------ launchers
-constexpr int kStreamRows = 32;
+constexpr int kStreamRows = 8;
 enum { STREAM = 0, SMALL = 1, MIDDLE = 2, LARGE = 3 };
 
 int choose(int64_t rows, int k, int n, int groups, int out_dtype, int num_cu) {
@@ -728,10 +754,16 @@ template <typename O>
 hipError_t launch(const Fp8Params& p, hipStream_t s) {
   const int cfg = choose(p.rows, p.k, p.n, p.groups, p.out_dtype, p.num_cu);
   if (cfg == STREAM) {
-    const int slabs = (p.n + 63) / 64;
-    const dim3 grid((unsigned)(slabs * p.groups));
-    if (p.rows <= 8 * (int64_t)p.groups) fp8_stream_kernel<O, 1><<<grid, 256, 0, s>>>(p, slabs);
-    else fp8_stream_kernel<O, 2><<<grid, 256, 0, s>>>(p, slabs);
+    // waves of 16 columns, or where they are few four to as many
+    const int slots = (int)std::min<int64_t>(p.groups, p.rows);  // groups that can have rows
+    const int64_t waves = (int64_t)slots * ((p.n + 15) / 16);
+    if (waves >= 8 * (int64_t)p.num_cu) {
+      const int blocks = (p.n + 63) / 64;
+      fp8_stream_kernel<O, 1><<<dim3((unsigned)(blocks * slots)), 256, 0, s>>>(p, blocks);
+    } else {
+      const int blocks = (p.n + 15) / 16;
+      fp8_stream_kernel<O, 4><<<dim3((unsigned)(blocks * slots)), 256, 0, s>>>(p, blocks);
+    }
   } else if (cfg == LARGE) {
     if constexpr (sizeof(O) == 2) fp8_large_kernel<<<dim3((unsigned)(p.num_cu / 8 * 8)), 512, 0, s>>>(p);
   } else {

@@ -29,6 +29,18 @@ __device__ __forceinline__ float row_max(float v) {
   v = fmaxf(v, dpp<kHalfMirror>(v));
   return fmaxf(v, dpp<kMirror>(v));
 }
+template <int CTRL>
+__device__ __forceinline__ int dpp(int i) {
+  return __builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false);
+}
+__device__ __forceinline__ int wave_max(int v) {
+  v = max(v, dpp<kXor1>(v));
+  v = max(v, dpp<kXor2>(v));
+  v = max(v, dpp<kHalfMirror>(v));
+  v = max(v, dpp<kMirror>(v));
+  return max(max(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+             max(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
 __device__ __forceinline__ float lane_value(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }

@@ -35,13 +35,17 @@ __device__ __forceinline__ float exp_acc(float x) {
   return y > -200.f ? fmaf(e, r * kLn2, e) : 0.f;  // x = -inf: r is NaN
 }
 
-constexpr int kThreads = 1024, kOne = 64;  // tokens one launch takes
-constexpr int kScatter = 512;               // threads of the second launch: four blocks a unit
-int lanes_of(int experts) { return experts <= 128 ? 16 : 64; }
-int chunk_of(int experts) { return kThreads / lanes_of(experts); }
+constexpr int kOne = 64;       // tokens one launch takes
+constexpr int kScatter = 512;  // threads of the second launch: four blocks a unit
+// Few lanes a token, many experts a lane: the instructions of a reduction serve as
+// many tokens as a wave has teams, until too few waves are left to hide their latency
+// (32768 fp32 tokens, 64 experts, forward's first launch and the gradient: 16 lanes of 4
+// 11.5 and 8.3 us, 8 of 8 9.8 and 8.1, 4 of 16 9.6 and 9.2).
+int lanes_of(int experts) { return experts <= 32 ? 4 : experts <= 64 ? 8 : experts <= 256 ? 16 : experts <= 512 ? 32 : 64; }
+int chunk_of(int experts) { return lanes_of(experts) <= 16 ? 64 : 1024 / lanes_of(experts); }
 int64_t chunks_of(int64_t rows, int experts) { return (rows + chunk_of(experts) - 1) / chunk_of(experts); }
-// Every block reads all counts while that is at most 32 MB in all (a launch less:
-// 32768 tokens, 64 experts, MEAS).
+// Every block reads all counts while that is at most 32 MB in all: a launch less
+// (32768 tokens, 64 experts: one launch of 6.9 us for two of 7.2 and 4.1).
 bool counts_in_scatter(int64_t chunks, int experts) { return chunks * chunks * ((experts + 3) / 4 * 4) <= (32 << 20); }
 
 struct RouteWs {
@@ -79,16 +83,43 @@ __host__ __device__ __forceinline__ RouteWs route_ws(void* base, int64_t chunks,
 template <typename E_, int T_, int V_>
 struct RCfg {
   typedef E_ E;
-  static constexpr int T = T_, V = V_, TEAMS = kThreads / T_;
+  static constexpr int T = T_, V = V_, MAXE = T_ * V_ < kMaxE ? T_ * V_ : kMaxE;
+  static constexpr int THREADS = T_ <= 16 ? 64 * T_ : 1024, WAVES = THREADS / 64, TEAMS = THREADS / T_;
 };
 
 template <int T>
 __device__ __forceinline__ float team_max(float v) {
-  return T == 16 ? row_max(v) : wave_max(v);
+  v = fmaxf(v, dpp<kXor1>(v));
+  v = fmaxf(v, dpp<kXor2>(v));
+  if constexpr (T >= 8) v = fmaxf(v, dpp<kHalfMirror>(v));
+  if constexpr (T >= 16) v = fmaxf(v, dpp<kMirror>(v));
+  if constexpr (T >= 32) v = fmaxf(v, __shfl_xor(v, 16));
+  if constexpr (T >= 64) v = fmaxf(v, __shfl_xor(v, 32));
+  return v;
 }
 template <int T>
 __device__ __forceinline__ float team_sum(float v) {
-  return T == 16 ? row_sum(v) : wave_sum(v);
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  if constexpr (T >= 8) v += dpp<kHalfMirror>(v);
+  if constexpr (T >= 16) v += dpp<kMirror>(v);
+  if constexpr (T >= 32) v += __shfl_xor(v, 16);
+  if constexpr (T >= 64) v += __shfl_xor(v, 32);
+  return v;
+}
+// Over the wave's teams: what lanes of one place in their teams hold.
+template <int T>
+__device__ __forceinline__ float over_teams(float v) {
+  if constexpr (T <= 4) v += dpp<0x124>(v);  // row_ror:4
+  if constexpr (T <= 8) v += dpp<0x128>(v);  // row_ror:8
+  if constexpr (T <= 16) v += __shfl_xor(v, 16);
+  if constexpr (T <= 32) v += __shfl_xor(v, 32);
+  return v;
+}
+template <int T>
+__device__ __forceinline__ uint64_t team_bits(uint64_t votes) {  // of this lane's team, from bit 0
+  if constexpr (T == 64) return votes;
+  else return (votes >> ((threadIdx.x & 63) & ~(T - 1))) & ((1ull << T) - 1);
 }
 
 // A lane's logits, -inf past the last expert.
@@ -167,10 +198,7 @@ __device__ __forceinline__ RowStat softmax_row(float (&e)[C::V], const float (&z
   bool nan = false;
 #pragma unroll
   for (int j = 0; j < C::V; ++j) nan |= z[j] != z[j] || z[j] == __builtin_inff();
-  const uint64_t votes = __ballot(nan);
-  const int shift = (threadIdx.x & 63) & ~(C::T - 1);
-  const uint64_t mine = C::T == 64 ? votes : (votes >> shift) & ((1ull << (C::T & 63)) - 1);
-  s.bad = live && mine != 0;
+  s.bad = live && team_bits<C::T>(__ballot(nan)) != 0;
   s.dead = !live || (!s.bad && s.high == -__builtin_inff());
   return s;
 }
@@ -178,16 +206,19 @@ __device__ __forceinline__ RowStat softmax_row(float (&e)[C::V], const float (&z
 struct Masks {
   uint64_t bits[kMaxE];
 };
+// A chunk's choices: index (-1: none left) and logit; its tokens' largest logit and
+// what a gate is divided by (NaN: a bad row).
 struct Chosen {
-  int16_t id[kThreads / 16][kMaxTop];
+  int16_t id[64][kMaxTop];
+  float z[64][kMaxTop];
+  float high[64], den[64];
 };
 
-// Rows of one chunk: ids and gates to memory, the chosen to the masks, sums of p
-// to registers.
+// Rows of one chunk: choices to LDS, sums of p to registers.
 template <class C>
-__device__ __forceinline__ void route_rows(const RouteParams& p, int64_t first, int count, Masks& M, Chosen& S,
-                                           float (&share)[C::V], float& zsum, int& live_count) {
-  const int team = threadIdx.x / C::T, lane = threadIdx.x % C::T, shift = (threadIdx.x & 63) & ~(C::T - 1);
+__device__ __forceinline__ void route_rows(const RouteParams& p, int64_t first, int count, Chosen& S, float (&share)[C::V],
+                                           float& zsum, int& live_count) {
+  const int team = threadIdx.x / C::T, lane = threadIdx.x % C::T;
   const int rounds = (count + C::TEAMS - 1) / C::TEAMS;
   for (int i = 0; i < rounds; ++i) {
     const int at = i * C::TEAMS + team;
@@ -197,102 +228,99 @@ __device__ __forceinline__ void route_rows(const RouteParams& p, int64_t first, 
     load_logits<C>(z, p, row, lane);
     const bool live = inside && (!p.live || p.live[row] != 0);
     const RowStat s = softmax_row<C>(e, z, live);
-    if (!s.dead) {
-      const float inv = 1.f / s.sum;
+    const float inv = s.dead ? 0.f : 1.f / s.sum;
 #pragma unroll
-      for (int j = 0; j < C::V; ++j) share[j] += e[j] * inv;
-      if (lane == 0) {
-        const float lse = s.bad ? __builtin_nanf("") : s.high + logf(s.sum);
-        zsum += lse * lse;
-        ++live_count;
-      }
+    for (int j = 0; j < C::V; ++j) share[j] += s.dead ? 0.f : e[j] * inv;
+    const float lse = s.bad ? __builtin_nanf("") : s.high + logf(s.sum);
+    if (!s.dead && lane == 0) {
+      zsum += lse * lse;
+      ++live_count;
     }
-    // lane k keeps choice k: the logit; its index comes from the lane that has it
     const float none = -__builtin_inff();
     const bool routed = !s.dead && !s.bad;
-    float mine = none, chosen_sum = 0.f;
+    float chosen_sum = 0.f;
     for (int k = 0; k < p.top; ++k) {
       float m = z[0];
 #pragma unroll
       for (int j = 1; j < C::V; ++j) m = fmaxf(m, z[j]);
       const float best = team_max<C::T>(m);
-      const uint64_t votes = __ballot(m == best);
-      const uint64_t match = C::T == 64 ? votes : (votes >> shift) & ((1ull << (C::T & 63)) - 1);
+      const uint64_t match = team_bits<C::T>(__ballot(m == best));
       const bool ok = routed && best != none;
       if (ok) chosen_sum += exp_acc(best - s.high);
-      if (ok && lane == __ffsll((unsigned long long)match) - 1) {
-        bool found = false;
+      // the first lane with a match, its first match
+      int v = C::V - 1;
 #pragma unroll
-        for (int j = 0; j < C::V; ++j)
-          if (!found && z[j] == best) {
-            found = true;
-            z[j] = none;
-            S.id[team][k] = (int16_t)(lane * C::V + j);
-          }
+      for (int j = C::V - 2; j >= 0; --j) v = z[j] == best ? j : v;
+      const bool mine = ok && lane == __ffsll((unsigned long long)match) - 1;
+      if (inside && (mine || (!ok && lane == 0))) {
+        S.id[at][k] = (int16_t)(ok ? lane * C::V + v : -1);
+        S.z[at][k] = best;
       }
-      if (lane == k && ok) mine = best;
+#pragma unroll
+      for (int j = 0; j < C::V; ++j) z[j] = mine && j == v ? none : z[j];
     }
-    // the team's lanes exchange through LDS: nothing moves across this point
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (inside && lane < p.top) {
-      const int id = mine != none ? S.id[team][lane] : -1;
-      p.ids[row * p.top + lane] = id;
-      const float gate = exp_acc(mine - s.high) / (p.normalize ? chosen_sum : s.sum);
-      p.gates[row * p.top + lane] = s.bad ? __builtin_nanf("") : id < 0 ? 0.f : gate;
-      if (id >= 0) atomicOr((unsigned long long*)&M.bits[id], 1ull << at);
+    if (inside && lane == 0) {
+      S.high[at] = s.high;
+      S.den[at] = s.bad ? __builtin_nanf("") : p.normalize ? chosen_sum : s.sum;
     }
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
-// Sums over the teams, in their order, of what each lane holds of its experts, and of
-// lse^2 and live tokens: all threads get the latter, sums[e] the former.
+// Ids and gates of a chunk to memory, the chosen to the masks.
 template <class C>
-__device__ __forceinline__ void join_teams(float* sums, float (*stage)[kMaxE], const float (&share)[C::V], float& z, int& n,
-                                           float* zs, int* ns, int experts) {
+__device__ __forceinline__ void route_pairs(const RouteParams& p, int64_t first, int count, Masks& M, const Chosen& S) {
+  for (int i = threadIdx.x; i < count * p.top; i += C::THREADS) {
+    const int t = i / p.top, k = i - t * p.top, id = S.id[t][k];
+    const float den = S.den[t];
+    p.ids[first * p.top + i] = id;
+    p.gates[first * p.top + i] = id >= 0 ? exp_acc(S.z[t][k] - S.high[t]) / den : den != den ? den : 0.f;
+    if (id >= 0) atomicOr((unsigned long long*)&M.bits[id], 1ull << t);
+  }
+}
+
+template <class C>
+struct Join {
+  static constexpr int ROWS = C::WAVES < 8 ? C::WAVES : 8;
+  float sums[C::MAXE], stage[ROWS][C::MAXE], z[C::WAVES];
+  int n[C::WAVES];
+};
+// Sums over the teams, in a fixed order, of what each lane holds of its experts (J.sums),
+// and of lse^2 and live tokens, which all threads get.
+template <class C>
+__device__ __forceinline__ void join_teams(Join<C>& J, const float (&share)[C::V], float& z, int& n, int experts) {
+  constexpr int ROWS = Join<C>::ROWS;
   const int wid = threadIdx.x >> 6, lane = threadIdx.x % C::T;
   float v[C::V];
 #pragma unroll
-  for (int j = 0; j < C::V; ++j) {
-    v[j] = share[j];
-    if constexpr (C::T == 16) {  // the wave's four teams
-      v[j] += __shfl_xor(v[j], 16);
-      v[j] += __shfl_xor(v[j], 32);
-    }
-  }
-  if constexpr (C::T == 16) {
-    z += __shfl_xor(z, 16);
-    z += __shfl_xor(z, 32);
-    n += __shfl_xor(n, 16);
-    n += __shfl_xor(n, 32);
-  }
+  for (int j = 0; j < C::V; ++j) v[j] = over_teams<C::T>(share[j]);
+  z = over_teams<C::T>(z);
+  n = (int)over_teams<C::T>((float)n);  // 64 at most
   if ((threadIdx.x & 63) == 0) {
-    zs[wid] = z;
-    ns[wid] = n;
+    J.z[wid] = z;
+    J.n[wid] = n;
   }
-  // sixteen waves through eight rows of LDS
-  for (int half = 0; half < 2; ++half) {
-    if (wid >> 3 == half && (C::T == 64 || (threadIdx.x & 63) < 16))
+  for (int part = 0; part < C::WAVES / ROWS; ++part) {
+    if (wid / ROWS == part && (int)(threadIdx.x & 63) < C::T)
 #pragma unroll
       for (int j = 0; j < C::V; ++j) {
         const int e = lane * C::V + j;
-        if (e < experts) stage[wid & 7][e] = half ? stage[wid & 7][e] + v[j] : v[j];
+        float* q = &J.stage[wid % ROWS][e];
+        if (e < experts) *q = part ? *q + v[j] : v[j];
       }
     __syncthreads();
   }
-  for (int e = threadIdx.x; e < experts; e += kThreads) {
-    float t = stage[0][e];
+  for (int e = threadIdx.x; e < experts; e += C::THREADS) {
+    float t = J.stage[0][e];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) t += stage[w][e];
-    sums[e] = t;
+    for (int w = 1; w < ROWS; ++w) t += J.stage[w][e];
+    J.sums[e] = t;
   }
   z = 0.f;
   n = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) {
-    z += zs[w];
-    n += ns[w];
+  for (int w = 0; w < C::WAVES; ++w) {
+    z += J.z[w];
+    n += J.n[w];
   }
   __syncthreads();
 }
@@ -330,68 +358,67 @@ __device__ __forceinline__ double wave_sum_double(double v) {
 
 // Everything, for up to kOne tokens (or none).
 template <class C>
-__global__ __launch_bounds__(kThreads, 4) void route_one_kernel(RouteParams p) {
+__global__ __launch_bounds__(C::THREADS) void route_one_kernel(RouteParams p) {
   __shared__ Masks M;
   __shared__ Chosen S;
-  __shared__ float sums[kMaxE], stage[8][kMaxE], zs[kThreads / 64];
-  __shared__ int counts[kMaxE], off[kMaxE + 1], ns[kThreads / 64];
+  __shared__ Join<C> J;
+  __shared__ int counts[C::MAXE], off[C::MAXE + 1];
   const int count = (int)p.rows;
-  for (int e = threadIdx.x; e < p.experts; e += kThreads) M.bits[e] = 0;
-  __syncthreads();
+  for (int e = threadIdx.x; e < p.experts; e += C::THREADS) M.bits[e] = 0;
   float share[C::V], z = 0.f;
   int n = 0;
 #pragma unroll
   for (int j = 0; j < C::V; ++j) share[j] = 0.f;
-  if (count) route_rows<C>(p, 0, count, M, S, share, z, n);
-  join_teams<C>(sums, stage, share, z, n, zs, ns, p.experts);  // its barriers: the masks are whole, ids written
-  for (int e = threadIdx.x; e < p.experts; e += kThreads) counts[e] = __popcll(M.bits[e]);
+  if (count) route_rows<C>(p, 0, count, S, share, z, n);
+  join_teams<C>(J, share, z, n, p.experts);  // its barriers: the choices are whole
+  route_pairs<C>(p, 0, count, M, S);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.experts; e += C::THREADS) counts[e] = __popcll(M.bits[e]);
   __syncthreads();
   scan_offsets(off, counts, p.experts);
-  for (int e = threadIdx.x; e <= p.experts; e += kThreads) {
+  for (int e = threadIdx.x; e <= p.experts; e += C::THREADS) {
     p.counts[e] = e < p.experts ? counts[e] : n;
     p.offsets[e] = off[e];
   }
   if (threadIdx.x < 64) {
     double dot = 0.0;
-    for (int e = threadIdx.x; e < p.experts; e += 64) dot += (double)counts[e] * (double)sums[e];
+    for (int e = threadIdx.x; e < p.experts; e += 64) dot += (double)counts[e] * (double)J.sums[e];
     dot = wave_sum_double(dot);
     if (threadIdx.x == 0) write_loss(p, dot, z, n);
   }
-  if (p.slots) {
-    const int i0 = threadIdx.x;  // 1024 pairs at most
-    if (i0 < count * p.top) {
-      const int e = p.ids[i0];
-      int slot = -1;
-      if (e >= 0) {
-        slot = off[e] + __popcll(M.bits[e] & ((1ull << (i0 / p.top)) - 1));
-        p.tokens[slot] = i0 / p.top;
-      }
-      p.slots[i0] = slot;
+  if (!p.slots) return;
+  for (int i = threadIdx.x; i < count * p.top; i += C::THREADS) {
+    const int t = i / p.top, e = S.id[t][i - t * p.top];
+    int slot = -1;
+    if (e >= 0) {
+      slot = off[e] + __popcll(M.bits[e] & ((1ull << t) - 1));
+      p.tokens[slot] = t;
     }
-    for (int i = off[p.experts] + threadIdx.x; i < count * p.top; i += kThreads) p.tokens[i] = -1;
+    p.slots[i] = slot;
+    if (i >= off[p.experts]) p.tokens[i] = -1;
   }
 }
 
 template <class C>
-__global__ __launch_bounds__(kThreads, 4) void route_rows_kernel(RouteParams p, int64_t chunks, bool between) {
+__global__ __launch_bounds__(C::THREADS) void route_rows_kernel(RouteParams p, int64_t chunks, bool between) {
   __shared__ Masks M;
   __shared__ Chosen S;
-  __shared__ float sums[kMaxE], stage[8][kMaxE], zs[kThreads / 64];
-  __shared__ int ns[kThreads / 64];
+  __shared__ Join<C> J;
   const RouteWs w = route_ws(p.ws, chunks, p.experts, between);
   const int64_t b = blockIdx.x, first = b * C::TEAMS;
   const int count = (int)min((int64_t)C::TEAMS, p.rows - first);
-  for (int e = threadIdx.x; e < p.experts; e += kThreads) M.bits[e] = 0;
-  __syncthreads();
+  for (int e = threadIdx.x; e < p.experts; e += C::THREADS) M.bits[e] = 0;
   float share[C::V], z = 0.f;
   int n = 0;
 #pragma unroll
   for (int j = 0; j < C::V; ++j) share[j] = 0.f;
-  route_rows<C>(p, first, count, M, S, share, z, n);
-  join_teams<C>(sums, stage, share, z, n, zs, ns, p.experts);
+  route_rows<C>(p, first, count, S, share, z, n);
+  join_teams<C>(J, share, z, n, p.experts);
+  route_pairs<C>(p, first, count, M, S);
+  __syncthreads();
   const int wide = (p.experts + 3) / 4 * 4;
-  for (int e = threadIdx.x; e < wide; e += kThreads) w.count[b * wide + e] = e < p.experts ? (uint8_t)__popcll(M.bits[e]) : 0;
-  for (int e = threadIdx.x; e < p.experts; e += kThreads) w.share[b * p.experts + e] = sums[e];
+  for (int e = threadIdx.x; e < wide; e += C::THREADS) w.count[b * wide + e] = e < p.experts ? (uint8_t)__popcll(M.bits[e]) : 0;
+  for (int e = threadIdx.x; e < p.experts; e += C::THREADS) w.share[b * p.experts + e] = J.sums[e];
   if (threadIdx.x == 0) {
     w.zsum[b] = z;
     w.live[b] = n;
@@ -583,17 +610,22 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
   const int64_t step = (int64_t)gridDim.x * TEAMS;
   int64_t base = (int64_t)blockIdx.x * TEAMS;
   // a row's data, loaded ahead of what the row before it computes
-  float nz[C::V], ng = 0.f, nd = 0.f;
-  int nid = -1;
+  constexpr int NK = (kMaxTop + C::T - 1) / C::T;  // choices a lane holds: lane, lane + T, ..
+  float nz[C::V], ng[NK] = {}, nd[NK] = {};
+  int nid[NK];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) nid[i] = -1;
   bool nlive = false;
   auto fetch = [&](int64_t b) {
     const int64_t row = min(b + team, p.rows - 1);
     load_logits<C>(nz, p, row, lane);
-    if (p.dgates && lane < p.top) {
-      nid = p.ids[row * p.top + lane];
-      ng = p.gates[row * p.top + lane];
-      nd = p.dgates[row * p.top + lane];
-    }
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+      if (p.dgates && lane + i * C::T < p.top) {
+        nid[i] = p.ids[row * p.top + lane + i * C::T];
+        ng[i] = p.gates[row * p.top + lane + i * C::T];
+        nd[i] = p.dgates[row * p.top + lane + i * C::T];
+      }
     nlive = !p.live || p.live[row] != 0;
   };
   fetch(base);
@@ -612,8 +644,15 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
     float z[C::V], e[C::V];
 #pragma unroll
     for (int j = 0; j < C::V; ++j) z[j] = nz[j];
-    const int my_id = nid;
-    const float my_g = nid < 0 ? 0.f : ng, my_d = nid < 0 ? 0.f : nd;
+    int my_id[NK];
+    float my_g[NK], my_d[NK], gd = 0.f;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      my_id[i] = nid[i];
+      my_g[i] = nid[i] < 0 ? 0.f : ng[i];
+      my_d[i] = nid[i] < 0 ? 0.f : nd[i];
+      gd += my_g[i] * my_d[i];
+    }
     if (base + step < p.rows) fetch(base + step);
     const RowStat s = softmax_row<C>(e, z, live);
     const float inv = 1.f / s.sum;
@@ -624,7 +663,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
       dot += e[j] * a[j];
     }
     dot = team_sum<C::T>(dot);
-    const float gd = p.dgates ? team_sum<C::T>(my_g * my_d) : 0.f;
+    gd = team_sum<C::T>(gd);
     // p's factor: the balance and z parts, and without normalisation the gates' own
     const float lse = s.high + logf(s.sum);
     const float all = cz * lse - dot - (p.normalize ? 0.f : gd);
@@ -632,13 +671,17 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
     for (int j = 0; j < C::V; ++j) z[j] = e[j] * (a[j] + all);
     if (p.dgates) {
       // the chosen ones': normalised g (dg - sum g dg), else g dg
-      const float mine = my_g * (my_d - (p.normalize ? gd : 0.f));
-      for (int k = 0; k < p.top; ++k) {
-        const int id = __shfl(my_id, shift + k);
-        const float d = __shfl(mine, shift + k);
 #pragma unroll
-        for (int j = 0; j < C::V; ++j)
-          if (lane * C::V + j == id) z[j] += d;
+      for (int i = 0; i < NK; ++i) {
+        const float mine = my_g[i] * (my_d[i] - (p.normalize ? gd : 0.f));
+#pragma unroll
+        for (int k = 0; k < (C::T < kMaxTop ? C::T : kMaxTop); ++k) {
+          if (k + i * C::T >= p.top) break;
+          const int id = __shfl(my_id[i], shift + k) - lane * C::V;
+          const float d = __shfl(mine, shift + k);
+#pragma unroll
+          for (int j = 0; j < C::V; ++j) z[j] += j == id ? d : 0.f;
+        }
       }
     }
 #pragma unroll
@@ -649,10 +692,12 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
 
 template <typename E, typename F>
 hipError_t with_cfg(int experts, F&& f) {
-  if (experts <= 64) return f(RCfg<E, 16, 4>());
+  if (experts <= 16) return f(RCfg<E, 4, 4>());
+  if (experts <= 32) return f(RCfg<E, 4, 8>());
+  if (experts <= 64) return f(RCfg<E, 8, 8>());
   if (experts <= 128) return f(RCfg<E, 16, 8>());
-  if (experts <= 256) return f(RCfg<E, 64, 4>());
-  if (experts <= 512) return f(RCfg<E, 64, 8>());
+  if (experts <= 256) return f(RCfg<E, 16, 16>());
+  if (experts <= 512) return f(RCfg<E, 32, 16>());
   return f(RCfg<E, 64, 16>());
 }
 template <typename F>
@@ -673,8 +718,8 @@ hipError_t launch_route(const RouteParams& p, hipStream_t s) {
   const bool between = !counts_in_scatter(chunks, p.experts);
   hipError_t e = with_cfg(p, [&](auto c) {
     typedef decltype(c) C;
-    if (p.rows <= kOne) route_one_kernel<C><<<1, kThreads, 0, s>>>(p);
-    else route_rows_kernel<C><<<dim3((unsigned)chunks), kThreads, 0, s>>>(p, chunks, between);
+    if (p.rows <= kOne) route_one_kernel<C><<<1, C::THREADS, 0, s>>>(p);
+    else route_rows_kernel<C><<<dim3((unsigned)chunks), C::THREADS, 0, s>>>(p, chunks, between);
     return hipGetLastError();
   });
   if (e != hipSuccess || p.rows <= kOne) return e;
