@@ -12,14 +12,20 @@
 //  * fp32 results: that would be what limits them, so the values are widened to
 //    bf16, exactly, and multiplied at half the rate; the sum over each 128 of k is
 //    scaled (ldexp, exact) and added in fp32.
-//  * Tiles by rule (choose): up to kStreamRows rows a group, weights go from memory
-//    to the matrix cores without LDS, a block's waves sharing the contraction;
-//    64 x 64 and 128 x 128 through LDS, two k tiles; 256 x 256 (bf16) loaded
-//    straight into LDS, two groups of waves taking turns at the matrix cores.
+//  * Tiles by rule (choose): for few rows a group, weights go from memory to the
+//    matrix cores without LDS; 64 x 64 and 128 x 128 through LDS, two k tiles;
+//    256 x 256 (bf16) loaded straight into LDS, two groups of waves taking turns at
+//    the matrix cores.
 //  * The matrix instruction's operands are swapped (B first), so a lane ends with
 //    four neighbouring columns of one row of C.
-//  * Rows past a group's end read the group's last row; their results are not
-//    stored.
+//  * Rows past a group's end read the group's last row (256 x 256: zeros); their
+//    results are not stored.
+//
+// Measured, bf16: 32768 rows, 32 experts of 4096 x 1024 134 us (2.05 PFLOP/s), 143 to 154
+// with a router's uneven groups; it also writes 268 MB, 53 us at a copy's rate.  8192 x
+// 8192 x 8192 390 to 440 us, 2.5 to 2.8 PFLOP/s, by what clock the card holds: the
+// instructions alone reach 4.5 at full clock, and are busy 65 to 69% of the cycles.  16
+// rows through 16 experts 14.4 us for 67 MB of weights.  fp32: 375 us, 0.73 PFLOP/s.
 #include <algorithm>
 
 #include "pmx_groups.h"
@@ -739,22 +745,35 @@ __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
 }
 
 // ------------------------------------------------------------ launchers
-constexpr int kStreamRows = 8;
+// The host knows the mean of the groups' rows only, so the rules go by it.
+// Without LDS up to 2 rows a group, and 128 x 128 tiles: bf16, 32 experts of 4096 x
+// 1024, 16 rows 14.4 and 15.3 us, 60 rows 25.2 and 25.9, but 250 rows 29.2 and 26.1.
+// Up to 16 rows where there is not one such tile a unit, since its waves share the
+// contraction: 8 experts of 1024 x 4096, 64 rows 10.9 and 17.5 us, 128 rows 12.3 and
+// 17.8; or in fp32, whose tiles widen rows that are not there: 200 rows 28.3 and 35.0.
+// 256 x 256 from 256 rows (bf16, four k tiles, one tile a unit), and 128 x 128: 32 of
+// 4096 x 1024, 32768 rows 134 and 243 us, 10000 rows 63 and 72; one of 4096 x 4096, 4096
+// rows 60 and 79.
+// 128 x 128 where there is one a unit, and 64 x 64: 6000 rows 48 and 57 us; one of 2003
+// x 1152, 1023 rows, 144 tiles, 14.1 and 10.4 us.  In fp32, whose widening and matrix
+// instructions cost more than the weights' reading, not below 64 rows a group: 1000
+// rows 48.7 and 37.0 us (bf16 27.3 and 27.9).
 enum { STREAM = 0, SMALL = 1, MIDDLE = 2, LARGE = 3 };
 
 int choose(int64_t rows, int k, int n, int groups, int out_dtype, int num_cu) {
   const int64_t avg = rows / groups;
-  if (avg <= kStreamRows) return STREAM;
-  if (out_dtype == PMX_BF16 && avg >= 256 && n >= 256 && k >= 128 * kLargeK && (rows / 256) * ((n + 255) / 256) >= num_cu) return LARGE;
-  if ((rows / 128 + groups) * ((n + 127) / 128) >= num_cu) return MIDDLE;
-  return SMALL;
+  const bool wide = (rows / 128 + groups) * ((n + 127) / 128) >= num_cu;
+  if (avg <= 2 || (avg <= 16 && (!wide || out_dtype == PMX_F32))) return STREAM;
+  if (out_dtype == PMX_BF16 && avg >= 256 && n >= 256 && k >= 128 * kLargeK && (rows / 256) * ((n + 255) / 256) >= num_cu)
+    return LARGE;
+  return wide && !(out_dtype == PMX_F32 && avg <= 64) ? MIDDLE : SMALL;
 }
 
 template <typename O>
 hipError_t launch(const Fp8Params& p, hipStream_t s) {
   const int cfg = choose(p.rows, p.k, p.n, p.groups, p.out_dtype, p.num_cu);
   if (cfg == STREAM) {
-    // waves of 16 columns, or where they are few four to as many
+    // waves of 16 columns, or where there are not eight a unit four to as many
     const int slots = (int)std::min<int64_t>(p.groups, p.rows);  // groups that can have rows
     const int64_t waves = (int64_t)slots * ((p.n + 15) / 16);
     if (waves >= 8 * (int64_t)p.num_cu) {
