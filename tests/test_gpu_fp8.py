@@ -100,6 +100,32 @@ def test_large_groups(env, out):
         _check(env, x, w, cuts, dt)
 
 
+LARGE = [(8300, 520, 2100, [0, 100, 100, 4500, 4501, 8300], 0), (9000, 1000, 2304, [0, 8999, 9000], 0),
+         (9000, 1000, 2304, [0, 8999, 9000], 8), (9000, 600, 2304, [30, 5000, 8000], 3), (66000, 512, 256, None, 0),
+         (17000, 1152, 1111, [0, 0, 17000], 0), (30000, 768, 1024, [0] + [300 * i + 7 for i in range(1, 100)] + [30000], 0)]
+
+
+@pytest.mark.parametrize("case", range(len(LARGE)))
+def test_large_tiles(env, case):
+    """256 x 256 tiles: contractions of 4 to 9 blocks, uneven and empty groups, columns past the last whole tile, results
+    at odd row distances, more than 64 groups."""
+    torch, pmx = env
+    rows, k, n, cuts, pad = LARGE[case]
+    print("fp8 large tiles", LARGE[case][:3], flush=True)
+    g = torch.Generator(device="cuda").manual_seed(case)
+    x = torch.randn(rows, k, generator=g, device="cuda").bfloat16()
+    x *= torch.exp2(torch.randint(-6, 6, (rows, 1), generator=g, device="cuda").float()).bfloat16()
+    groups = 1 if cuts is None else len(cuts) - 1
+    w = torch.randn(groups, n, k, generator=g, device="cuda").bfloat16()
+    w[:, n // 2:, k // 3:] *= 0.01
+    y = _check(env, x, w, cuts, torch.bfloat16)
+    if pad:
+        out = torch.full((rows, n + pad), 3.0, dtype=torch.bfloat16, device="cuda")
+        off = torch.tensor(cuts, dtype=torch.int64, device="cuda")
+        got = pmx.fp8_product(*pmx.fp8_store(x), *pmx.fp8_store_weight(w), off, out=out[:, :n])
+        assert torch.equal(got, y) and bool((out[:, n:] == 3).all())
+
+
 @pytest.mark.parametrize("out", ["bfloat16", "float32"])
 def test_offsets(env, out):
     """Empty groups, rows in no group, int64, offsets out of range or order."""
@@ -155,8 +181,7 @@ def test_what_lies_outside_does_not_enter(env):
     torch, pmx = env
     nan = 0x7F
     for dt in (torch.float32, torch.bfloat16):
-        for rows, n in ((9, 70), (150, 300), (2300, 700)):
-            k = 384
+        for rows, n, k in ((9, 70, 384), (150, 300, 384), (2300, 700, 384), (16600, 1111, 640)):
             x, w = torch.randn(rows, k, device="cuda"), torch.randn(2, n, k, device="cuda")
             xq, xs = pmx.fp8_store(x)
             wq, ws = pmx.fp8_store_weight(w)
@@ -165,11 +190,12 @@ def test_what_lies_outside_does_not_enter(env):
             e4 = torch.float8_e4m3fn
             bx = torch.full((rows + 2, k + 32), nan, dtype=torch.uint8, device="cuda")
             bw = torch.full((2, n + 1, k + 16), nan, dtype=torch.uint8, device="cuda")
-            sx = torch.full((rows + 1, 7), 255, dtype=torch.uint8, device="cuda")
-            sw = torch.full((2, ws.shape[1] + 1, 5), 255, dtype=torch.uint8, device="cuda")
-            bx[1:-1, 16:16 + k], bw[:, :n, :k], sx[:rows, 1:4], sw[:, :-1, 2:5] = xq.view(torch.uint8), wq.view(torch.uint8), xs, ws
+            kb = k // 128
+            sx = torch.full((rows + 1, kb + 4), 255, dtype=torch.uint8, device="cuda")
+            sw = torch.full((2, ws.shape[1] + 1, kb + 2), 255, dtype=torch.uint8, device="cuda")
+            bx[1:-1, 16:16 + k], bw[:, :n, :k], sx[:rows, 1:1 + kb], sw[:, :-1, 2:] = xq.view(torch.uint8), wq.view(torch.uint8), xs, ws
             out = torch.full((rows, n + 5), 3.0, dtype=dt, device="cuda")
-            got = pmx.fp8_product(bx.view(e4)[1:-1, 16:16 + k], sx[:rows, 1:4], bw.view(e4)[:, :n, :k], sw[:, :-1, 2:5], off,
+            got = pmx.fp8_product(bx.view(e4)[1:-1, 16:16 + k], sx[:rows, 1:1 + kb], bw.view(e4)[:, :n, :k], sw[:, :-1, 2:], off,
                                   out=out[:, 2:n + 2])
             assert torch.equal(got, want) and bool((out[:, :2] == 3).all()) and bool((out[:, n + 2:] == 3).all())
 
