@@ -1006,11 +1006,9 @@ def layer_norm_grad(dY, X, stats, weight=None, params=True, out=None, dweight=No
     if params:
         if accumulate and (dweight is None or dbias is None):
             raise ValueError("accumulate needs dweight and dbias")
-        empty = _codes["empty"]
-        if dweight is None:
-            dweight = empty((cols,), dtype=f32, device=X.device)
-        if dbias is None:
-            dbias = empty((cols,), dtype=f32, device=X.device)
+        if dweight is None or dbias is None:
+            both = _codes["empty"](2 * cols, dtype=f32, device=X.device).split_with_sizes((cols, cols))
+            dweight, dbias = both[0] if dweight is None else dweight, both[1] if dbias is None else dbias
         for t in (dweight, dbias):
             if t.dtype != f32 or _vector(t, "dweight and dbias") != cols:
                 raise ValueError("dweight and dbias are fp32, one value per column")
@@ -1058,15 +1056,18 @@ def route(Z, top, live=None, balance=0.0, zloss=0.0, normalize=True, order=True,
     d = _on(Z, live)
     top = int(top)
     q = _route_problem(Z, top, live, balance, zloss, normalize)
-    empty, dev, i32 = _codes["empty"], Z.device, _codes["i32"]
+    empty, dev = _codes["empty"], Z.device
     rows, experts = q.rows, q.experts
-    ids = empty((rows, top), dtype=i32, device=dev)
-    gates = empty((rows, top), dtype=_codes["f32"], device=dev)
-    tally = empty((experts + 1,), dtype=i32, device=dev)
-    offsets = empty((experts + 1,), dtype=i32, device=dev)
-    slots = empty((rows, top), dtype=i32, device=dev) if order else None
-    tokens = empty((rows * top,), dtype=i32, device=dev) if order else None
-    loss = empty((), dtype=_codes["f32"], device=dev)
+    if top < 0:
+        raise ValueError("top is negative")
+    # one buffer of each type, cut up: an allocation costs the host as much as two views
+    n, e1 = rows * top, experts + 1
+    cuts = (n, e1, e1, n, n) if order else (n, e1, e1)
+    parts = empty(sum(cuts), dtype=_codes["i32"], device=dev).split_with_sizes(cuts)
+    ids, tally, offsets = parts[0].view(rows, top), parts[1], parts[2]
+    slots, tokens = (parts[3].view(rows, top), parts[4]) if order else (None, None)
+    gates, loss = empty(n + 1, dtype=_codes["f32"], device=dev).split_with_sizes((n, 1))
+    gates, loss = gates.view(rows, top), loss.view(())
     ref = ctypes.byref(q)
     key = ("route", rows, experts, top)
     need = _sizes.get(key)
