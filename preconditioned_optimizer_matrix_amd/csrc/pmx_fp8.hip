@@ -411,7 +411,6 @@ __global__ __launch_bounds__(256, S == 64 ? 3 : 2) void fp8_tile_kernel(Fp8Param
 // for the stores, 155 with stores that pass the caches by.)
 constexpr int kSide = 256, kHalf = 32 * 1024, kStage = 2 * kHalf;  // bytes of an operand's part, of a k tile
 constexpr int kLargeK = 4;                                         // k tiles it takes at least
-constexpr int kOutPitch = 144, kOutWave = 16 * kOutPitch;          // 16 rows of 64 results on their way out
 typedef __attribute__((address_space(3))) void* lds_ptr;
 __device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -632,64 +631,66 @@ __device__ __forceinline__ void large_turns(f32x16 (&acc)[4][2], const Large& L,
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// A wave's 128 x 64 results, 16 rows at a time through its place in LDS: 16 stores of
-// whole 128-byte lines where C is aligned and the tile's columns are whole.  They pass
-// the caches by: a launch has 32 MB of them at least, the L2s' size.
-__device__ __forceinline__ void large_store(f32x16 (&acc)[4][2], const Large& L, const LItem& it, uint8_t* stage) {
+// A wave's 128 x 64 results, 32 rows at a time through its 4 KB of LDS (16-byte pieces
+// swizzled as the operands'): 16 stores of whole 128-byte lines where C is aligned and
+// the tile's columns are whole.  They pass the caches by: a launch has 32 MB of them at
+// least, the L2s' size.
+__device__ __forceinline__ void large_store(f32x16 (&acc)[4][2], const Large& L, const LItem& it, const uint8_t* stage) {
   const Args p = args();
-  const int lane = here(threadIdx.x & 63), ldc = (int)p->ldc;
+  const int lane = here(threadIdx.x & 63), r = lane & 31, ldc = (int)p->ldc;
   uint16_t* c = reinterpret_cast<uint16_t*>(p->c) + (int64_t)it.row0 * p->ldc + it.n0;
   const bool whole = it.n0 + kSide <= p->n && p->ldc % 8 == 0 && p->ldc <= (1 << 21) && ((uintptr_t)p->c & 15) == 0;
   const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(c, 0, whole ? ((it.rows - 1) * ldc + kSide) * 2 : 0, 0x00020000);
-  const uint32_t w = lds_address(stage) + (lane & 15) * kOutPitch + 8 * (lane >> 5);
-  const uint32_t rd = lds_address(stage) + (lane >> 3) * kOutPitch + (lane & 7) * 16;
+  const uint32_t w = lds_address(stage) + r * 128 + swizzle(r) * 16 + 8 * (lane >> 5);
+  const uint32_t rd0 = lds_address(stage) + (lane >> 3) * 128 + ((lane & 7) ^ (lane >> 4)) * 16, rd1 = rd0 ^ 64;
   const int row0 = L.wm + (lane >> 3), col = L.wn + (lane & 7) * 8, left = p->n - it.n0 - col;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if ((lane >> 4 & 1) == h) {
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int v = 0; v < 4; ++v) {
+        const u32x2_t x = {pack_bf16(acc[i][j][4 * v], acc[i][j][4 * v + 1]), pack_bf16(acc[i][j][4 * v + 2], acc[i][j][4 * v + 3])};
+        asm volatile("ds_write_b64 %0, %1" ::"v"(w ^ (64 * j + 16 * v)), "v"(x) : "memory");
+      }
+    u32x4_t x[4];  // a wave's accesses to LDS keep their order
+    asm volatile(
+        "ds_read_b128 %0, %4\n\t"
+        "ds_read_b128 %1, %5 offset:1024\n\t"
+        "ds_read_b128 %2, %4 offset:2048\n\t"
+        "ds_read_b128 %3, %5 offset:3072\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+        : "v"(rd0), "v"(rd1)
+        : "memory");
+    if (whole) {  // rows past the group's end are past the buffer's
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const u32x2_t x = {pack_bf16(acc[i][j][4 * v], acc[i][j][4 * v + 1]), pack_bf16(acc[i][j][4 * v + 2], acc[i][j][4 * v + 3])};
-            asm volatile("ds_write_b64 %0, %1 offset:%c2" ::"v"(w), "v"(x), "n"(64 * j + 16 * v) : "memory");
+      for (int k = 0; k < 4; ++k)
+        __builtin_amdgcn_raw_buffer_store_b128(x[k], rsrc, (row0 * ldc + col) * 2, (32 * i + 8 * k) * ldc * 2, 2);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = row0 + 32 * i + 8 * k;
+        uint16_t* d = c + (int64_t)row * p->ldc + col;
+        if (row < it.rows && left >= 8) *reinterpret_cast<u32x4_a2*>(d) = x[k];
+        if (row < it.rows && left < 8)
+#pragma unroll 1
+          for (int t = 0; t < left; ++t) {
+            uint32_t u;
+            asm volatile("ds_read_u16 %0, %1\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(u)
+                         : "v"((k & 1 ? rd1 : rd0) + 1024 * k + 2 * t)
+                         : "memory");
+            d[t] = (uint16_t)u;
           }
       }
-      u32x4_t x[2];  // a wave's accesses to LDS keep their order
-      asm volatile(
-          "ds_read_b128 %0, %2\n\t"
-          "ds_read_b128 %1, %2 offset:%c3\n\t"
-          "s_waitcnt lgkmcnt(0)"
-          : "=&v"(x[0]), "=&v"(x[1])
-          : "v"(rd), "n"(8 * kOutPitch)
-          : "memory");
-      if (whole) {  // rows past the group's end are past the buffer's
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          __builtin_amdgcn_raw_buffer_store_b128(x[k], rsrc, (row0 * ldc + col) * 2, (32 * i + 16 * h + 8 * k) * ldc * 2, 2);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int row = row0 + 32 * i + 16 * h + 8 * k;
-          uint16_t* d = c + (int64_t)row * p->ldc + col;
-          if (row < it.rows && left >= 8) *reinterpret_cast<u32x4_a2*>(d) = x[k];
-          if (row < it.rows && left < 8)
-#pragma unroll 1
-            for (int t = 0; t < left; ++t) {
-              uint32_t u;
-              asm volatile("ds_read_u16 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(u) : "v"(rd + 8 * k * kOutPitch + 2 * t) : "memory");
-              d[t] = (uint16_t)u;
-            }
-        }
-      }
     }
+  }
   if (!whole) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // of another number
 }
 
 template <int GROUP>
-__device__ __forceinline__ void large_group(Large& L, LItem it, uint8_t* stage) {
+__device__ __forceinline__ void large_group(Large& L, LItem it) {
   LItem nx = it;
   bool more = L.next(nx);
   int g = 0;
@@ -710,7 +711,9 @@ __device__ __forceinline__ void large_group(Large& L, LItem it, uint8_t* stage) 
     for (int kt = 1; kt < L.kb; ++kt) large_turns<GROUP, false>(acc, L, it, nx, kt, g + kt, cur, next);
     g += L.kb;
     next.wait();
-    large_store(acc, L, it, stage);
+    // through the second group's half of A's last k tile, which both have read, and whose
+    // place the first group loads again only when it next multiplies
+    large_store(acc, L, it, L.smem + (g - 1 & 1) * kStage + kHalf / 2 + (L.wid & 3) * 4096);
     __builtin_amdgcn_s_barrier();
     if (!more) break;
     it = nx;
@@ -722,7 +725,6 @@ __device__ __forceinline__ void large_group(Large& L, LItem it, uint8_t* stage) 
 
 __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t out[8 * kOutWave];
   __shared__ Table T;
   build_table(T, p, kSide, (p.n + kSide - 1) / kSide, 0);
   zero_outside<uint16_t>(p, T.begin[0], T.begin[p.groups]);
@@ -740,8 +742,8 @@ __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
   for (int j = 0; j < 2; ++j) L.load_a(it, it, 1, 1, 2 * L.wid + j);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
-  if (L.wid >> 2) large_group<1>(L, it, out + L.wid * kOutWave);
-  else large_group<0>(L, it, out + L.wid * kOutWave);
+  if (L.wid >> 2) large_group<1>(L, it);
+  else large_group<0>(L, it);
 }
 
 // ------------------------------------------------------------ launchers
