@@ -57,23 +57,56 @@ __device__ __forceinline__ float wave_max(float v) {
 // Pieces of 16 bytes of a row of n elements, at any element alignment.
 typedef u32x4_t piece_a2 __attribute__((aligned(2)));
 typedef u32x4_t piece_a4 __attribute__((aligned(4)));
+template <size_t A>
+struct Parts;
+template <>
+struct Parts<2> {
+  typedef u32x2_t half __attribute__((aligned(2)));
+  typedef uint32_t word __attribute__((aligned(2)));
+};
+template <>
+struct Parts<4> {
+  typedef u32x2_t half __attribute__((aligned(4)));
+  typedef uint32_t word;
+};
 template <typename E>
 constexpr int kPiece = 16 / (int)sizeof(E);
 
-// Elements c .. of a row of n, zeros past its end.
+// Elements c .. of a row of n, zeros past its end (a row's last piece: 8, 4 and 2 bytes of it).
 template <typename E>
 __device__ __forceinline__ u32x4_t load_piece(const E* row, int c, int n) {
   constexpr int V = kPiece<E>;
+  typedef typename Parts<sizeof(E)>::half half_t;
+  typedef typename Parts<sizeof(E)>::word word_t;
   u32x4_t v = {0u, 0u, 0u, 0u};
-  if (c + V <= n) {
+  const int left = n - c;
+  if (left >= V) {
     if constexpr (sizeof(E) == 2) v = *reinterpret_cast<const piece_a2*>(row + c);
     else v = *reinterpret_cast<const piece_a4*>(row + c);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V - 1; ++j)
-      if (c + j < n) {
-        if constexpr (sizeof(E) == 2) v[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
-        else v[j] = __float_as_uint(row[c + j]);
+  }
+  if (n % V != 0 && left > 0 && left < V) {  // the first for all lanes alike
+    const E* p = row + c;
+    if (left & (V / 2)) {
+      const u32x2_t h = *reinterpret_cast<const half_t*>(p);
+      v[0] = h[0];
+      v[1] = h[1];
+      p += V / 2;
+    }
+    const bool second = left & (V / 2);
+    if (left & (V / 4)) {
+      const uint32_t w = *reinterpret_cast<const word_t*>(p);
+      v[0] = second ? v[0] : w;
+      v[2] = second ? w : 0u;
+      p += V / 4;
+    }
+    if constexpr (sizeof(E) == 2)
+      if (left & 1) {
+        const uint32_t w = *p;
+        const int at = left >> 1;  // the word it lies in
+        v[0] = at == 0 ? w : v[0];
+        v[1] = at == 1 ? w : v[1];
+        v[2] = at == 2 ? w : v[2];
+        v[3] = at == 3 ? w : v[3];
       }
   }
   return v;
@@ -95,16 +128,26 @@ __device__ __forceinline__ void store_piece(E* row, int c, int n, const float (&
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = __float_as_uint(f[j]);
   }
-  if (c + V <= n) {
+  typedef typename Parts<sizeof(E)>::half half_t;
+  typedef typename Parts<sizeof(E)>::word word_t;
+  const int left = n - c;
+  if (left >= V) {
     if constexpr (sizeof(E) == 2) *reinterpret_cast<piece_a2*>(row + c) = v;
     else *reinterpret_cast<piece_a4*>(row + c) = v;
-  } else {
-#pragma unroll
-    for (int j = 0; j < V - 1; ++j)
-      if (c + j < n) {
-        if constexpr (sizeof(E) == 2) row[c + j] = (E)(v[j >> 1] >> (16 * (j & 1)));
-        else row[c + j] = f[j];
-      }
+  }
+  if (n % V != 0 && left > 0 && left < V) {
+    E* p = row + c;
+    const bool second = left & (V / 2);
+    if (second) {
+      *reinterpret_cast<half_t*>(p) = u32x2_t{v[0], v[1]};
+      p += V / 2;
+    }
+    if (left & (V / 4)) {
+      *reinterpret_cast<word_t*>(p) = second ? v[2] : v[0];
+      p += V / 4;
+    }
+    if constexpr (sizeof(E) == 2)
+      if (left & 1) *p = (E)(left >> 1 == 0 ? v[0] : left >> 1 == 1 ? v[1] : left >> 1 == 2 ? v[2] : v[3]);
   }
 }
 

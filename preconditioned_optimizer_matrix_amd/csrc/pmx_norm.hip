@@ -6,13 +6,17 @@
 //
 // Bound: HBM.  A row stays in registers, packed as it was read, from its load
 // to its result, so the variance is the two-pass one of the mean's deviations
-// and costs no second read.  One wave holds rows of up to 1024 elements, four
-// or sixteen waves longer ones.  Blocks are persistent: the next row's loads
-// are under way while this one is reduced, weights stay in registers, and in
-// the backward pass a thread's columns stay the same, so it sums dy and dy h of
-// its rows in registers.  The block's teams add those sums in a fixed order in
-// LDS, a second launch adds the blocks' in theirs: no atomics, the same bits on
-// every call.  Statistics and sums are fp32.
+// and costs no second read.  16 lanes hold short rows, a wave those of up to 1024
+// elements, four to sixteen waves longer ones.  Blocks are persistent: the next
+// row's loads are under way while this one is reduced, weights stay in registers
+// (the longest rows': in LDS), and in the backward pass a thread's columns stay the
+// same, so it sums dy and dy h of its rows in registers.  The block's teams add those
+// sums pairwise in LDS, a second launch adds the blocks' in their order: no atomics,
+// the same bits on every call.  Statistics and sums are fp32.
+//
+// Measured (bytes of the rows alone): 32768 x 1024 bf16 forward 22 us, 6.1 TB/s, backward
+// 39, 5.1 TB/s, of which 5 the join; 16384 x 1024 fp32 20.5 and 35; 524288 x 64 bf16 39 and
+// 54; 8192 x 4096 bf16 24 and 44; 2048 x 16384 bf16 32 and 46.  8 rows: 3.3 us.
 #include <algorithm>
 
 #include "pmx_layer.h"
@@ -20,19 +24,21 @@
 namespace pmx {
 namespace {
 
-// W waves a row, NV pieces of 16 bytes a thread, TEAMS rows at a time a block.
-template <typename E_, int W_, int NV_, int TEAMS_>
+// LANES a row, NV pieces of 16 bytes a lane, TEAMS rows at a time a block.
+template <typename E_, int LANES_, int NV_, int TEAMS_>
 struct NCfg {
   typedef E_ E;
-  static constexpr int W = W_, NV = NV_, TEAMS = TEAMS_, V = kPiece<E_>;
-  static constexpr int LANES = 64 * W, THREADS = LANES * TEAMS, COLS = LANES * NV * V;
+  static constexpr int LANES = LANES_, NV = NV_, TEAMS = TEAMS_, V = kPiece<E_>;
+  static constexpr int W = LANES < 64 ? 1 : LANES / 64, THREADS = LANES * TEAMS, COLS = LANES * NV * V;
+  // 1024 threads have 128 registers each: weights in LDS, and with 16 elements a lane no row ahead
+  static constexpr bool LDS_W = LANES == 1024, AHEAD = !(LDS_W && NV * V == 16);
 };
 
-// Sums over the team's lanes of N values; red: [2][TEAMS * W][N], alternating.
+// Sums over the team's lanes of N values; red: [2][waves][N], alternating.
 template <class C, int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[C::TEAMS * C::W][N], int& flip) {
+__device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[C::THREADS / 64][N], int& flip) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  for (int i = 0; i < N; ++i) v[i] = C::LANES == 16 ? row_sum(v[i]) : wave_sum(v[i]);
   if constexpr (C::W > 1) {
     const int wid = threadIdx.x >> 6, team = wid / C::W;
     if ((threadIdx.x & 63) == 0) {
@@ -87,7 +93,7 @@ __device__ __forceinline__ void load_row(u32x4_t (&v)[C::NV], const void* p, int
 template <class C>
 __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormParams p) {
   typedef typename C::E E;
-  __shared__ float red[2][C::TEAMS * C::W][1];
+  __shared__ float red[2][C::THREADS / 64][1];
   const int team = threadIdx.x / C::LANES, lane = threadIdx.x % C::LANES;
   const int64_t step = (int64_t)gridDim.x * C::TEAMS;
   const float cols = (float)p.cols;
@@ -142,11 +148,33 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormParams p) {
   }
 }
 
+// V floats to elements c .. of a row of n.
+template <int V>
+__device__ __forceinline__ void store_piece4(float* row, int c, int n, const float (&f)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; k += 4) {
+    const float q[4] = {f[k], f[k + 1], f[k + 2], f[k + 3]};
+    store_piece(row, c + k, n, q);
+  }
+}
+
+// What is computed from the packed row again is not kept in registers meanwhile (for
+// the longest rows, which have none left; it costs time elsewhere: 32768 x 1024 bf16
+// 44 -> 48 us).
+template <int N>
+__device__ __forceinline__ void again(u32x4_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
+
 template <class C>
 __global__ __launch_bounds__(C::THREADS) void norm_grad_kernel(NormParams p) {
   typedef typename C::E E;
-  __shared__ float red[2][C::TEAMS * C::W][2];
-  __shared__ float sums[2][C::TEAMS > 1 ? C::COLS : 1];
+  constexpr int HALF = C::TEAMS / 2;
+  __shared__ float red[2][C::THREADS / 64][2];
+  // weights [NV * V][LANES]; the teams' sums, half of them at a time
+  __shared__ float lw[C::LDS_W ? C::COLS : 1];
+  __shared__ float sums[HALF ? HALF : 1][2][HALF ? C::COLS : 1];
   const int team = threadIdx.x / C::LANES, lane = threadIdx.x % C::LANES;
   const int64_t step = (int64_t)gridDim.x * C::TEAMS;
   const float inv = 1.f / (float)p.cols;
@@ -154,11 +182,24 @@ __global__ __launch_bounds__(C::THREADS) void norm_grad_kernel(NormParams p) {
   int64_t base = (int64_t)blockIdx.x * C::TEAMS;
   auto row_of = [&](int64_t b) { return min(b + team, p.rows - 1); };
   u32x4_t x[C::NV], g[C::NV];
-  load_row<C>(x, p.x, p.ldx, row_of(base), p.cols, lane);
-  load_row<C>(g, p.dy, p.lddy, row_of(base), p.cols, lane);
-  float mean = p.stats[2 * row_of(base)], r = p.stats[2 * row_of(base) + 1];
-  float w[C::NV][C::V], dw[C::NV][C::V], db[C::NV][C::V];
-  load_param<C>(w, p.weight, p.param_dtype, p.cols, lane, 1.f);
+  float mean, r;
+  auto fetch = [&](u32x4_t(&a)[C::NV], u32x4_t(&b)[C::NV], float& m, float& q, int64_t at) {
+    const int64_t row = row_of(at);
+    load_row<C>(a, p.x, p.ldx, row, p.cols, lane);
+    load_row<C>(b, p.dy, p.lddy, row, p.cols, lane);
+    m = p.stats[2 * row];
+    q = p.stats[2 * row + 1];
+  };
+  fetch(x, g, mean, r, base);
+  float wr[C::NV][C::V], dw[C::NV][C::V], db[C::NV][C::V];
+  load_param<C>(wr, p.weight, p.param_dtype, p.cols, lane, 1.f);
+  if constexpr (C::LDS_W) {  // each lane its own: no barrier
+#pragma unroll
+    for (int i = 0; i < C::NV; ++i)
+#pragma unroll
+      for (int j = 0; j < C::V; ++j) lw[(i * C::V + j) * C::LANES + lane] = wr[i][j];
+  }
+  auto w = [&](int i, int j) { return C::LDS_W ? lw[(i * C::V + j) * C::LANES + lane] : wr[i][j]; };
 #pragma unroll
   for (int i = 0; i < C::NV; ++i)
 #pragma unroll
@@ -167,12 +208,7 @@ __global__ __launch_bounds__(C::THREADS) void norm_grad_kernel(NormParams p) {
     u32x4_t nx[C::NV], ng[C::NV];
     float nmean = 0.f, nr = 0.f;
     const bool more = base + step < p.rows;
-    if (more) {
-      load_row<C>(nx, p.x, p.ldx, row_of(base + step), p.cols, lane);
-      load_row<C>(ng, p.dy, p.lddy, row_of(base + step), p.cols, lane);
-      nmean = p.stats[2 * row_of(base + step)];
-      nr = p.stats[2 * row_of(base + step) + 1];
-    }
+    if (C::AHEAD && more) fetch(nx, ng, nmean, nr, base + step);
     const int64_t row = base + team;
     const bool own = row < p.rows;
     float s[2] = {0.f, 0.f};
@@ -180,15 +216,19 @@ __global__ __launch_bounds__(C::THREADS) void norm_grad_kernel(NormParams p) {
     for (int i = 0; i < C::NV; ++i)
 #pragma unroll
       for (int j = 0; j < C::V; ++j) {
-        const float dy = element<E>(g[i], j), h = (element<E>(x[i], j) - mean) * r;
-        s[0] += dy * w[i][j];
-        s[1] += dy * w[i][j] * h;
+        const float dy = element<E>(g[i], j), h = (element<E>(x[i], j) - mean) * r, gw = dy * w(i, j);
+        s[0] += gw;
+        s[1] += gw * h;
         if (own) {
           dw[i][j] += dy * h;
           db[i][j] += dy;
         }
       }
     team_sum<C, 2>(s, red, flip);
+    if constexpr (C::LDS_W) {
+      again(x);
+      again(g);
+    }
     if (own && p.dx) {
       const float m0 = s[0] * inv, m1 = s[1] * inv;
       E* dx = reinterpret_cast<E*>(p.dx) + row * p.lddx;
@@ -198,12 +238,13 @@ __global__ __launch_bounds__(C::THREADS) void norm_grad_kernel(NormParams p) {
 #pragma unroll
         for (int j = 0; j < C::V; ++j) {
           const float h = (element<E>(x[i], j) - mean) * r;
-          f[j] = r * (element<E>(g[i], j) * w[i][j] - m0 - h * m1);
+          f[j] = r * (element<E>(g[i], j) * w(i, j) - m0 - h * m1);
         }
         store_piece(dx, (i * C::LANES + lane) * C::V, p.cols, f);
       }
     }
-    if (more) {
+    if (!more) break;
+    if constexpr (C::AHEAD) {
 #pragma unroll
       for (int i = 0; i < C::NV; ++i) {
         x[i] = nx[i];
@@ -211,36 +252,40 @@ __global__ __launch_bounds__(C::THREADS) void norm_grad_kernel(NormParams p) {
       }
       mean = nmean;
       r = nr;
+    } else {
+      fetch(x, g, mean, r, base + step);
     }
   }
   if (!p.part) return;
-  // the teams' sums in their order
-  float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
-  if constexpr (C::TEAMS > 1) {
-    for (int t = 0; t < C::TEAMS; ++t) {
-      if (team == t)
+  // the teams' sums, pairwise: the upper half of those left hands its sums to the lower
 #pragma unroll
-        for (int i = 0; i < C::NV; ++i)
+  for (int half = HALF; half > 0; half /= 2) {
+    if (team >= half && team < 2 * half)
 #pragma unroll
-          for (int j = 0; j < C::V; ++j) {
-            const int c = (i * C::V + j) * C::LANES + lane;
-            sums[0][c] = t ? sums[0][c] + dw[i][j] : dw[i][j];
-            sums[1][c] = t ? sums[1][c] + db[i][j] : db[i][j];
-          }
-      __syncthreads();
-    }
-  }
-  if (team == 0)
+      for (int i = 0; i < C::NV; ++i)
 #pragma unroll
-    for (int i = 0; i < C::NV; ++i)
-#pragma unroll
-      for (int j = 0; j < C::V; ++j) {
-        const int c = (i * C::LANES + lane) * C::V + j, k = (i * C::V + j) * C::LANES + lane;
-        if (c < p.cols) {
-          out[c] = C::TEAMS > 1 ? sums[0][k] : dw[i][j];
-          out[p.cols + c] = C::TEAMS > 1 ? sums[1][k] : db[i][j];
+        for (int j = 0; j < C::V; ++j) {
+          sums[team - half][0][(i * C::V + j) * C::LANES + lane] = dw[i][j];
+          sums[team - half][1][(i * C::V + j) * C::LANES + lane] = db[i][j];
         }
-      }
+    __syncthreads();
+    if (team < half)
+#pragma unroll
+      for (int i = 0; i < C::NV; ++i)
+#pragma unroll
+        for (int j = 0; j < C::V; ++j) {
+          dw[i][j] += sums[team][0][(i * C::V + j) * C::LANES + lane];
+          db[i][j] += sums[team][1][(i * C::V + j) * C::LANES + lane];
+        }
+    __syncthreads();
+  }
+  if (team) return;
+  float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
+#pragma unroll
+  for (int i = 0; i < C::NV; ++i) {
+    store_piece4<C::V>(out, (i * C::LANES + lane) * C::V, p.cols, dw[i]);
+    store_piece4<C::V>(out + p.cols, (i * C::LANES + lane) * C::V, p.cols, db[i]);
+  }
 }
 
 // dw and db: the blocks' sums in their order, 32 segments of them at a time.
@@ -280,17 +325,19 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormParams p) {
 template <typename E, typename F>
 hipError_t with_cfg(int cols, F&& f) {
   constexpr int V = kPiece<E>;
-  if (cols <= 64 * V) return f(NCfg<E, 1, 1, 8>());
-  if (cols <= 128 * V) return f(NCfg<E, 1, 2, 8>());
+  if (cols <= 16 * V) return f(NCfg<E, 16, 1, 32>());
+  if (cols <= 32 * V) return f(NCfg<E, 16, 2, 32>());
+  if (cols <= 64 * V) return f(NCfg<E, 64, 1, 8>());
+  if (cols <= 128 * V) return f(NCfg<E, 64, 2, 8>());
   if constexpr (sizeof(E) == 4) {
-    if (cols <= 256 * V) return f(NCfg<E, 1, 4, 8>());
+    if (cols <= 256 * V) return f(NCfg<E, 64, 4, 8>());
   } else {
-    if (cols <= 256 * V) return f(NCfg<E, 4, 1, 2>());
+    if (cols <= 256 * V) return f(NCfg<E, 256, 1, 2>());
   }
-  if (cols <= 512 * V) return f(NCfg<E, 4, 2, 2>());
-  if (cols <= 1024 * V) return f(NCfg<E, 4, 4, 2>());
-  if (cols <= 2048 * V) return f(NCfg<E, 16, 2, 1>());
-  if constexpr (sizeof(E) == 4) return f(NCfg<E, 16, 4, 1>());
+  if (cols <= 512 * V) return f(NCfg<E, 256, 2, 2>());
+  if (cols <= 1024 * V) return f(NCfg<E, 512, 2, 1>());
+  if (cols <= 2048 * V) return f(NCfg<E, 1024, 2, 1>());
+  if constexpr (sizeof(E) == 4) return f(NCfg<E, 1024, 4, 1>());
   return hipErrorInvalidValue;
 }
 template <typename F>
@@ -298,8 +345,12 @@ hipError_t with_cfg(int dtype, int cols, F&& f) {
   return dtype == PMX_BF16 ? with_cfg<uint16_t>(cols, f) : with_cfg<float>(cols, f);
 }
 
-int grad_blocks(int64_t rows, int teams) {
-  return (int)std::min<int64_t>((rows + teams - 1) / teams, 512);
+// Blocks of the backward pass: two a unit where a lane has one piece of a row on its
+// way, else one, which halves what the second launch reads: 65536 x 512 bf16 (one piece)
+// 38 and 45 us, 32768 x 1024 (two) 41 and 39, 2048 x 4096 23 and 18.
+int grad_blocks(int64_t rows, int teams, int pieces) {
+  const int64_t most = pieces == 1 && rows >= 4096 ? 512 : 256;
+  return (int)std::min<int64_t>((rows + teams - 1) / teams, most);
 }
 
 }  // namespace
@@ -308,7 +359,7 @@ size_t norm_grad_floats(int64_t rows, int cols, int dtype) {
   if (rows == 0) return 0;
   size_t n = 0;
   (void)with_cfg(dtype, cols, [&](auto c) {
-    n = (size_t)grad_blocks(rows, decltype(c)::TEAMS) * 2 * cols;
+    n = (size_t)grad_blocks(rows, decltype(c)::TEAMS, decltype(c)::NV) * 2 * cols;
     return hipSuccess;
   });
   return n;
@@ -330,7 +381,7 @@ hipError_t launch_norm_grad(NormParams p, hipStream_t s) {
   if (p.rows > 0) {
     const hipError_t e = with_cfg(p.dtype, p.cols, [&](auto c) {
       typedef decltype(c) C;
-      p.blocks = grad_blocks(p.rows, C::TEAMS);
+      p.blocks = grad_blocks(p.rows, C::TEAMS, C::NV);
       norm_grad_kernel<C><<<dim3(p.blocks), dim3(C::THREADS), 0, s>>>(p);
       return hipGetLastError();
     });
