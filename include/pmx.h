@@ -738,13 +738,11 @@ pmx_status pmx_silu_checkpoint_grad(pmx_handle handle, const void* dA, pmx_dtype
  * C is PMX_F32 or PMX_BF16; sums are fp32.  Values 16-byte aligned, row distances
  * and stride_b multiples of 16.  Limits as in pmx_grouped_product.
  */
-pmx_status pmx_fp8_product_workspace_size(int64_t rows, int k, int n, int groups, size_t* bytes);
 pmx_status pmx_fp8_product(pmx_handle handle, const uint8_t* A, int64_t rows, int k, int64_t lda,
                            const uint8_t* A_scales, int64_t ldas, const uint8_t* B, int n, int64_t ldb,
                            int64_t stride_b, const uint8_t* B_scales, int64_t ldbs, int64_t stride_bs,
                            const void* offsets, pmx_itype itype, int groups, void* C,
-                           pmx_dtype out_dtype, int64_t ldc, void* workspace, size_t workspace_bytes,
-                           void* stream);
+                           pmx_dtype out_dtype, int64_t ldc, void* stream);
 
 /*
  * Launch trace for benchmarking.  While enabled, every kernel that a call on

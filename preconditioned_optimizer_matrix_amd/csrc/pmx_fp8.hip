@@ -799,8 +799,6 @@ hipError_t launch(const Fp8Params& p, hipStream_t s) {
 
 }  // namespace
 
-int fp8_splits(int64_t rows, int k, int n, int groups) { return 1; }
-
 hipError_t launch_fp8(const Fp8Params& p, hipStream_t s) {
   return p.out_dtype == PMX_BF16 ? launch<uint16_t>(p, s) : launch<float>(p, s);
 }

@@ -262,11 +262,8 @@ struct Fp8Params {
   void* c;
   int64_t ldc;
   int out_dtype;
-  float* part;
-  int splits;
   int num_cu;
 };
-int fp8_splits(int64_t rows, int k, int n, int groups);
 hipError_t launch_fp8(const Fp8Params& p, hipStream_t s);
 
 }  // namespace pmx

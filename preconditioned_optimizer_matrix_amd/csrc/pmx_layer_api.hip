@@ -386,28 +386,16 @@ bool fp8_shape_ok(int64_t rows, int k, int n, int groups) {
   return rows >= 0 && rows <= kMaxRows && k >= 1 && k <= kMaxSide && n >= 1 && n <= kMaxSide && groups >= 1 &&
          groups <= PMX_MAX_GROUPS;
 }
-// tile counts and their splits are 32-bit on the device
+// tile counts are 32-bit on the device
 bool fp8_items_ok(int64_t rows, int n, int groups) {
   return (rows / 16 + groups) * (int64_t)((n + 63) / 64) * 64 <= kMaxRows;
 }
-size_t fp8_ws(int64_t rows, int k, int n, int groups) {
-  const int s = rows ? fp8_splits(rows, (int)up128(k), n, groups) : 1;
-  return s > 1 ? (size_t)s * rows * n * sizeof(float) : 0;
-}
 }  // namespace
-
-pmx_status pmx_fp8_product_workspace_size(int64_t rows, int k, int n, int groups, size_t* bytes) {
-  if (!bytes || !fp8_shape_ok(rows, k, n, groups)) return PMX_ERR_INVALID_VALUE;
-  if (!fp8_items_ok(rows, n, groups)) return PMX_ERR_NOT_SUPPORTED;
-  *bytes = fp8_ws(rows, k, n, groups);
-  return PMX_OK;
-}
 
 pmx_status pmx_fp8_product(pmx_handle h, const uint8_t* A, int64_t rows, int k, int64_t lda, const uint8_t* A_scales,
                            int64_t ldas, const uint8_t* B, int n, int64_t ldb, int64_t stride_b,
                            const uint8_t* B_scales, int64_t ldbs, int64_t stride_bs, const void* offsets,
-                           pmx_itype itype, int groups, void* C, pmx_dtype out_dtype, int64_t ldc, void* ws,
-                           size_t ws_bytes, void* stream) {
+                           pmx_itype itype, int groups, void* C, pmx_dtype out_dtype, int64_t ldc, void* stream) {
   if (!h || !dtype_ok(out_dtype) || !itype_ok(itype) || !fp8_shape_ok(rows, k, n, groups)) return PMX_ERR_INVALID_VALUE;
   const size_t os = elem_size(out_dtype);
   const int64_t kp = up128(k);
@@ -424,16 +412,13 @@ pmx_status pmx_fp8_product(pmx_handle h, const uint8_t* A, int64_t rows, int k, 
   if (!fp8_items_ok(rows, n, groups) || lda > kMaxGroupedLd || ldb > kMaxGroupedLd || ldas > kMaxGroupedLd ||
       ldbs > kMaxGroupedLd)
     return PMX_ERR_NOT_SUPPORTED;
-  const size_t need = fp8_ws(rows, k, n, groups);
   const Extent all[] = {extent(C, rows, n, ldc, os),
-                        extent(ws, 1, (int64_t)need, (int64_t)need, 1),
                         values_extent(A, lda, rows, k, 1),
                         scales_extent(A_scales, ldas, rows, k, 1),
                         extent_batch(B, groups, stride_b, n, kp, ldb, 1),
                         extent_batch(B_scales, groups, stride_bs, sn, kp / kBlock8, ldbs, 1),
                         extent(offsets, 1, groups + 1, groups + 1, index_size(itype))};
-  if (clash(all, 2)) return PMX_ERR_ALIAS;
-  if (workspace_bad(ws, ws_bytes, need)) return PMX_ERR_WORKSPACE;
+  if (clash(all, 1)) return PMX_ERR_ALIAS;
   if (rows == 0) return PMX_OK;
   Fp8Params p = {};
   p.a = A;
@@ -455,8 +440,6 @@ pmx_status pmx_fp8_product(pmx_handle h, const uint8_t* A, int64_t rows, int k, 
   p.c = C;
   p.ldc = ldc;
   p.out_dtype = out_dtype;
-  p.part = (float*)ws;
-  p.splits = fp8_splits(rows, (int)kp, n, groups);
   p.num_cu = h->num_cu;
   return enqueue(h, stream, [&](hipStream_t s) { return launch_fp8(p, s); });
 }

@@ -53,7 +53,7 @@ EXPORTS = [
     "pmx_route", "pmx_route_grad", "pmx_route_workspace_size",
     "pmx_fp8_store", "pmx_fp8_load", "pmx_fp8_store_weight",
     "pmx_silu_checkpoint", "pmx_silu_checkpoint_grad",
-    "pmx_fp8_product", "pmx_fp8_product_workspace_size",
+    "pmx_fp8_product",
 ]
 
 # kernel classes of the launch trace (pmx_kernel_class)
@@ -220,10 +220,8 @@ def _load():
                                        _i64, _vp, _i64, _vp]),
         "pmx_silu_checkpoint_grad": (_i32, [_vp, _vp, _i32, _i64, _i32, _i64, _vp, _i64, _vp,
                                             _i64, _i32, _vp, _i64, _vp, _i64, _vp]),
-        "pmx_fp8_product_workspace_size": (_i32, [_i64, _i32, _i32, _i32, ctypes.POINTER(_sz)]),
         "pmx_fp8_product": (_i32, [_vp, _vp, _i64, _i32, _i64, _vp, _i64, _vp, _i32, _i64, _i64,
-                                   _vp, _i64, _i64, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _sz,
-                                   _vp]),
+                                   _vp, _i64, _i64, _vp, _i32, _i32, _vp, _i32, _i64, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -1237,7 +1235,7 @@ def silu_checkpoint_grad(dA, values, scales, gated=False, again=True, out=None, 
     return out, act
 
 
-def fp8_product(A, A_scales, B, B_scales, offsets=None, out=None, out_dtype=None, ws=None):
+def fp8_product(A, A_scales, B, B_scales, offsets=None, out=None, out_dtype=None):
     """C[t] = A[t] B[e]^T for the rows offsets[e] <= t < offsets[e + 1] of group
     e, rows in no group zeros: A and its scales from fp8_store (rows x k), B and
     its scales from fp8_store_weight (groups x n x k; transposed for the input
@@ -1263,11 +1261,9 @@ def fp8_product(A, A_scales, B, B_scales, offsets=None, out=None, out_dtype=None
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else _torch().bfloat16
     out, ldc = _out_like(out, (rows, n), out_dtype, A.device)
-    need = _need("pmx_fp8_product_workspace_size", rows, k, n, groups)
-    wp, wn = _ws_for(need, ws, A.device)
     h, st = _call(d)
     check(lib.pmx_fp8_product(
         h, A.data_ptr(), rows, k, lda, A_scales.data_ptr(), ldas, B.data_ptr(), n, ldb, sb,
-        B_scales.data_ptr(), ldbs, sbs, op, ot, groups, out.data_ptr(), _elem_code(out), ldc, wp, wn, st),
+        B_scales.data_ptr(), ldbs, sbs, op, ot, groups, out.data_ptr(), _elem_code(out), ldc, st),
         "fp8_product")
     return out

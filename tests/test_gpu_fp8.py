@@ -235,5 +235,3 @@ def test_refusals(env):
     alias = torch.empty(20 * 256, dtype=torch.uint8, device="cuda")
     refused(lambda: pmx.fp8_product(alias.view(torch.float8_e4m3fn).view(20, 256), xs, wq, ws, off,
                                     out=alias[:20 * 30 * 2].view(torch.bfloat16).view(20, 30)), pmx.PmxError)
-    bad = off.clone()
-    refused(lambda: pmx.fp8_product(xq, xs, wq, ws, bad, ws=torch.empty(8, device="cuda")[::2]))

@@ -66,7 +66,8 @@ def _close(torch, got, want, tol, what):
 
 
 SIZES = [(1, 1), (1, 7), (3, 64), (17, 500), (64, 511), (65, 512), (40, 513), (33, 1001), (9, 1024), (5, 1025), (37, 2047),
-         (8, 4096), (21, 4099), (6, 8192), (3, 8193), (4, 16384), (2, 16381), (700, 129), (2500, 40)]
+         (8, 4096), (21, 4099), (6, 8192), (3, 8193), (4, 16384), (2, 16381), (700, 129), (2500, 40), (50, 100), (1100, 2100), (600, 8200),
+         (300, 16384)]
 
 
 @pytest.mark.parametrize("rows,cols", SIZES)
