@@ -454,19 +454,19 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(RouteParams p, int64_t
 // The loss from the chunks' sums: 16 experts a block, the chunks in 32 segments; the
 // last block to finish adds the parts up.
 __device__ __forceinline__ void route_loss(const RouteParams& p, const RouteWs& w, int q, int64_t chunks) {
-  __shared__ float seg[32][17];
+  __shared__ double seg[32][17];
   __shared__ int part[32][17];
   __shared__ double zs[8];
   __shared__ int ns[8], last;
   const int parts = (p.experts + 15) / 16, wide = (p.experts + 3) / 4 * 4;
   const int in = threadIdx.x & 15, s = threadIdx.x >> 4, e = q * 16 + in;
   const int64_t per = (chunks + 31) / 32, c0 = min(s * per, chunks), c1 = min(c0 + per, chunks);
-  float t = 0.f;
+  double t = 0.0;  // up to 2^16 chunks a segment
   int c_e = 0;
   if (e < p.experts)
 #pragma unroll 8
     for (int64_t c = c0; c < c1; ++c) {
-      t += w.share[c * p.experts + e];
+      t += (double)w.share[c * p.experts + e];
       c_e += w.count[c * wide + e];
     }
   seg[s][in] = t;
@@ -477,7 +477,7 @@ __device__ __forceinline__ void route_loss(const RouteParams& p, const RouteWs& 
     int c = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      d += (double)seg[8 * s + i][in];
+      d += seg[8 * s + i][in];
       c += part[8 * s + i][in];
     }
     d += __shfl_xor(d, 16);

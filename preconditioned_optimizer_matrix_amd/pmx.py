@@ -1056,8 +1056,8 @@ def route(Z, top, live=None, balance=0.0, zloss=0.0, normalize=True, order=True,
     q = _route_problem(Z, top, live, balance, zloss, normalize)
     empty, dev = _codes["empty"], Z.device
     rows, experts = q.rows, q.experts
-    if top < 0:
-        raise ValueError("top is negative")
+    if top < 0 or top >> 31:
+        raise ValueError("top is out of range")
     # one buffer of each type, cut up: an allocation costs the host as much as two views
     n, e1 = rows * top, experts + 1
     cuts = (n, e1, e1, n, n) if order else (n, e1, e1)

@@ -126,6 +126,17 @@ def test_large_tiles(env, case):
         assert torch.equal(got, y) and bool((out[:, n:] == 3).all())
 
 
+def test_large_tiles_without_rows(env):
+    """No row, or one, in any group where the rows alone ask for 256 x 256 tiles; the rest of the result is zeros."""
+    torch, pmx = env
+    x, w = torch.randn(9000, 512, device="cuda").bfloat16(), torch.randn(2, 2304, 512, device="cuda").bfloat16()
+    for cuts in ([0, 0, 0], [9000, 9000, 9000], [4000, 4000, 4001]):
+        y = _check(env, x, w, cuts, torch.bfloat16)
+        live = torch.zeros(9000, dtype=torch.bool, device="cuda")
+        live[cuts[0]:cuts[-1]] = True
+        assert bool((y[~live] == 0).all())
+
+
 @pytest.mark.parametrize("out", ["bfloat16", "float32"])
 def test_offsets(env, out):
     """Empty groups, rows in no group, int64, offsets out of range or order."""

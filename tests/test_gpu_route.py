@@ -258,6 +258,8 @@ def test_refusals(env):
     refused(lambda: pmx.route(torch.randn(6, 40, device="cuda"), 17), pmx.PmxError)
     refused(lambda: pmx.route(torch.randn(2, pmx.MAX_GROUPS + 1, device="cuda"), 2), pmx.PmxError)
     refused(lambda: pmx.route(z, 2, balance=float("inf")), pmx.PmxError)
+    refused(lambda: pmx.route(z, -1))
+    refused(lambda: pmx.route(z, (1 << 32) + 2))
     refused(lambda: pmx.route(z.half(), 2))
     refused(lambda: pmx.route(z.t(), 2))
     refused(lambda: pmx.route(z, 2, live=torch.ones(5, dtype=torch.bool, device="cuda")))
