@@ -2,7 +2,7 @@
 // gates, counts, the order of the pairs by expert, and the balance loss with
 // its gradient.  Formulas and edge cases: include/pmx.h.
 //
-// Design: a block takes a chunk of tokens, 64 up to 256 experts.  A team of 4 to 64 lanes
+// Design: a block takes a chunk of tokens (chunk_of).  A team of 4 to 64 lanes
 // holds a token's row in registers, a lane neighbouring experts, so among equal logits
 // the lowest lane with a match and its first match are the lowest index.  A chunk's choice of an expert is one 64-bit mask in LDS: its count is
 // the mask's bits, a pair's rank the bits below its token, whatever order they were
@@ -35,17 +35,20 @@ __device__ __forceinline__ float exp_acc(float x) {
   return y > -200.f ? fmaf(e, r * kLn2, e) : 0.f;  // x = -inf: r is NaN
 }
 
-constexpr int kOne = 64;       // tokens one launch takes
 constexpr int kScatter = 512;  // threads of the second launch: four blocks a unit
-// Few lanes a token, many experts a lane: the instructions of a reduction serve as
-// many tokens as a wave has teams, until too few waves are left to hide their latency
-// (32768 fp32 tokens, 64 experts, forward's first launch and the gradient: 16 lanes of 4
-// 11.5 and 8.3 us, 8 of 8 9.8 and 8.1, 4 of 16 9.6 and 9.2; 262144 bf16 tokens, 128
-// experts, the whole forward and the gradient: 16 lanes of 8 142 and 47 us, 8 of 16 97 and
-// 43; the same tokens of 64 fp32: 8 of 8 72 and 27, 4 of 16 66 and 35).
-int lanes_of(int experts) { return experts <= 32 ? 4 : experts <= 128 ? 8 : experts <= 256 ? 16 : experts <= 512 ? 32 : 64; }
-int chunk_of(int experts) { return lanes_of(experts) <= 16 ? 64 : 1024 / lanes_of(experts); }
-int64_t chunks_of(int64_t rows, int experts) { return (rows + chunk_of(experts) - 1) / chunk_of(experts); }
+// Tokens a block.  Above 256 experts a token a team, in blocks of half the size once
+// there is more than one a unit: 500 experts, 4097 fp32 tokens, the whole forward 25.2 us
+// with 32 a block and 27.1 with 16, 32768 bf16 tokens 81 and 73; 1000 experts, 16 and 8 a
+// block, 4096 tokens 33.6 and 33.5, 32768 180 and 158.
+int chunk_of(int64_t rows, int experts) {
+  if (experts <= 256) return 64;
+  if (experts <= 512) return rows <= 8192 ? 32 : 16;
+  return rows <= 16 ? 16 : 8;
+}
+// One launch where one block takes a token a team: 64 tokens of 1000 experts in it 49 us,
+// in two launches 22.
+bool one_launch(int64_t rows, int experts) { return rows <= chunk_of(rows, experts); }
+int64_t chunks_of(int64_t rows, int experts) { return (rows + chunk_of(rows, experts) - 1) / chunk_of(rows, experts); }
 // Every block reads all counts while that is at most 32 MB in all: a launch less
 // (32768 tokens, 64 experts: one launch of 6.9 us for two of 7.2 and 4.1).
 bool counts_in_scatter(int64_t chunks, int experts) { return chunks * chunks * ((experts + 3) / 4 * 4) <= (32 << 20); }
@@ -81,12 +84,12 @@ __host__ __device__ __forceinline__ RouteWs route_ws(void* base, int64_t chunks,
   return w;
 }
 
-// T lanes a token, V experts a lane.
-template <typename E_, int T_, int V_>
+// T lanes a token, V experts a lane, TEAMS tokens a block (the gradient: 256 threads).
+template <typename E_, int T_, int V_, int TEAMS_>
 struct RCfg {
   typedef E_ E;
   static constexpr int T = T_, V = V_, MAXE = T_ * V_ < kMaxE ? T_ * V_ : kMaxE;
-  static constexpr int THREADS = T_ <= 16 ? 64 * T_ : 1024, WAVES = THREADS / 64, TEAMS = THREADS / T_;
+  static constexpr int TEAMS = TEAMS_, THREADS = T_ * TEAMS_, WAVES = THREADS / 64;
 };
 
 template <int T>
@@ -358,7 +361,7 @@ __device__ __forceinline__ double wave_sum_double(double v) {
   return v;
 }
 
-// Everything, for up to kOne tokens (or none).
+// Everything, for one chunk of tokens (or none).
 template <class C>
 __global__ __launch_bounds__(C::THREADS) void route_one_kernel(RouteParams p) {
   __shared__ Masks M;
@@ -461,7 +464,7 @@ __device__ __forceinline__ void route_loss(const RouteParams& p, const RouteWs& 
   const int parts = (p.experts + 15) / 16, wide = (p.experts + 3) / 4 * 4;
   const int in = threadIdx.x & 15, s = threadIdx.x >> 4, e = q * 16 + in;
   const int64_t per = (chunks + 31) / 32, c0 = min(s * per, chunks), c1 = min(c0 + per, chunks);
-  double t = 0.0;  // up to 2^16 chunks a segment
+  double t = 0.0;  // up to 2^17 chunks a segment
   int c_e = 0;
   if (e < p.experts)
 #pragma unroll 8
@@ -692,45 +695,52 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
   }
 }
 
+// Few lanes a token, many experts a lane: the instructions of a reduction serve as
+// many tokens as a wave has teams, until too few waves are left to hide their latency
+// (32768 fp32 tokens, 64 experts, forward's first launch and the gradient: 16 lanes of 4
+// 11.5 and 8.3 us, 8 of 8 9.8 and 8.1, 4 of 16 9.6 and 9.2; 262144 bf16 tokens, 128
+// experts, the whole forward and the gradient: 16 lanes of 8 142 and 47 us, 8 of 16 97 and
+// 43; the same tokens of 64 fp32: 8 of 8 72 and 27, 4 of 16 66 and 35).
 template <typename E, typename F>
-hipError_t with_cfg(int experts, F&& f) {
-  if (experts <= 16) return f(RCfg<E, 4, 4>());
-  if (experts <= 32) return f(RCfg<E, 4, 8>());
-  if (experts <= 64) return f(RCfg<E, 8, 8>());
-  if (experts <= 128) return f(RCfg<E, 8, 16>());
-  if (experts <= 256) return f(RCfg<E, 16, 16>());
-  if (experts <= 512) return f(RCfg<E, 32, 16>());
-  return f(RCfg<E, 64, 16>());
+hipError_t with_cfg(int chunk, int experts, F&& f) {
+  if (experts <= 16) return f(RCfg<E, 4, 4, 64>());
+  if (experts <= 32) return f(RCfg<E, 4, 8, 64>());
+  if (experts <= 64) return f(RCfg<E, 8, 8, 64>());
+  if (experts <= 128) return f(RCfg<E, 8, 16, 64>());
+  if (experts <= 256) return f(RCfg<E, 16, 16, 64>());
+  if (experts <= 512) return chunk == 32 ? f(RCfg<E, 32, 16, 32>()) : f(RCfg<E, 32, 16, 16>());
+  return chunk == 16 ? f(RCfg<E, 64, 16, 16>()) : f(RCfg<E, 64, 16, 8>());
 }
 template <typename F>
 hipError_t with_cfg(const RouteParams& p, F&& f) {
-  return p.dtype == PMX_BF16 ? with_cfg<uint16_t>(p.experts, f) : with_cfg<float>(p.experts, f);
+  const int chunk = chunk_of(p.rows, p.experts);
+  return p.dtype == PMX_BF16 ? with_cfg<uint16_t>(chunk, p.experts, f) : with_cfg<float>(chunk, p.experts, f);
 }
 
 }  // namespace
 
 size_t route_workspace(int64_t rows, int experts) {
-  if (rows <= kOne) return 0;
+  if (one_launch(rows, experts)) return 0;
   const int64_t c = chunks_of(rows, experts);
   return route_ws(nullptr, c, experts, !counts_in_scatter(c, experts)).bytes;
 }
 
 hipError_t launch_route(const RouteParams& p, hipStream_t s) {
   const int64_t chunks = chunks_of(p.rows, p.experts);
-  const bool between = !counts_in_scatter(chunks, p.experts);
+  const bool between = !counts_in_scatter(chunks, p.experts), one = one_launch(p.rows, p.experts);
   hipError_t e = with_cfg(p, [&](auto c) {
     typedef decltype(c) C;
-    if (p.rows <= kOne) route_one_kernel<C><<<1, C::THREADS, 0, s>>>(p);
+    if (one) route_one_kernel<C><<<1, C::THREADS, 0, s>>>(p);
     else route_rows_kernel<C><<<dim3((unsigned)chunks), C::THREADS, 0, s>>>(p, chunks, between);
     return hipGetLastError();
   });
-  if (e != hipSuccess || p.rows <= kOne) return e;
+  if (e != hipSuccess || one) return e;
   if (between) {
     route_scan_kernel<<<dim3((p.experts + 15) / 16), 1024, 0, s>>>(p, chunks);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  route_scatter_kernel<<<dim3((unsigned)(chunks + (p.experts + 15) / 16)), kScatter, 0, s>>>(p, chunk_of(p.experts), chunks, between);
+  route_scatter_kernel<<<dim3((unsigned)(chunks + (p.experts + 15) / 16)), kScatter, 0, s>>>(p, chunk_of(p.rows, p.experts), chunks, between);
   return hipGetLastError();
 }
 

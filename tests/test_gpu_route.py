@@ -108,7 +108,8 @@ def _check(env, z, top, live=None, balance=1e-2, zloss=1e-3, normalize=True, see
 
 CASES = [(1, 1, 1), (1, 2, 1), (5, 3, 3), (16, 32, 2), (64, 64, 4), (65, 64, 8), (63, 16, 16), (100, 17, 2), (129, 65, 5),
          (300, 128, 8), (257, 129, 3), (90, 256, 16), (80, 257, 7), (70, 512, 6), (200, 513, 4), (33, 1000, 16), (66, 1000, 1),
-         (16383, 8, 2), (16384, 8, 2), (20011, 33, 3)]
+         (16383, 8, 2), (16384, 8, 2), (20011, 33, 3), (8192, 257, 3), (8195, 300, 5),
+         (3001, 1000, 4), (16, 700, 8), (17, 700, 8), (32, 300, 4), (64, 400, 6)]
 
 
 @pytest.mark.parametrize("rows,experts,top", CASES)
