@@ -15,6 +15,10 @@
 //
 // Bound: HBM; each value is read and written once.  16 lanes share a block, 8
 // values a lane: 16 bytes of bf16 in, 8 bytes out, the maximum over a DPP row.
+//
+// Measured: gated silu, 32768 x 4096 bf16, 1.07 GB 199 to 209 us (5.2 TB/s), backward with
+// the activation 1.34 GB 241 us (5.6 TB/s); stored and read back, 8192 x 4096 bf16, 101 MB
+// 17 to 18 and 16.5 us; weights, 32 of 4096 x 1024 bf16, 403 MB 90 us, transposed 93.
 #include <algorithm>
 
 #include "pmx_layer.h"

@@ -24,7 +24,8 @@
 // Measured, bf16: 32768 rows, 32 experts of 4096 x 1024 134 us (2.05 PFLOP/s), 143 to 154
 // with a router's uneven groups; it also writes 268 MB, 53 us at a copy's rate.  8192 x
 // 8192 x 8192 390 to 440 us, 2.5 to 2.8 PFLOP/s, by what clock the card holds: the
-// instructions alone reach 4.5 at full clock, and are busy 65 to 69% of the cycles.  16
+// instructions alone reach 4.5 at full clock, and are busy 65 to 69% of the cycles (the
+// uneven groups: 55%).  16
 // rows through 16 experts 14.4 us for 67 MB of weights.  fp32: 375 us, 0.73 PFLOP/s.
 #include <algorithm>
 
