@@ -21,8 +21,8 @@
 //  * Rows past a group's end read the group's last row (256 x 256: zeros); their
 //    results are not stored.
 //
-// Measured, bf16: 32768 rows, 32 experts of 4096 x 1024 134 us (2.05 PFLOP/s), 143 to 154
-// with a router's uneven groups; it also writes 268 MB, 53 us at a copy's rate.  8192 x
+// Measured, bf16: 32768 rows, 32 experts of 4096 x 1024 134 to 153 us (1.8 to 2.05
+// PFLOP/s), 141 to 160 with a router's uneven groups; it also writes 268 MB, 53 us at a copy's rate.  8192 x
 // 8192 x 8192 390 to 440 us, 2.5 to 2.8 PFLOP/s, by what clock the card holds: the
 // instructions alone reach 4.5 at full clock, and are busy 65 to 69% of the cycles (the
 // uneven groups: 55%).  16
@@ -635,7 +635,8 @@ __device__ __forceinline__ void large_turns(f32x16 (&acc)[4][2], const Large& L,
 // A wave's 128 x 64 results, 32 rows at a time through its 4 KB of LDS (16-byte pieces
 // swizzled as the operands'): 16 stores of whole 128-byte lines where C is aligned and
 // the tile's columns are whole.  They pass the caches by: a launch has 32 MB of them at
-// least, the L2s' size.
+// least, the L2s' size.  (From registers, 32 bytes of a row at a time: 151 -> 186 us, past
+// the caches 238.)
 __device__ __forceinline__ void large_store(f32x16 (&acc)[4][2], const Large& L, const LItem& it, const uint8_t* stage) {
   const Args p = args();
   const int lane = here(threadIdx.x & 63), r = lane & 31, ldc = (int)p->ldc;

@@ -2,11 +2,12 @@
 // gates, counts, the order of the pairs by expert, and the balance loss with
 // its gradient.  Formulas and edge cases: include/pmx.h.
 //
-// Design: a block takes a chunk of tokens (chunk_of).  A team of 4 to 64 lanes
-// holds a token's row in registers, a lane neighbouring experts, so among equal logits
-// the lowest lane with a match and its first match are the lowest index.  A chunk's choice of an expert is one 64-bit mask in LDS: its count is
-// the mask's bits, a pair's rank the bits below its token, whatever order they were
-// set in.  So the pairs are sorted by (expert, token) without a sort:
+// Design: a block takes a chunk of tokens (chunk_of).  A team of 4 to 64 lanes holds a
+// token's row in registers, a lane neighbouring experts, so among equal logits the
+// lowest lane with a match and its first match are the lowest index.  A chunk's choice
+// of an expert is one 64-bit mask in LDS: its count is the mask's bits, a pair's rank the
+// bits below its token, whatever order they were set in.  So the pairs are sorted by
+// (expert, token) without a sort:
 //   1. rows:    ids, gates, masks -> counts a chunk; sums of p and lse^2 a chunk
 //   2. scatter: each block adds up the counts of the chunks before its own and of all
 //               (a byte each), so offsets and each pair's row; the first blocks sum p
@@ -27,12 +28,14 @@ namespace {
 constexpr int kMaxE = PMX_MAX_GROUPS, kMaxTop = PMX_MAX_ROUTE_TOP;
 constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147180559945309f;
 
-// exp(x) for x <= 0: the product's rounding error goes back in as a factor.
+// exp(x) for x <= 0, 0 for -inf and NaN: the product's rounding error goes back in as a
+// factor.
 __device__ __forceinline__ float exp_acc(float x) {
+  x = fmaxf(x, -200.f);
   const float y = x * kLog2e;
-  const float r = fmaf(x, kLog2e, -y) + x * kLog2eLow;
+  const float r = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -y));
   const float e = __builtin_amdgcn_exp2f(y);
-  return y > -200.f ? fmaf(e, r * kLn2, e) : 0.f;  // x = -inf: r is NaN
+  return fmaf(e, r * kLn2, e);
 }
 
 constexpr int kScatter = 512;  // threads of the second launch: four blocks a unit
@@ -178,10 +181,10 @@ __device__ __forceinline__ void store_logits(void* dz, int64_t ld, int64_t row, 
 }
 
 struct RowStat {
-  float high, sum;
+  float high, sum, inv;  // inv: e inv are the probabilities, 0 in dead and NaN in bad rows
   bool dead, bad;  // nothing to choose from; NaN or +inf
 };
-// Turns z into exp(z - max).
+// e: exp(z - max), always finite (0 for NaN and where the largest is infinite).
 template <class C>
 __device__ __forceinline__ RowStat softmax_row(float (&e)[C::V], const float (&z)[C::V], bool live) {
   RowStat s;
@@ -192,19 +195,16 @@ __device__ __forceinline__ RowStat softmax_row(float (&e)[C::V], const float (&z
   float t = 0.f;
 #pragma unroll
   for (int j = 0; j < C::V; ++j) {
-    const float d = z[j] - s.high;
-    // NaN (also inf - inf, where the row holds +inf) stays
-    e[j] = d == d ? exp_acc(d) : d;
+    e[j] = exp_acc(z[j] - s.high);
+    t += e[j];
   }
-#pragma unroll
-  for (int j = 0; j < C::V; ++j) t += e[j];
   s.sum = team_sum<C::T>(t);
-  // a row of -inf gives NaN as well, but one that holds NaN beside them is bad
   bool nan = false;
 #pragma unroll
-  for (int j = 0; j < C::V; ++j) nan |= z[j] != z[j] || z[j] == __builtin_inff();
+  for (int j = 0; j < C::V; ++j) nan |= !(z[j] < __builtin_inff());
   s.bad = live && team_bits<C::T>(__ballot(nan)) != 0;
   s.dead = !live || (!s.bad && s.high == -__builtin_inff());
+  s.inv = s.dead ? 0.f : s.bad ? __builtin_nanf("") : 1.f / s.sum;
   return s;
 }
 
@@ -233,9 +233,8 @@ __device__ __forceinline__ void route_rows(const RouteParams& p, int64_t first, 
     load_logits<C>(z, p, row, lane);
     const bool live = inside && (!p.live || p.live[row] != 0);
     const RowStat s = softmax_row<C>(e, z, live);
-    const float inv = s.dead ? 0.f : 1.f / s.sum;
 #pragma unroll
-    for (int j = 0; j < C::V; ++j) share[j] += s.dead ? 0.f : e[j] * inv;
+    for (int j = 0; j < C::V; ++j) share[j] += e[j] * s.inv;
     const float lse = s.bad ? __builtin_nanf("") : s.high + logf(s.sum);
     if (!s.dead && lane == 0) {
       zsum += lse * lse;
@@ -660,25 +659,24 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
     }
     if (base + step < p.rows) fetch(base + step);
     const RowStat s = softmax_row<C>(e, z, live);
-    const float inv = 1.f / s.sum;
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < C::V; ++j) {
-      e[j] *= inv;
+      e[j] *= s.inv;
       dot += e[j] * a[j];
     }
     dot = team_sum<C::T>(dot);
     gd = team_sum<C::T>(gd);
     // p's factor: the balance and z parts, and without normalisation the gates' own
     const float lse = s.high + logf(s.sum);
-    const float all = cz * lse - dot - (p.normalize ? 0.f : gd);
+    const float all = s.dead ? 0.f : cz * lse - dot - (p.normalize ? 0.f : gd);
 #pragma unroll
     for (int j = 0; j < C::V; ++j) z[j] = e[j] * (a[j] + all);
     if (p.dgates) {
       // the chosen ones': normalised g (dg - sum g dg), else g dg
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
-        const float mine = my_g[i] * (my_d[i] - (p.normalize ? gd : 0.f));
+        const float mine = s.dead ? 0.f : my_g[i] * (my_d[i] - (p.normalize ? gd : 0.f));
 #pragma unroll
         for (int k = 0; k < (C::T < kMaxTop ? C::T : kMaxTop); ++k) {
           if (k + i * C::T >= p.top) continue;
@@ -689,8 +687,6 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < C::V; ++j) z[j] = s.dead ? 0.f : s.bad ? __builtin_nanf("") : z[j];
     if (inside) store_logits<C>(p.dz, p.lddz, row, p.experts, lane, z);
   }
 }
@@ -700,15 +696,21 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteParams p) {
 // (32768 fp32 tokens, 64 experts, forward's first launch and the gradient: 16 lanes of 4
 // 11.5 and 8.3 us, 8 of 8 9.8 and 8.1, 4 of 16 9.6 and 9.2; 262144 bf16 tokens, 128
 // experts, the whole forward and the gradient: 16 lanes of 8 142 and 47 us, 8 of 16 97 and
-// 43; the same tokens of 64 fp32: 8 of 8 72 and 27, 4 of 16 66 and 35).
+// 43; the same tokens of 64 fp32: 8 of 8 72 and 27, 4 of 16 66 and 35).  Twelve a lane where
+// that is enough: the 262144 of 96 bf16 103 and 47, 94 and 36; 32768 of 384 69 and 33, 62
+// and 24; of 640 133 and 53, 123 and 44.
 template <typename E, typename F>
 hipError_t with_cfg(int chunk, int experts, F&& f) {
   if (experts <= 16) return f(RCfg<E, 4, 4, 64>());
   if (experts <= 32) return f(RCfg<E, 4, 8, 64>());
   if (experts <= 64) return f(RCfg<E, 8, 8, 64>());
+  if (experts <= 96) return f(RCfg<E, 8, 12, 64>());
   if (experts <= 128) return f(RCfg<E, 8, 16, 64>());
+  if (experts <= 192) return f(RCfg<E, 16, 12, 64>());
   if (experts <= 256) return f(RCfg<E, 16, 16, 64>());
+  if (experts <= 384) return chunk == 32 ? f(RCfg<E, 32, 12, 32>()) : f(RCfg<E, 32, 12, 16>());
   if (experts <= 512) return chunk == 32 ? f(RCfg<E, 32, 16, 32>()) : f(RCfg<E, 32, 16, 16>());
+  if (experts <= 768) return chunk == 16 ? f(RCfg<E, 64, 12, 16>()) : f(RCfg<E, 64, 12, 8>());
   return chunk == 16 ? f(RCfg<E, 64, 16, 16>()) : f(RCfg<E, 64, 16, 8>());
 }
 template <typename F>

@@ -270,3 +270,22 @@ def test_refusals(env):
     refused(lambda: pmx.route_grad(z, r, upstream=torch.ones(2, device="cuda")))
     refused(lambda: pmx.route_grad(z, r._replace(tally=r.tally[:-1])))
     refused(lambda: pmx.route_grad(z, r, out=torch.empty(6, 9, device="cuda")))
+
+
+def test_rows_left_out_without_normalization(env):
+    """Rows with nothing left, and rows that are not live whatever they hold, have gates 0 and gradient 0."""
+    torch, pmx = env
+    for experts, top, rows in ((10, 4, 60), (200, 4, 150), (700, 2, 40)):
+        z = torch.randn(rows, experts, generator=torch.Generator().manual_seed(5)).cuda()
+        z[3] = -math.inf
+        live = torch.ones(rows, dtype=torch.uint8, device="cuda")
+        live[6] = live[7] = live[8] = 0
+        z[8] = -math.inf
+        _check(env, z, top, live=live, normalize=False)
+        z[6], z[7, 1] = float("nan"), math.inf
+        kw = dict(live=live, balance=1e-2, zloss=1e-3, normalize=False)
+        r = pmx.route(z, top, **kw)
+        dz = pmx.route_grad(z, r, torch.ones(rows, top, device="cuda"), **kw)
+        assert bool(r.loss.isfinite()) and bool(dz.isfinite().all())
+        for t in (3, 6, 7, 8):
+            assert bool((r.ids[t] == -1).all()) and bool((r.gates[t] == 0).all()) and bool((dz[t] == 0).all())
