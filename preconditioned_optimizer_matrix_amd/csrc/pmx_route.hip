@@ -16,8 +16,10 @@
 // does everything in one launch.  Every sum has a fixed order.
 //
 // Bound: launches and latency; the logits are read once forward and once in the
-// gradient.  32768 x 64 fp32 (8 MB each time), top 4: 8.7 and 6.8 us for the two launches,
-// 7.9 for the gradient; 16 tokens of 64: 5 us in one launch.
+// gradient.  32768 x 64 fp32 (8 MB each time), top 4: 8.5 and 6.7 us for the two launches,
+// 7.6 for the gradient; 16 tokens of 32: 4.8 us in one launch.  With many tokens the
+// instructions themselves: 262144 x 128 bf16, top 4, 61 a logit forward and 42 in the
+// gradient keep the units busy for 50 and 43 us.
 #include <algorithm>
 
 #include "pmx_layer.h"
