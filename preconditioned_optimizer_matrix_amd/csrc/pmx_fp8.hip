@@ -660,7 +660,7 @@ __device__ __forceinline__ void large_store(f32x16 (&acc)[4][2], const Large& L,
         "ds_read_b128 %0, %4\n\t"
         "ds_read_b128 %1, %5 offset:1024\n\t"
         "ds_read_b128 %2, %4 offset:2048\n\t"
-        "ds_read_b128 %3, %5 offset:3072\n\t"
+        "ds_read_b128 %3, %5 offset:3*1024\n\t"
         "s_waitcnt lgkmcnt(0)"
         : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
         : "v"(rd0), "v"(rd1)
