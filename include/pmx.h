@@ -735,8 +735,13 @@ pmx_status pmx_silu_checkpoint_grad(pmx_handle handle, const void* dA, pmx_dtype
  * up(k) values at B + e stride_b with ceil(n / 128) x up(k) / 128 scales at
  * B_scales + e stride_bs (pmx_fp8_store_weight).  Values past column k take part:
  * they are zeros as stored.  offsets NULL: one group of all rows (groups = 1).
- * C is PMX_F32 or PMX_BF16; sums are fp32.  Values 16-byte aligned, row distances
- * and stride_b multiples of 16.  Limits as in pmx_grouped_product.
+ * C is PMX_F32 or PMX_BF16, which also chooses the precision of the sums:
+ *   PMX_F32   exact products, added in fp32
+ *   PMX_BF16  of each eight neighbouring products (k = 8 i .. 8 i + 7, before their
+ *             scales) what lies below 2^-13 of the largest may be cut off, towards
+ *             zero; the sums of eight are added in fp32
+ * Values 16-byte aligned, row distances and stride_b multiples of 16.  Limits as in
+ * pmx_grouped_product.
  */
 pmx_status pmx_fp8_product(pmx_handle handle, const uint8_t* A, int64_t rows, int k, int64_t lda,
                            const uint8_t* A_scales, int64_t ldas, const uint8_t* B, int n, int64_t ldb,

@@ -1239,7 +1239,10 @@ def fp8_product(A, A_scales, B, B_scales, offsets=None, out=None, out_dtype=None
     """C[t] = A[t] B[e]^T for the rows offsets[e] <= t < offsets[e + 1] of group
     e, rows in no group zeros: A and its scales from fp8_store (rows x k), B and
     its scales from fp8_store_weight (groups x n x k; transposed for the input
-    gradient).  One group needs no offsets.  C in bf16 (the default) or fp32."""
+    gradient).  One group needs no offsets.  C in bf16 (the default) or fp32,
+    which also chooses the precision of the sums: fp32 adds exact products in
+    fp32, bf16 may lose what lies below 2^-13 of the largest of eight
+    neighbouring products."""
     d = _on(A, A_scales, B, B_scales, offsets, out)
     rows, k, lda, ldas = _fp8_of(A, A_scales)
     if B.dtype != _codes["e4m3"] or B_scales.dtype != _codes["byte"]:
