@@ -602,7 +602,9 @@ pmx_status pmx_distill_grad(pmx_handle handle, const pmx_distill_problem* proble
  *   m = mean x, r = 1 / sqrt(mean (x - m)^2 + eps), Y = (x - m) r weight + bias
  * weight and bias (cols values of param_dtype) may be NULL: ones, zeros.  stats
  * (rows x 2 fp32: m, r) is what the gradient needs, or NULL.  Y has X's type.
- * Statistics are fp32, of the deviations from the mean (no E x^2 - m^2).
+ * Statistics are fp32, of the deviations from the mean (no E x^2 - m^2); fp32 rows'
+ * mean is corrected by that of the deviations, so a mean that is large beside the
+ * spread costs Y no digits, and stats' m is the mean rounded once more.
  * 0 <= eps < infinity; a row of equal values with eps = 0 gives NaN.
  * rows may be 0.
  */

@@ -9,11 +9,11 @@
 namespace pmx {
 
 // ---------------------------------------------------------------------------
-// Reductions over 16 lanes (a DPP row) and over a wave; every lane gets the result.
+// Reductions over 16 lanes (a DPP row) and over a wave; every lane gets the result.  All lanes
+// are active (one that is not would count as 0), so an exchange is one instruction with its sum.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
-  const int i = __float_as_int(v);
-  return __int_as_float(__builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // quad_perm, row_half_mirror, row_mirror
 
@@ -46,7 +46,11 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
 }
 __device__ __forceinline__ float wave_sum(float v) {
   v = row_sum(v);
-  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+  // rows 0 and 1, 2 and 3, then the halves change places
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(h[0]) + __uint_as_float(h[1]);
 }
 __device__ __forceinline__ float wave_max(float v) {
   v = row_max(v);

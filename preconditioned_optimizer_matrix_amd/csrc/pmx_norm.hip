@@ -6,7 +6,13 @@
 //
 // Bound: HBM.  A row stays in registers, packed as it was read, from its load
 // to its result, so the variance is the two-pass one of the mean's deviations
-// and costs no second read.  16 lanes hold short rows, a wave those of up to 1024
+// and costs no second read.  An fp32 row's first sum rounds, and with it the mean, by some
+// 2^-24 of the largest |x|, which is much where the mean is large beside the spread; so
+// the second pass adds up the deviations d too, whose mean D corrects the mean and the
+// variance, mean d^2 - D^2, and is taken off every d (16384 x 1024 23.4 us with it and
+// without, 55924 x 300 26.6 and 25.3, 3355 x 5000 32 and 29).  Of bf16 values, 8 bits each, a
+// sum of 16384 is exact unless they differ by a factor of four, and then the spread is as
+// large.  16 lanes hold short rows, a wave those of up to 1024
 // elements, four to sixteen waves longer ones.  Blocks are persistent: the next
 // row's loads are under way while this one is reduced, weights stay in registers
 // (the longest rows': in LDS), and in the backward pass a thread's columns stay the
@@ -90,13 +96,25 @@ __device__ __forceinline__ void load_row(u32x4_t (&v)[C::NV], const void* p, int
   for (int i = 0; i < C::NV; ++i) v[i] = load_piece(r, (i * C::LANES + lane) * C::V, cols);
 }
 
+// The rows' registers are wanted here, and nothing computed from them is kept past it.  In
+// the backward pass of the longest rows, which have no registers left (it costs time
+// elsewhere: 32768 x 1024 bf16 44 -> 48 us); and between two rows of the fp32 forward pass,
+// where the wait for the next row would else come behind the loads of the one after it
+// (3355 x 5000 36.8 -> 34.4 us).
+template <int N>
+__device__ __forceinline__ void again(u32x4_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
+
 template <class C>
 __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormParams p) {
   typedef typename C::E E;
-  __shared__ float red[2][C::THREADS / 64][1];
+  constexpr int N2 = sizeof(E) == 4 ? 2 : 1;  // sums of the second pass
+  __shared__ float red1[2][C::THREADS / 64][1], red2[2][C::THREADS / 64][N2];
   const int team = threadIdx.x / C::LANES, lane = threadIdx.x % C::LANES;
   const int64_t step = (int64_t)gridDim.x * C::TEAMS;
-  const float cols = (float)p.cols;
+  const float cols = (float)p.cols, inv = 1.f / cols;
   int flip = 0;
   int64_t base = (int64_t)blockIdx.x * C::TEAMS;
   // the block's teams go round together (barriers); a team past the end repeats the last row
@@ -106,27 +124,46 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormParams p) {
   float w[C::NV][C::V], b[C::NV][C::V];
   load_param<C>(w, p.weight, p.param_dtype, p.cols, lane, 1.f);
   load_param<C>(b, p.bias, p.param_dtype, p.cols, lane, 0.f);
+  if constexpr (N2 == 2) again(x);
   for (; base < p.rows; base += step) {
     u32x4_t next[C::NV];
     const bool more = base + step < p.rows;
     if (more) load_row<C>(next, p.x, p.ldx, row_of(base + step), p.cols, lane);
-    float s[1] = {0.f};
+    float t[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < C::NV; ++i)
 #pragma unroll
-      for (int j = 0; j < C::V; ++j) s[0] += element<E>(x[i], j);
-    team_sum<C, 1>(s, red, flip);
-    const float mean = s[0] / cols;  // a row of equal values has their mean
-    s[0] = 0.f;
+      for (int j = 0; j < C::V; ++j) t[0] += element<E>(x[i], j);
+    team_sum<C, 1>(t, red1, flip);
+    const float mean = t[0] / cols;
+    float s[N2] = {}, off = 0.f;
 #pragma unroll
     for (int i = 0; i < C::NV; ++i)
 #pragma unroll
       for (int j = 0; j < C::V; ++j) {
-        const float d = element<E>(x[i], j) - mean;
-        if ((i * C::LANES + lane) * C::V + j < p.cols) s[0] += d * d;
+        float d = element<E>(x[i], j) - mean;
+        d = (i * C::LANES + lane) * C::V + j < p.cols ? d : 0.f;
+        s[0] = fmaf(d, d, s[0]);
+        if constexpr (N2 == 2) {
+          s[1] += d;
+          x[i][j] = __float_as_uint(d);
+        }
       }
-    team_sum<C, 1>(s, red, flip);
-    const float r = 1.f / sqrtf(s[0] / cols + p.eps);
+    team_sum<C, N2>(s, red2, flip);
+    if constexpr (N2 == 2) {
+      // a row of equal values: d is the same few units of the last place everywhere, both sums
+      // are exact, and what is left of d and of the variance is 0
+      // s[1] / cols, rounded once: the quotient's error goes back in (the compiler's division takes
+      // three times the instructions)
+      off = s[1] * inv;
+      off = fmaf(fmaf(-off, cols, s[1]), inv, off);
+    }
+    float var = s[0] / cols;
+    if constexpr (N2 == 2) {
+      var = fmaf(-off, off, var);
+      var = var < 0.f ? 0.f : var;
+    }
+    const float r = 1.f / sqrtf(var + p.eps);
     const int64_t row = base + team;
     if (row < p.rows) {
       E* y = reinterpret_cast<E*>(p.y) + row * p.ldy;
@@ -134,17 +171,19 @@ __global__ __launch_bounds__(C::THREADS) void norm_kernel(NormParams p) {
       for (int i = 0; i < C::NV; ++i) {
         float f[C::V];
 #pragma unroll
-        for (int j = 0; j < C::V; ++j) f[j] = (element<E>(x[i], j) - mean) * r * w[i][j] + b[i][j];
+        for (int j = 0; j < C::V; ++j) f[j] = (element<E>(x[i], j) - (N2 == 2 ? off : mean)) * r * w[i][j] + b[i][j];
         store_piece(y, (i * C::LANES + lane) * C::V, p.cols, f);
       }
       if (lane == 0 && p.stats) {
-        p.stats[2 * row] = mean;
+        p.stats[2 * row] = mean + off;
         p.stats[2 * row + 1] = r;
       }
     }
-    if (more)
+    if (more) {
 #pragma unroll
       for (int i = 0; i < C::NV; ++i) x[i] = next[i];
+      if constexpr (N2 == 2) again(x);
+    }
   }
 }
 
@@ -156,15 +195,6 @@ __device__ __forceinline__ void store_piece4(float* row, int c, int n, const flo
     const float q[4] = {f[k], f[k + 1], f[k + 2], f[k + 3]};
     store_piece(row, c + k, n, q);
   }
-}
-
-// What is computed from the packed row again is not kept in registers meanwhile (for
-// the longest rows, which have none left; it costs time elsewhere: 32768 x 1024 bf16
-// 44 -> 48 us).
-template <int N>
-__device__ __forceinline__ void again(u32x4_t (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
 }
 
 template <class C>
