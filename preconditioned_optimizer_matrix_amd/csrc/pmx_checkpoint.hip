@@ -26,12 +26,17 @@
 namespace pmx {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-
-__device__ __forceinline__ float sigmoid(float x) {
-  const float d = 1.f + __builtin_amdgcn_exp2f(-kLog2e * x);
-  const float r = __builtin_amdgcn_rcpf(d);
-  return d < 0x1p126f ? fmaf(r, fmaf(-d, r, 1.f), r) : r;  // one Newton step: v_rcp is off by up to an ulp
+// s(x), and 1 - s(x) without what the difference would cancel: with t = exp(-|x|) one is
+// 1 / (1 + t), the other t / (1 + t), each a few ulps off wherever x lies.  For bf16 results
+// t may be off by |x| 2^-24, the rounding of the exponent's argument: at most 2^-17, where t
+// is not 0, and theirs is 2^-8 (32768 x 4096 bf16 forward 124 us, 127.5 with exp_acc).
+template <typename E>
+__device__ __forceinline__ float sigmoid(float x, float& one_minus) {
+  const float t = sizeof(E) == 4 ? exp_acc(-fabsf(x)) : __builtin_amdgcn_exp2f(-kLog2e * fabsf(x));
+  const float d = 1.f + t, q = __builtin_amdgcn_rcpf(d);
+  const float r = fmaf(q, fmaf(-d, q, 1.f), q), tr = t * r;  // one Newton step: v_rcp is off by up to an ulp
+  one_minus = x >= 0.f ? tr : r;
+  return x >= 0.f ? r : tr;
 }
 
 // |x| as bits where finite, else 0: whole-number order is that of the magnitudes.
@@ -163,7 +168,8 @@ __global__ __launch_bounds__(256) void silu8_kernel(Store8Params p, Deal d) {
     if (GATED) load8(u, x + p.cols, c, p.cols);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      a[j] = f[j] * sigmoid(f[j]);
+      float rest;
+      a[j] = f[j] * sigmoid<E>(f[j], rest);
       if (GATED) a[j] *= u[j];
     }
     put_block(f, v, s, b, lane16);
@@ -183,13 +189,14 @@ __global__ __launch_bounds__(256) void silu8_grad_kernel(Store8Params p, Deal d)
     if (GATED) get_block(u, v, s, d.blocks + b, lane16);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float sg = sigmoid(x[j]), y = x[j] * sg;
+      float rest;
+      const float sg = sigmoid<E>(x[j], rest), y = x[j] * sg;
       a[j] = GATED ? y * u[j] : y;
       if (GATED) {
         du[j] = g[j] * y;
         g[j] *= u[j];
       }
-      g[j] *= sg * (1.f + x[j] * (1.f - sg));
+      g[j] *= sg * (1.f + x[j] * rest);
     }
     E* dx = reinterpret_cast<E*>(p.dx) + row * p.lddx;
     store8(dx, c, p.cols, g);

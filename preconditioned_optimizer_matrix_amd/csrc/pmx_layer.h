@@ -57,6 +57,17 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
 }
 
+constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147180559945309f;
+// exp(x) for x <= 0, 0 for -inf and NaN: the product's rounding error goes back in as a
+// factor.
+__device__ __forceinline__ float exp_acc(float x) {
+  x = fmaxf(x, -200.f);
+  const float y = x * kLog2e;
+  const float r = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return fmaf(e, r * kLn2, e);
+}
+
 // ---------------------------------------------------------------------------
 // Pieces of 16 bytes of a row of n elements, at any element alignment.
 typedef u32x4_t piece_a2 __attribute__((aligned(2)));

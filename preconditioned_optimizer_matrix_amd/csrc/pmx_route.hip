@@ -28,17 +28,6 @@ namespace pmx {
 namespace {
 
 constexpr int kMaxE = PMX_MAX_GROUPS, kMaxTop = PMX_MAX_ROUTE_TOP;
-constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147180559945309f;
-
-// exp(x) for x <= 0, 0 for -inf and NaN: the product's rounding error goes back in as a
-// factor.
-__device__ __forceinline__ float exp_acc(float x) {
-  x = fmaxf(x, -200.f);
-  const float y = x * kLog2e;
-  const float r = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -y));
-  const float e = __builtin_amdgcn_exp2f(y);
-  return fmaf(e, r * kLn2, e);
-}
 
 constexpr int kScatter = 512;  // threads of the second launch: four blocks a unit
 // Tokens a block.  Above 256 experts a token a team, in blocks of half the size once
