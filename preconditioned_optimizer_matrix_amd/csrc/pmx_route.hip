@@ -339,12 +339,14 @@ __device__ __forceinline__ void scan_offsets(int* off, const int* counts, int n)
   __syncthreads();
 }
 
-// loss = balance E / (top n) sum_e c_e P_e / n + zloss / n sum lse^2, from the sum of c_e n P_e
+// loss = balance E / (top n) sum_e c_e P_e / n + zloss / n sum lse^2, from the sum of c_e n P_e.
+// A bad row makes zsum NaN, and the loss whatever its terms; a zsum that is infinite only
+// counts where it has a weight.
 __device__ __forceinline__ void write_loss(const RouteParams& p, double dot, double zsum, int n) {
   const double nn = n;
-  *p.loss = n == 0 ? 0.f
-                   : (float)((p.balance != 0.f ? (double)p.balance * p.experts / (p.top * nn * nn) * dot : 0.0) +
-                             (p.zloss != 0.f ? (double)p.zloss / nn * zsum : 0.0));
+  const double balance = p.balance != 0.f ? (double)p.balance * p.experts / (p.top * nn * nn) * dot : 0.0;
+  const double z = p.zloss != 0.f ? (double)p.zloss / nn * zsum : 0.0;
+  *p.loss = n == 0 ? 0.f : zsum != zsum ? __builtin_nanf("") : (float)(balance + z);
 }
 __device__ __forceinline__ double wave_sum_double(double v) {
   for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
