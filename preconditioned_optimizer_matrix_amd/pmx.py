@@ -1058,6 +1058,13 @@ def route(Z, top, live=None, balance=0.0, zloss=0.0, normalize=True, order=True,
     rows, experts = q.rows, q.experts
     if top < 0 or top >> 31:
         raise ValueError("top is out of range")
+    ref = ctypes.byref(q)
+    key = ("route", rows, experts, top)
+    need = _sizes.get(key)
+    if need is None:  # refuses sizes beyond the limits before anything of them is allocated
+        sz = _sz()
+        check(lib.pmx_route_workspace_size(ref, ctypes.byref(sz)), "route_workspace_size")
+        need = _keep_size(key, sz.value)
     # one buffer of each type, cut up: an allocation costs the host as much as two views
     n, e1 = rows * top, experts + 1
     cuts = (n, e1, e1, n, n) if order else (n, e1, e1)
@@ -1066,13 +1073,6 @@ def route(Z, top, live=None, balance=0.0, zloss=0.0, normalize=True, order=True,
     slots, tokens = (parts[3].view(rows, top), parts[4]) if order else (None, None)
     gates, loss = empty(n + 1, dtype=_codes["f32"], device=dev).split_with_sizes((n, 1))
     gates, loss = gates.view(rows, top), loss.view(())
-    ref = ctypes.byref(q)
-    key = ("route", rows, experts, top)
-    need = _sizes.get(key)
-    if need is None:
-        sz = _sz()
-        check(lib.pmx_route_workspace_size(ref, ctypes.byref(sz)), "route_workspace_size")
-        need = _keep_size(key, sz.value)
     wp, wn = _ws_for(need, ws, dev)
     h, st = _call(d)
     check(lib.pmx_route(h, ref, ids.data_ptr(), gates.data_ptr(), tally.data_ptr(), offsets.data_ptr(),
