@@ -637,8 +637,9 @@ __device__ __forceinline__ void large_turns(f32x16 (&acc)[4][2], const Large& L,
 
 // A wave's 128 x 64 results, 32 rows at a time through its 4 KB of LDS (16-byte pieces
 // swizzled as the operands'): 16 stores of whole 128-byte lines where C is aligned and
-// the tile's columns are whole.  They pass the caches by: a launch has 32 MB of them at
-// least, the L2s' size.  (From registers, 32 bytes of a row at a time: 151 -> 186 us, past
+// the tile's columns are whole.  They pass the caches by: a launch has more than 16 MB of
+// them (256 tiles, of the last column of tiles one column at least), and 32 MB is the
+// size of all L2s.  (From registers, 32 bytes of a row at a time: 151 -> 186 us, past
 // the caches 238.)
 __device__ __forceinline__ void large_store(f32x16 (&acc)[4][2], const Large& L, const LItem& it, const uint8_t* stage) {
   const Args p = args();
@@ -760,7 +761,8 @@ __global__ __launch_bounds__(512, 2) void fp8_large_kernel(Fp8Params p) {
 // 17.8; or in fp32, whose tiles widen rows that are not there: 200 rows 28.3 and 35.0.
 // 256 x 256 from 256 rows (bf16, four k tiles, one tile a unit), and 128 x 128: 32 of
 // 4096 x 1024, 32768 rows 134 and 243 us, 10000 rows 63 and 72; one of 4096 x 4096, 4096
-// rows 60 and 79.
+// rows 60 and 79.  A last column of tiles that is nearly empty counts like the others: one of
+// 1024, 32768 rows, 257 columns 25 and 28 us, 300 columns 30 and 27.5, 384 22 and 27.
 // 128 x 128 where there is one a unit, and 64 x 64: 6000 rows 48 and 57 us; one of 2003
 // x 1152, 1023 rows, 144 tiles, 14.1 and 10.4 us.  In fp32, whose widening and matrix
 // instructions cost more than the weights' reading, not below 64 rows a group: 1000
