@@ -741,7 +741,8 @@ pmx_status pmx_silu_checkpoint_grad(pmx_handle handle, const void* dA, pmx_dtype
  *   PMX_F32   exact products, added in fp32
  *   PMX_BF16  of each eight neighbouring products (k = 8 i .. 8 i + 7, before their
  *             scales) what lies below 2^-13 of the largest may be cut off, towards
- *             zero; the sums of eight are added in fp32
+ *             zero, where an operand below 2^-6 counts as 2^-6 (a zero as none); the
+ *             sums of eight are added in fp32
  * Values 16-byte aligned, row distances and stride_b multiples of 16.  Limits as in
  * pmx_grouped_product.
  */
