@@ -21,8 +21,8 @@
 // the same bits on every call.  Statistics and sums are fp32.
 //
 // Measured (bytes of the rows alone): 32768 x 1024 bf16 forward 22 us, 6.1 TB/s, backward
-// 39, 5.1 TB/s, of which 4 to 5 the join; 16384 x 1024 fp32 20.5 and 35; 524288 x 64 bf16 39
-// and 53; 8192 x 4096 bf16 25 and 43; 2048 x 16384 bf16 32 and 46.  8 rows: 3.3 us.
+// 38, 5.3 TB/s, of which 4 to 5 the join; 16384 x 1024 fp32 21 and 35; 524288 x 64 bf16 37
+// and 51; 8192 x 4096 bf16 24 and 42; 2048 x 16384 bf16 31 and 47.  8 rows: 3.3 us.
 #include <algorithm>
 
 #include "pmx_layer.h"
